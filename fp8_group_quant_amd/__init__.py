@@ -1,20 +1,24 @@
-"""Python binding of libfp8q.so: per-token-group FP8 quantization and block-scaled FP8
-GEMMs for AMD Instinct MI355X (gfx950).
+"""Python binding of libfp8q.so: per-token-group FP8 quantization, block-scaled FP8 GEMMs,
+and the operators between them in a serving layer (quantizing norm, 4-bit key/value cache,
+attention over it) for AMD Instinct MI355X (gfx950).
 
 This module only marshals torch tensors (device memory, strides, the current HIP
 stream) into the C ABI declared in include/fp8q.h; every step of the computation runs
 in the library's HIP kernels. The functions named fp8q_* mirror the C entry points one
 to one and write into caller-allocated tensors; group_quant() additionally allocates
 its outputs (the role of _allocate_outputs in the sglang PR #30924 design, prhub
-report section "实现拆解" item 2).
+report section "实现拆解" item 2), as do rms_norm_group_quant(), kv4_read() and
+kv4_attention(); alloc_kv4_cache() allocates a cache.
 
 There is no fallback: if libfp8q.so is missing or the device is not a gfx950, calls
 raise.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -33,6 +37,7 @@ _SCALE_FMT = {"f32": SCALE_F32, "ue8m0": SCALE_UE8M0, "ue8m0_packed": SCALE_UE8M
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _INT = ctypes.c_int
+_F32 = ctypes.c_float
 
 _SIGNATURES = {
     "fp8q_group_quant": [_P, _INT, _I64, _I64, _I64, _I64, _I64, _P, _I64, _I64, _P, _INT, _I64, _I64,
@@ -54,6 +59,16 @@ _SIGNATURES = {
                                    _P, _I64, _P, _P, _I64, _I64, _I64, _I64, _I64, _I64, _P],
     "fp8q_grouped_gemm_contiguous": [_P, _I64, _P, _INT, _I64, _I64, _P, _I64, _I64, _P, _INT, _I64, _I64, _I64,
                                      _P, _I64, _P, _I64, _I64, _I64, _I64, _P],
+    "fp8q_rms_norm_group_quant": [_P, _INT, _I64, _I64, _I64, _P, _I64, _P, _I64, _P, _F32, _P, _I64, _P, _INT,
+                                  _I64, _I64, _INT, _P],
+    "fp8q_kv4_write": [_P, _I64, _I64, _P, _I64, _I64, _INT, _I64, _I64, _I64, _P, _P, _P, _P, _P, _I64, _I64,
+                       _I64, _I64, _I64, _I64, _I64, _I64, _P],
+    "fp8q_kv4_read": [_P, _I64, _I64, _P, _I64, _I64, _INT, _I64, _I64, _I64, _P, _P, _P, _P, _P, _I64, _I64,
+                      _I64, _I64, _I64, _I64, _I64, _I64, _P],
+    "fp8q_kv4_attention": [_P, _INT, _I64, _I64, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _I64, _I64, _I64,
+                           _P, _I64, _I64, _P, _P, _P, _I64, _I64, _P, _I64, _I64, _I64, _I64, _I64, _I64, _F32,
+                           _INT, _P, _I64, _P],
+    "fp8q_kv4_attention_workspace_size": [_I64, _I64, _I64, _I64, _I64, _I64],
     "fp8q_status_string": [_INT],
     "fp8q_last_error": [],
     "fp8q_device_check": [_INT],
@@ -83,7 +98,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
             continue
         fn.argtypes = args
         fn.restype = (ctypes.c_char_p if name in ("fp8q_status_string", "fp8q_last_error")
-                      else _I64 if name == "fp8q_gemm_workspace_size" else _INT)
+                      else _I64 if name.endswith("_workspace_size") else _INT)
     _lib = lib
     return lib
 
@@ -234,6 +249,23 @@ def _u8(t: torch.Tensor) -> torch.Tensor:
 _WS_SIZES: dict = {}
 
 
+def _allocating_on(stream, device):
+    """Context in which torch allocates on the stream that the kernels run on, so that the caching
+    allocator hands the blocks to no other stream's work before they finish."""
+    if stream is None:
+        return contextlib.nullcontext()
+    st = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.stream(st)
+
+
+def _alloc_workspace(nbytes: int, device, stream) -> torch.Tensor | None:
+    """nbytes of device memory (None for 0) for kernels on `stream`."""
+    if nbytes <= 0:
+        return None
+    with _allocating_on(stream, device):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
 def fp8q_gemm_workspace_size(M: int, N: int, K: int, mode: int = GEMM_BLOCK128) -> int:
     """Bytes of workspace with which fp8q_gemm_blockscaled_ws takes its split-K path for this
     shape on the current device (0: none needed)."""
@@ -262,17 +294,7 @@ def fp8q_gemm_blockscaled(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb
     if a8.stride(1) != 1 or b8.stride(1) != 1 or y.stride(1) != 1:
         raise ValueError("innermost dimensions must be contiguous")
     if workspace is None and mode == GEMM_BLOCK128:
-        nbytes = fp8q_gemm_workspace_size(M, N, K, mode)
-        if nbytes > 0:
-            # allocated on the stream the kernels run on, so that the caching allocator hands
-            # the block to no other stream's work before they finish
-            if stream is None:
-                workspace = torch.empty(nbytes, dtype=torch.uint8, device=a8.device)
-            else:
-                st = stream if isinstance(stream, torch.cuda.Stream) else \
-                    torch.cuda.ExternalStream(int(stream), device=a8.device)
-                with torch.cuda.stream(st):
-                    workspace = torch.empty(nbytes, dtype=torch.uint8, device=a8.device)
+        workspace = _alloc_workspace(fp8q_gemm_workspace_size(M, N, K, mode), a8.device, stream)
     ws_ptr = None if workspace is None else workspace.data_ptr()
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(load_library().fp8q_gemm_blockscaled_ws(
@@ -365,6 +387,187 @@ def fp8q_grouped_gemm_contiguous(a: torch.Tensor, sa: torch.Tensor, b: torch.Ten
         _ptr(a8), a8.stride(0), _ptr(sa), _scale_fmt_of(sa), sa.stride(0), sa.stride(1),
         _ptr(b8), b8.stride(0), b8.stride(1), _ptr(sb), _scale_fmt_of(sb), sb.stride(0), sb.stride(1),
         sb.stride(2), _ptr(y), y.stride(0), _ptr(mi), T, W, N, K, _stream(stream)))
+
+
+# ------------------------------------------------------------------------------ norm
+def fp8q_rms_norm_group_quant(x: torch.Tensor, weight: torch.Tensor, q: torch.Tensor, s: torch.Tensor,
+                              group_size: int = 128, eps: float = 1e-6, residual: torch.Tensor | None = None,
+                              residual_out: torch.Tensor | None = None, stream=None) -> None:
+    """h = x (+ residual); y = h / sqrt(mean(h^2) + eps) * weight; y quantized as by
+    fp8q_group_quant into q (uint8 or float8_e4m3fn) and s (a [M, K/G] view, whose type and strides
+    choose the format and layout). x, residual, residual_out [M, K] and weight [K] have one type;
+    residual_out receives h rounded to it (it may be the residual's or x's own tensor)."""
+    if x.dim() != 2 or x.dtype not in _DTYPES:
+        raise ValueError("x must be a 2-D bf16, fp16 or fp32 tensor")
+    M, K = x.shape
+    rows = [x] + [t for t in (residual, residual_out) if t is not None]
+    for t in rows:
+        if t.dtype != x.dtype or tuple(t.shape) != (M, K):
+            raise ValueError("residual and residual_out must have x's shape and type")
+    if weight.dtype != x.dtype or tuple(weight.shape) != (K,) or (K > 1 and weight.stride(0) != 1):
+        raise ValueError("weight must be a contiguous [K] tensor of x's type")
+    if q.element_size() != 1 or tuple(q.shape) != (M, K):
+        raise ValueError(f"q has shape {tuple(q.shape)} of {q.dtype}, expected e4m3 bytes of {(M, K)}")
+    if K > 1 and any(t.stride(1) != 1 for t in (*rows, q)):
+        raise ValueError("innermost dimensions must be contiguous")
+    fmt = _scale_fmt_of(s)
+    ng = K // group_size // (4 if fmt == SCALE_UE8M0_PACKED else 1) if group_size > 0 else 0
+    if tuple(s.shape) != (M, ng):
+        raise ValueError(f"s has shape {tuple(s.shape)}, expected {(M, ng)}")
+    _check(load_library().fp8q_rms_norm_group_quant(
+        x.data_ptr(), _DTYPES[x.dtype], M, K, x.stride(0),
+        _ptr(residual), 0 if residual is None else residual.stride(0),
+        _ptr(residual_out), 0 if residual_out is None else residual_out.stride(0),
+        weight.data_ptr(), eps, q.data_ptr(), q.stride(0), s.data_ptr(), fmt, s.stride(0), s.stride(1),
+        group_size, _stream(stream)))
+
+
+def rms_norm_group_quant(x: torch.Tensor, weight: torch.Tensor, group_size: int = 128, scale_fmt: str = "ue8m0",
+                         layout: str = "col", eps: float = 1e-6, residual: torch.Tensor | None = None,
+                         stream=None) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor | None]:
+    """Allocating form: (q uint8 [M, K] of e4m3 bytes, scales viewed as [M, K/G], x + residual
+    or None without a residual)."""
+    M, K = x.shape
+    with _allocating_on(stream, x.device):
+        q = torch.empty(M, K, dtype=torch.uint8, device=x.device)
+        s = alloc_scales(None, M, K // group_size, scale_fmt, layout, x.device)
+        h = None if residual is None else torch.empty(M, K, dtype=x.dtype, device=x.device)
+    fp8q_rms_norm_group_quant(x, weight, q, s, group_size, eps, residual, h, stream)
+    return q, s, h
+
+
+# ------------------------------------------------------------------------------ 4-bit cache
+class Kv4Cache(NamedTuple):
+    """A paged cache of 4-bit keys and values: uint8 codes k, v viewed as [pages, page_size,
+    heads, D/2] and uint8 UE8M0 scales k_scales, v_scales viewed as [pages, page_size, heads, D/32]. The
+    strides carry the layout; k and v have the same, and so have their scales."""
+    k: torch.Tensor
+    k_scales: torch.Tensor
+    v: torch.Tensor
+    v_scales: torch.Tensor
+
+
+def alloc_kv4_cache(pages: int, page_size: int, heads: int, head_dim: int, layout: str = "head",
+                    device="cuda") -> Kv4Cache:
+    """A cache of zeros. layout "head": a head's tokens of one page are adjacent (the order that
+    attention reads); "token": a token's heads are."""
+    def rows(width):
+        if layout == "head":
+            return torch.zeros(pages, heads, page_size, width, dtype=torch.uint8, device=device).transpose(1, 2)
+        if layout == "token":
+            return torch.zeros(pages, page_size, heads, width, dtype=torch.uint8, device=device)
+        raise ValueError("layout must be 'head' or 'token'")
+    return Kv4Cache(rows(head_dim // 2), rows(head_dim // 32), rows(head_dim // 2), rows(head_dim // 32))
+
+
+def _kv4_args(cache: Kv4Cache, heads: int, head_dim: int) -> tuple:
+    """The cache's C arguments: pointers, sizes and strides."""
+    k, ks, v, vs = cache
+    if k.dim() != 4 or ks.dim() != 4:
+        raise ValueError("cached tensors must be [pages, page_size, heads, ...]")
+    pages, page = k.shape[:2]
+    if k.shape != v.shape or ks.shape != vs.shape or tuple(k.shape) != (pages, page, heads, head_dim // 2) \
+            or tuple(ks.shape) != (pages, page, heads, head_dim // 32):
+        raise ValueError(f"cached tensors do not fit {heads} heads of {head_dim}: codes {tuple(k.shape)}, "
+                         f"scales {tuple(ks.shape)}")
+    cs, ss = k.stride(), ks.stride()
+    if cs != v.stride() or ss != vs.stride():
+        raise ValueError("keys and values must have the same strides")
+    if cs[3] != 1 or ss[3] != 1:
+        raise ValueError("innermost dimensions must be contiguous")
+    if not (k.dtype == ks.dtype == v.dtype == vs.dtype == torch.uint8):
+        raise ValueError("cached tensors must be uint8")
+    return (k.data_ptr(), ks.data_ptr(), v.data_ptr(), vs.data_ptr(), pages, page,
+            cs[0], cs[1], cs[2], ss[0], ss[1], ss[2])
+
+
+def _kv4_rows(entry: str, k, v, slots, cache, stream) -> None:
+    if k.dim() != 3 or k.shape != v.shape or k.dtype != v.dtype or k.dtype not in _DTYPES:
+        raise ValueError("k and v must be [T, heads, D] tensors of one type (bf16, fp16 or fp32)")
+    T, H, D = k.shape
+    if k.numel() > 0 and (k.stride(2) != 1 or v.stride(2) != 1):
+        raise ValueError("innermost dimensions must be contiguous")
+    if _dev_i32(slots, "slots").numel() != T:
+        raise ValueError("slots needs one entry per token")
+    _check(getattr(load_library(), entry)(
+        k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1), _DTYPES[k.dtype], T, H, D,
+        slots.data_ptr(), *_kv4_args(cache, H, D), _stream(stream)))
+
+
+def fp8q_kv4_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache: Kv4Cache, stream=None) -> None:
+    """Quantizes token t's keys and values (k, v [T, heads, D]) into slot slots[t] of the cache
+    (int32; slot n is token n % page_size of page n // page_size, negative or past the end: skipped)."""
+    _kv4_rows("fp8q_kv4_write", k, v, slots, cache, stream)
+
+
+def fp8q_kv4_read(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache: Kv4Cache, stream=None) -> None:
+    """Reads slot slots[t] of the cache into k[t] and v[t] [T, heads, D] (zeros for a slot outside
+    the cache)."""
+    _kv4_rows("fp8q_kv4_read", k, v, slots, cache, stream)
+
+
+def kv4_read(cache: Kv4Cache, slots: torch.Tensor, dtype: torch.dtype = torch.bfloat16,
+             stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """Allocating form of fp8q_kv4_read: (k, v) as [T, heads, D] of dtype."""
+    shape = (slots.numel(), cache.k.shape[2], 2 * cache.k.shape[3])
+    with _allocating_on(stream, slots.device):
+        k, v = (torch.empty(shape, dtype=dtype, device=slots.device) for _ in range(2))
+    fp8q_kv4_read(k, v, slots, cache, stream)
+    return k, v
+
+
+def fp8q_kv4_attention_workspace_size(seqs: int, tokens: int, heads: int, kv_heads: int, head_dim: int,
+                                      max_kv_tokens: int) -> int:
+    """Bytes of workspace with which fp8q_kv4_attention splits long caches over more of the
+    current device (0: it needs none). max_kv_tokens is the page table's width times page_size."""
+    return int(load_library().fp8q_kv4_attention_workspace_size(seqs, tokens, heads, kv_heads, head_dim, max_kv_tokens))
+
+
+def fp8q_kv4_attention(q: torch.Tensor, cache: Kv4Cache, block_table: torch.Tensor, kv_lens: torch.Tensor,
+                       out: torch.Tensor, sm_scale: float, causal: bool = True,
+                       q_indptr: torch.Tensor | None = None, lse: torch.Tensor | None = None, stream=None,
+                       workspace: torch.Tensor | None = None) -> None:
+    """out[t, h] = softmax(sm_scale * q[t, h] k^T) v over the cached tokens that the query sees.
+    q, out [T, heads, D] (bf16 or fp16); block_table int32 [B, max_pages]; kv_lens int32 [B];
+    q_indptr int32 [B + 1]: sequence b's queries are rows q_indptr[b] .. q_indptr[b + 1] - 1 (None: row
+    b, T == B). causal: the last query of a sequence sees all its cached tokens, the one before it
+    one less, ... lse [T, heads] fp32 receives the logarithm of each row's softmax sum.
+    When the shape can use a workspace and none is given, one is taken from torch's allocator."""
+    if q.dim() != 3 or q.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError("q must be a [T, heads, D] bf16 or fp16 tensor")
+    T, H, D = q.shape
+    if out.dtype != q.dtype or out.shape != q.shape:
+        raise ValueError("out must have q's shape and type")
+    if q.numel() > 0 and (q.stride(2) != 1 or out.stride(2) != 1):
+        raise ValueError("innermost dimensions must be contiguous")
+    B = _dev_i32(kv_lens, "kv_lens").numel()
+    if block_table.dtype != torch.int32 or not block_table.is_cuda or block_table.dim() != 2 \
+            or block_table.shape[0] != B or (block_table.numel() > 0 and block_table.stride(1) != 1):
+        raise ValueError("block_table must be a device int32 [B, max_pages] tensor with contiguous rows")
+    if q_indptr is not None and _dev_i32(q_indptr, "q_indptr").numel() != B + 1:
+        raise ValueError("q_indptr needs B + 1 entries")
+    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (T, H) or (H > 1 and lse.stride(1) != 1)):
+        raise ValueError("lse must be a float32 [T, heads] tensor with contiguous rows")
+    kv_heads, max_pages = cache.k.shape[2], block_table.shape[1]
+    if workspace is None:
+        workspace = _alloc_workspace(fp8q_kv4_attention_workspace_size(B, T, H, kv_heads, D, max_pages * cache.k.shape[1]),
+                                     q.device, stream)
+    _check(load_library().fp8q_kv4_attention(
+        q.data_ptr(), _DTYPES[q.dtype], q.stride(0), q.stride(1), *_kv4_args(cache, kv_heads, D),
+        block_table.data_ptr(), block_table.stride(0), max_pages, kv_lens.data_ptr(), _ptr(q_indptr),
+        out.data_ptr(), out.stride(0), out.stride(1), _ptr(lse), 0 if lse is None else lse.stride(0),
+        B, T, H, kv_heads, D, sm_scale, int(causal), _ptr(workspace),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def kv4_attention(q: torch.Tensor, cache: Kv4Cache, block_table: torch.Tensor, kv_lens: torch.Tensor,
+                  sm_scale: float, causal: bool = True, q_indptr: torch.Tensor | None = None,
+                  stream=None) -> torch.Tensor:
+    """Allocating form of fp8q_kv4_attention (rows of q in no sequence are left unset)."""
+    with _allocating_on(stream, q.device):
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    fp8q_kv4_attention(q, cache, block_table, kv_lens, out, sm_scale, causal, q_indptr, None, stream)
+    return out
 
 
 def fp8q_device_check(device: int = 0) -> int:

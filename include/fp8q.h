@@ -1,6 +1,7 @@
 /*
- * fp8q.h — C ABI of libfp8q.so: per-token-group FP8 quantization of activations
- * and the block-scaled FP8 GEMMs that consume it, for AMD Instinct MI355X (gfx950).
+ * fp8q.h — C ABI of libfp8q.so: per-token-group FP8 quantization of activations, the
+ * block-scaled FP8 GEMMs that consume it, and the operators between them in a serving layer
+ * (quantizing norm, 4-bit key/value cache, attention over it), for AMD Instinct MI355X (gfx950).
  *
  * What the calls compute is defined by these sources:
  *   [PR30924]  prhub report of sglang PR #30924, "[JIT] Trait-driven
@@ -318,6 +319,124 @@ int fp8q_grouped_gemm_contiguous(const uint8_t* a, int64_t lda,
                                  const void* sb, int sb_fmt, int64_t sb_se, int64_t sb_sn, int64_t sb_sk,
                                  uint16_t* y, int64_t ldy, const int32_t* m_indices,
                                  int64_t T, int64_t W, int64_t N, int64_t K, void* stream);
+
+/*
+ * fp8q_rms_norm_group_quant — root-mean-square norm of each row, with the residual's addition
+ * before it and group quantization to e4m3 after it
+ *
+ * x is [M][K] of in_dtype (row m at x + m*x_sm); weight is [K] of in_dtype. In fp32:
+ *   h = x (+ residual, [M][K] of in_dtype, row m at residual + m*r_sm)
+ *   y = (h * r) * weight, r = 1 / sqrt( sum_k h^2 / K + eps )
+ * y, not rounded to a narrower type, is quantized as by fp8q_group_quant (same scale formats,
+ * layouts and group sizes, group_size == K included) into q and s (row m of q at q + m*q_sm;
+ * scale of group g at s + m*s_sm + g*s_sg). h rounded to in_dtype is stored at residual_out
+ * (row m at residual_out + m*ro_sm) if it is given; it may be the residual's or x's own tensor
+ * (same strides). residual and residual_out may be NULL (no addition, not stored);
+ * residual_out needs a residual [EINVAL].
+ *
+ * Requirements as for fp8q_group_quant, plus: K <= 65536 [EUNSUPPORTED]; eps finite, >= 0
+ * [EINVAL]; weight, residual, residual_out and their row strides 16-byte aligned [EALIGN].
+ */
+int fp8q_rms_norm_group_quant(const void* x, int in_dtype, int64_t M, int64_t K, int64_t x_sm,
+                              const void* residual, int64_t r_sm, void* residual_out, int64_t ro_sm,
+                              const void* weight, float eps,
+                              uint8_t* q, int64_t q_sm,
+                              void* s, int scale_fmt, int64_t s_sm, int64_t s_sg,
+                              int group_size, void* stream);
+
+/*
+ * The paged 4-bit key/value cache
+ *
+ * A cache holds `pages` pages of page_size tokens of H heads, keys and values apart. The row of
+ * (page, token in page, head) is D elements: D / 2 bytes of e2m1 codes (sign, 2 exponent and 1
+ * mantissa bits: 0, 0.5, 1, 1.5, 2, 3, 4, 6; element 2i in the low half of byte i) at
+ * kc + page*c_sp + token*c_st + head*c_sh (values: vc, same strides) and D / 32 UE8M0 scale
+ * bytes at ks + page*s_sp + token*s_st + head*s_sh (values: vs). Strides are in bytes; either
+ * tokens or heads may lie next to each other. Slot n of the cache is token n % page_size of page
+ * n / page_size.
+ * The scale of a 32-element block is the group rule of fp8q_group_quant with 6, the largest
+ * e2m1 value, in the place of 448: amax = max(max |x_i|, 1e-10f); 2^(byte-127) is the smallest
+ * power of two >= amax / 6; code_i = e2m1_round_nearest_even( x_i / 2^(byte-127) ).
+ *
+ * Requirements of every call: D in {64, 128, 256}, page_size a power of two, H <= 2^20,
+ * pages * page_size < 2^31 [EUNSUPPORTED]; codes and their strides 16-byte aligned, scales and
+ * their strides aligned to D / 32 bytes [EALIGN]; strides non-negative [EINVAL].
+ */
+
+/*
+ * fp8q_kv4_write — quantizes T rows of keys and values into slots of the cache
+ *
+ * k and v are [T][H][D] of in_dtype (BF16, F16, F32): row (t, head) of k is at
+ * k + t*k_st + head*k_sh, of v likewise (the two may be views of one tensor). slots is a DEVICE
+ * int32[T]: token t goes to slot slots[t]; a slot outside [0, pages * page_size), such as -1 for
+ * a padding token, is skipped. Two tokens with the same slot leave one or the other's values,
+ * block by block.
+ * k, v and their strides 16-byte aligned, slots 4-byte [EALIGN]; cached rows must not overlap
+ * [EINVAL]; T < 2^31 [EUNSUPPORTED].
+ */
+int fp8q_kv4_write(const void* k, int64_t k_st, int64_t k_sh,
+                   const void* v, int64_t v_st, int64_t v_sh,
+                   int in_dtype, int64_t T, int64_t H, int64_t D, const int32_t* slots,
+                   uint8_t* kc, uint8_t* ks, uint8_t* vc, uint8_t* vs, int64_t pages, int64_t page_size,
+                   int64_t c_sp, int64_t c_st, int64_t c_sh, int64_t s_sp, int64_t s_st, int64_t s_sh,
+                   void* stream);
+
+/*
+ * fp8q_kv4_read — reads T slots of the cache back as rows of out_dtype
+ *
+ * The arguments of fp8q_kv4_write with k and v as outputs: row t gets the values that slot
+ * slots[t] holds, rounded to out_dtype (exact in BF16 and F32); a slot outside the cache gives
+ * zeros. Output rows must not overlap [EINVAL].
+ */
+int fp8q_kv4_read(void* k, int64_t k_st, int64_t k_sh,
+                  void* v, int64_t v_st, int64_t v_sh,
+                  int out_dtype, int64_t T, int64_t H, int64_t D, const int32_t* slots,
+                  const uint8_t* kc, const uint8_t* ks, const uint8_t* vc, const uint8_t* vs,
+                  int64_t pages, int64_t page_size,
+                  int64_t c_sp, int64_t c_st, int64_t c_sh, int64_t s_sp, int64_t s_st, int64_t s_sh,
+                  void* stream);
+
+/*
+ * fp8q_kv4_attention — attention of queries over the cached keys and values
+ *
+ * q and out are [T][Hq][D] of dtype (BF16 or F16; row (t, head) at q + t*q_st + head*q_sh, out
+ * likewise with o_*). The cache holds Hkv heads; query head i reads cached head i / (Hq / Hkv).
+ * B sequences: sequence b has the query rows [q_indptr[b], q_indptr[b+1]) (DEVICE int32[B + 1],
+ * ascending, both ends clamped to [0, T]; NULL: row b, and T == B) and kv_lens[b] cached tokens (DEVICE
+ * int32[B], clamped to [0, max_pages * page_size]); if q_indptr does not ascend and its ranges
+ * hold more than T rows, rows may stay unwritten. Cached token j is token j % page_size of
+ * page table[b*table_sb + j / page_size] (DEVICE int32). A page index outside [0, pages) leaves
+ * its tokens out. With causal != 0 the sequence's last query sees all kv_lens[b] tokens, the one
+ * before it one less, and so on; with causal == 0 every query sees all.
+ *   out = sum_j p_j v_j, p = softmax_j( sm_scale * q . k_j ) over the tokens that are seen
+ *   lse = ln sum_j exp( sm_scale * q . k_j )   ([T][Hq] fp32 at lse + t*l_st + head; NULL: not stored)
+ * A row that sees no token gets zeros, and -infinity in lse. Rows of q in no sequence are not
+ * written. Cached bytes past a sequence's length, and table entries past its pages, are never
+ * used. Scores, sums and the output are accumulated in fp32.
+ *
+ * fp8q_kv4_attention_workspace_size returns the bytes of workspace with which the call splits
+ * long caches over more of the device (max_tokens = max_pages * page_size; 0: it needs none, or
+ * the sizes are refused). With a smaller or NULL workspace the call runs unsplit: same results
+ * up to the order of fp32 sums, each deterministic. The library writes only that many bytes;
+ * calls that overlap in time must not share a workspace.
+ *
+ * Requirements: Hq a multiple of Hkv [EINVAL]; B <= 4096, T * Hq < 2^31, Hq <= 2^20,
+ * max_pages * page_size <= 2^30 [EUNSUPPORTED]; q, out, their strides and the workspace 16-byte
+ * aligned, the index arrays and lse 4-byte [EALIGN]; out rows not overlapping, sm_scale finite,
+ * workspace_bytes >= 0 [EINVAL]; and the cache's.
+ */
+int64_t fp8q_kv4_attention_workspace_size(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                                          int64_t max_tokens);
+
+int fp8q_kv4_attention(const void* q, int dtype, int64_t q_st, int64_t q_sh,
+                       const uint8_t* kc, const uint8_t* ks, const uint8_t* vc, const uint8_t* vs,
+                       int64_t pages, int64_t page_size,
+                       int64_t c_sp, int64_t c_st, int64_t c_sh, int64_t s_sp, int64_t s_st, int64_t s_sh,
+                       const int32_t* table, int64_t table_sb, int64_t max_pages, const int32_t* kv_lens,
+                       const int32_t* q_indptr,
+                       void* out, int64_t o_st, int64_t o_sh, float* lse, int64_t l_st,
+                       int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                       float sm_scale, int causal, void* workspace, int64_t workspace_bytes, void* stream);
 
 /* Human-readable name of a status code. Never returns NULL. */
 const char* fp8q_status_string(int status);
