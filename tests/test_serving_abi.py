@@ -109,7 +109,7 @@ ATTN = dict(q=0x10000, dtype=0, q_st=8 * 128, q_sh=128, **CACHE, table=0x20000, 
     (dict(q=None), EINVAL), (dict(out=None), EINVAL), (dict(sm_scale=math.inf), EINVAL), (dict(sm_scale=math.nan), EINVAL),
     (dict(q_st=-8), EINVAL), (dict(table_sb=-1), EINVAL), (dict(table_sb=0), EDEVICE),
     (dict(o_sh=64), EINVAL), (dict(o_st=128), EINVAL), (dict(o_st=128, o_sh=7 * 128), EDEVICE), (dict(l_st=4), EINVAL),
-    (dict(q=0x10008), EALIGN), (dict(q_sh=132), EALIGN), (dict(out=0x50008), EALIGN), (dict(o_sh=129), EALIGN),
+    (dict(q=0x10008), EALIGN), (dict(q_sh=132), EALIGN), (dict(out=0x50008), EALIGN), (dict(o_sh=129, o_st=2048), EALIGN),
     (dict(lse=0x60001), EALIGN), (dict(table=0x20002), EALIGN), (dict(workspace=0x70008), EALIGN),
     (dict(workspace_bytes=-1), EINVAL), (dict(pages=0, kc=None, ks=None, vc=None, vs=None), EDEVICE),
 ])
