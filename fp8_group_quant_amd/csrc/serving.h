@@ -71,10 +71,11 @@ struct Kv4AttnParams {
   int32_t Hq, Hkv, group;    // group = Hq / Hkv
   float scale_log2;          // softmax scale times log2(e)
   int32_t causal;
-  int64_t max_base;          // items without splitting, at most
-  int32_t target;            // split over the cache axis: work items wanted
-  int32_t* plan;             // split only: prefix of the items, then the spans per chunk
-  float* parts;              // split only: partial outputs, maxima and sums by item
+  int64_t max_units;         // query tiles x cached heads, at most
+  int32_t blocks;            // split only, as the next three: blocks that share the line of spans
+  int64_t* plan_line;        // [B + 1] spans before each sequence
+  int32_t* plan_first;       // [B + 1] query tiles before each sequence
+  float* parts;              // partial outputs, maxima and sums by piece
 };
 
 // Bytes of workspace with which attention of this shape splits the cache axis on the current
