@@ -68,7 +68,7 @@ _SIGNATURES = {
     "fp8q_kv4_attention": [_P, _INT, _I64, _I64, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _I64, _I64, _I64,
                            _P, _I64, _I64, _P, _P, _P, _I64, _I64, _P, _I64, _I64, _I64, _I64, _I64, _I64, _F32,
                            _INT, _P, _I64, _P],
-    "fp8q_kv4_attention_workspace_size": [_I64, _I64, _I64, _I64, _I64, _I64],
+    "fp8q_kv4_attention_workspace_size": [_INT, _I64, _I64, _I64, _I64, _I64, _I64],
     "fp8q_status_string": [_INT],
     "fp8q_last_error": [],
     "fp8q_device_check": [_INT],
@@ -516,11 +516,12 @@ def kv4_read(cache: Kv4Cache, slots: torch.Tensor, dtype: torch.dtype = torch.bf
     return k, v
 
 
-def fp8q_kv4_attention_workspace_size(seqs: int, tokens: int, heads: int, kv_heads: int, head_dim: int,
-                                      max_kv_tokens: int) -> int:
+def fp8q_kv4_attention_workspace_size(dtype: torch.dtype, seqs: int, tokens: int, heads: int, kv_heads: int,
+                                      head_dim: int, max_kv_tokens: int) -> int:
     """Bytes of workspace with which fp8q_kv4_attention splits long caches over more of the
     current device (0: it needs none). max_kv_tokens is the page table's width times page_size."""
-    return int(load_library().fp8q_kv4_attention_workspace_size(seqs, tokens, heads, kv_heads, head_dim, max_kv_tokens))
+    return int(load_library().fp8q_kv4_attention_workspace_size(_DTYPES[dtype], seqs, tokens, heads, kv_heads,
+                                                                head_dim, max_kv_tokens))
 
 
 def fp8q_kv4_attention(q: torch.Tensor, cache: Kv4Cache, block_table: torch.Tensor, kv_lens: torch.Tensor,
@@ -550,8 +551,8 @@ def fp8q_kv4_attention(q: torch.Tensor, cache: Kv4Cache, block_table: torch.Tens
         raise ValueError("lse must be a float32 [T, heads] tensor with contiguous rows")
     kv_heads, max_pages = cache.k.shape[2], block_table.shape[1]
     if workspace is None:
-        workspace = _alloc_workspace(fp8q_kv4_attention_workspace_size(B, T, H, kv_heads, D, max_pages * cache.k.shape[1]),
-                                     q.device, stream)
+        workspace = _alloc_workspace(fp8q_kv4_attention_workspace_size(
+            q.dtype, B, T, H, kv_heads, D, max_pages * cache.k.shape[1]), q.device, stream)
     _check(load_library().fp8q_kv4_attention(
         q.data_ptr(), _DTYPES[q.dtype], q.stride(0), q.stride(1), *_kv4_args(cache, kv_heads, D),
         block_table.data_ptr(), block_table.stride(0), max_pages, kv_lens.data_ptr(), _ptr(q_indptr),

@@ -256,7 +256,9 @@ int attention_entry(const void* q, int dtype, int64_t q_st, int64_t q_sh, const 
   p.Hq = static_cast<int32_t>(Hq);
   p.Hkv = static_cast<int32_t>(Hkv);
   p.group = static_cast<int32_t>(Hq / Hkv);
-  p.scale_log2 = sm_scale * 1.4426950408889634f;
+  // a scale of zero stays above the smallest numbers, so that a masked score times it is -infinity
+  p.scale_log2 = std::max(std::fabs(sm_scale) * 1.4426950408889634f, 1e-30f);
+  p.q_sign = sm_scale < 0.0f ? 0x80008000u : 0u;
   p.causal = causal != 0;
   return launch_kv4_attention(dtype, D, p, workspace, workspace_bytes, static_cast<hipStream_t>(stream));
 }
@@ -290,11 +292,13 @@ int fp8q_kv4_read(void* k, int64_t k_st, int64_t k_sh, void* v, int64_t v_st, in
                           page_size, c_sp, c_st, c_sh, s_sp, s_st, s_sh, stream);
 }
 
-int64_t fp8q_kv4_attention_workspace_size(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_tokens) {
+int64_t fp8q_kv4_attention_workspace_size(int dtype, int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                                          int64_t max_tokens) {
   if (fp8q::check_attention_sizes("fp8q_kv4_attention_workspace_size: ", B, T, Hq, Hkv, D, max_tokens) != FP8Q_OK ||
-      B == 0 || T == 0 || Hq == 0 || fp8q::check_current_device() != FP8Q_OK)
+      (dtype != FP8Q_DTYPE_BF16 && dtype != FP8Q_DTYPE_F16) || B == 0 || T == 0 || Hq == 0 ||
+      fp8q::check_current_device() != FP8Q_OK)
     return 0;
-  return fp8q::kv4_attention_workspace(B, T, Hq, Hkv, D, max_tokens);
+  return fp8q::kv4_attention_workspace(dtype, B, T, Hq, Hkv, D, max_tokens);
 }
 
 int fp8q_kv4_attention(const void* q, int dtype, int64_t q_st, int64_t q_sh, const uint8_t* kc, const uint8_t* ks,

@@ -48,9 +48,13 @@ constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kRows = 16;   // query rows of an item
 constexpr int kTile = 32;   // tokens of a wave's step
-constexpr int kSpan = kTile * kWaves;  // tokens of a block's step: chunks are whole spans
+constexpr int kStep = kTile * kWaves;  // tokens of a block's step
 constexpr int kPadV = 16;   // elements between the V rows in LDS
 constexpr int kMinRun = 2;  // spans of a block's run at least
+constexpr float kLn2 = 0.6931471805599453f;
+// Outputs are rescaled only when a row's maximum has grown by more than 2^8 since it last was:
+// probabilities then reach 2^8, which costs fp32 sums and bf16 factors no precision.
+constexpr float kHeadroom = 8.0f;
 constexpr float kNegInf = -__builtin_inff();
 
 __device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }
@@ -73,6 +77,10 @@ __device__ __forceinline__ int32_t clamp32(int32_t v, int64_t hi) {
   return v < 0 ? 0 : v > hi ? static_cast<int32_t>(hi) : v;
 }
 
+// The index arrays are only read: a load at a wave-uniform place is scalar.
+typedef const __attribute__((address_space(4))) int32_t* ConstInts;
+__device__ __forceinline__ int32_t read_int(const int32_t* a, int64_t i) { return ((ConstInts)a)[i]; }
+
 struct Seq {
   int32_t q0, q_len, kv_len;
 };
@@ -82,35 +90,38 @@ __device__ __forceinline__ Seq sequence(const Kv4AttnParams& p, int32_t b) {
   s.q0 = b;
   s.q_len = 1;
   if (p.q_indptr) {
-    s.q0 = clamp32(p.q_indptr[b], p.T);
-    s.q_len = max(clamp32(p.q_indptr[b + 1], p.T) - s.q0, 0);
+    s.q0 = clamp32(read_int(p.q_indptr, b), p.T);
+    s.q_len = max(clamp32(read_int(p.q_indptr, b + 1), p.T) - s.q0, 0);
   }
-  s.kv_len = clamp32(p.kv_lens[b], p.max_tokens);
+  s.kv_len = clamp32(read_int(p.kv_lens, b), p.max_tokens);
   return s;
 }
 
+template <int ROWS>
 __device__ __forceinline__ int32_t tiles_of(const Kv4AttnParams& p, const Seq& s) {
-  return static_cast<int32_t>((static_cast<int64_t>(s.q_len) * p.group + kRows - 1) / kRows);
+  return static_cast<int32_t>((static_cast<uint32_t>(s.q_len) * p.group + ROWS - 1) / ROWS);  // T * Hq < 2^31
 }
 // A sequence without cached tokens has one empty span, so that its rows are written.
-__device__ __forceinline__ int32_t spans_of(const Seq& s) { return max((s.kv_len + kSpan - 1) / kSpan, 1); }
+__device__ __forceinline__ int32_t spans_of(const Kv4AttnParams& p, const Seq& s) {
+  return max((s.kv_len + (1 << p.span_shift) - 1) >> p.span_shift, 1);
+}
 
 // ------------------------------------------------------------------ units and runs
 // Prefixes over the sequences: first[b] the query tiles, line[b] the (tile, span) pairs before
 // sequence b. Unit (b, tile, head) is number (first[b] + tile) * Hkv + head and has the places
-// [line[b] * Hkv + (tile * Hkv + head) * spans, + spans) of the line of all spans.
+// [line[b] * Hkv + (tile * Hkv + head) * spans, + spans) of the line of all spans. The host
+// chooses the span so that the line has fewer than 2^31 places.
 struct Plan {
-  int64_t* line;   // [B + 1]
+  int32_t* line;   // [B + 1]
   int32_t* first;  // [B + 1]
 };
 
 // Inclusive sum over the block's threads; `lds` holds one value per wave.
-template <typename T>
-__device__ __forceinline__ T block_scan(T v, T* lds, T& total) {
+__device__ __forceinline__ long long block_scan(long long v, long long* lds, long long& total) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) {
-    const T up = __shfl_up(v, off, 64);
+    const long long up = __shfl_up(v, off, 64);
     if (lane >= off) v += up;
   }
   if (lane == 63) lds[wave] = v;
@@ -126,6 +137,7 @@ __device__ __forceinline__ T block_scan(T v, T* lds, T& total) {
 
 // Fills the plan in LDS; every block computes the same from the lengths. A q_indptr that does
 // not ascend can name more rows than there are: then the plan is empty and nothing is run.
+template <int ROWS>
 __device__ __forceinline__ void make_plan(const Kv4AttnParams& p, const Plan& plan) {
   __shared__ long long tot_line[kWaves], tot_first[kWaves];
   const int tid = threadIdx.x;
@@ -135,9 +147,9 @@ __device__ __forceinline__ void make_plan(const Kv4AttnParams& p, const Plan& pl
   long long my_line = 0, my_first = 0;
   for (int32_t b = beg; b < end; b++) {
     const Seq s = sequence(p, b);
-    const long long tiles = tiles_of(p, s);
+    const long long tiles = tiles_of<ROWS>(p, s);
     my_first += tiles;
-    my_line += tiles * spans_of(s);
+    my_line += tiles * spans_of(p, s);
   }
   long long all_line, all_first;
   long long at_first = block_scan(my_first, tot_first, all_first) - my_first;
@@ -146,21 +158,20 @@ __device__ __forceinline__ void make_plan(const Kv4AttnParams& p, const Plan& pl
   for (int32_t b = beg; b < end; b++) {
     const Seq s = sequence(p, b);
     plan.first[b] = fits ? static_cast<int32_t>(at_first) : 0;
-    plan.line[b] = fits ? at_line : 0;
-    const long long tiles = tiles_of(p, s);
+    plan.line[b] = fits ? static_cast<int32_t>(at_line) : 0;
+    const long long tiles = tiles_of<ROWS>(p, s);
     at_first += tiles;
-    at_line += tiles * spans_of(s);
+    at_line += tiles * spans_of(p, s);
   }
   if (tid == kThreads - 1) {
     plan.first[B] = fits ? static_cast<int32_t>(all_first) : 0;
-    plan.line[B] = fits ? all_line : 0;
+    plan.line[B] = fits ? static_cast<int32_t>(all_line) : 0;
   }
   __syncthreads();
 }
 
 // The last b with pref[b] <= v (pref ascending, pref[0] <= v).
-template <typename T>
-__device__ __forceinline__ int32_t find_seq(const T* pref, int32_t B, T v) {
+__device__ __forceinline__ int32_t find_seq(const int32_t* pref, int32_t B, int32_t v) {
   int32_t lo = 0, hi = B;
   while (hi - lo > 1) {
     const int32_t mid = (lo + hi) >> 1;
@@ -170,9 +181,97 @@ __device__ __forceinline__ int32_t find_seq(const T* pref, int32_t B, T v) {
 }
 
 // Spans of one block's run when `blocks` blocks share a line of `total` spans.
-__device__ __forceinline__ int64_t run_length(int64_t total, int32_t blocks) {
-  return max((total + blocks - 1) / blocks, static_cast<int64_t>(kMinRun));
+__device__ __forceinline__ int32_t run_length(int32_t total, int32_t blocks) {
+  return max(total / blocks + (total % blocks != 0), kMinRun);
 }
+
+__device__ __forceinline__ int32_t uniform(int32_t v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// One unit's tokens [t0, t1) of a block's run.
+struct Work {
+  Seq seq;
+  int32_t b, tile, head, t0, t1;
+  bool whole;     // all of the unit's tokens
+  int32_t piece;  // else: where its partial results go
+};
+
+// A block's places [at, stop) on the line: of spans when splitting, else of units in steps of the
+// grid. `direct`: one unit per sequence and cached head, in order, so that no plan is needed.
+template <int ROWS, bool SPLIT>
+struct Walk {
+  const Kv4AttnParams& p;
+  const Plan plan;
+  const bool direct;
+  int32_t at, stop;
+
+  __device__ __forceinline__ Walk(const Kv4AttnParams& params, int32_t* lds)
+      : p(params), plan{lds, lds + params.B + 1},
+        direct(!SPLIT && params.q_indptr == nullptr && params.group <= ROWS) {
+    const int32_t B = static_cast<int32_t>(p.B);
+    if (!direct) make_plan<ROWS>(p, plan);
+    if constexpr (SPLIT) {
+      const int32_t total = uniform(plan.line[B]) * p.Hkv, run = run_length(total, p.blocks);
+      at = static_cast<int32_t>(min(static_cast<int64_t>(blockIdx.x) * run, static_cast<int64_t>(total)));
+      stop = at + min(run, total - at);
+      if (blockIdx.x == 0) {  // for the join
+        for (int32_t b = threadIdx.x; b <= B; b += kThreads) {
+          p.plan[b] = plan.line[b];
+          p.plan[B + 1 + b] = plan.first[b];
+        }
+      }
+    } else {
+      at = blockIdx.x;
+      stop = (direct ? B : uniform(plan.first[B])) * p.Hkv;
+    }
+  }
+
+  __device__ __forceinline__ bool next(Work& w) {
+    if (at >= stop) return false;
+    const int32_t B = static_cast<int32_t>(p.B);
+    int32_t s0 = 0, s1;
+    if constexpr (SPLIT) {
+      w.b = uniform(find_seq(plan.line, B, at / p.Hkv));
+      w.seq = sequence(p, w.b);
+      const int32_t spans = spans_of(p, w.seq), in = at - uniform(plan.line[w.b]) * p.Hkv, unit = in / spans;
+      w.tile = unit / p.Hkv;
+      w.head = unit - w.tile * p.Hkv;
+      s0 = in - unit * spans;
+      s1 = min(spans, s0 + (stop - at));
+      at += s1 - s0;
+      w.whole = s0 == 0 && s1 == spans;
+      w.piece = blockIdx.x + uniform(plan.first[w.b]) * p.Hkv + unit;
+    } else {
+      const int32_t u = at / p.Hkv;
+      w.head = at - u * p.Hkv;
+      w.b = direct ? u : uniform(find_seq(plan.first, B, u));
+      w.seq = sequence(p, w.b);
+      w.tile = direct ? 0 : u - uniform(plan.first[w.b]);
+      s1 = spans_of(p, w.seq);
+      w.whole = true;
+      w.piece = 0;
+      at += min(static_cast<int32_t>(gridDim.x), stop - at);
+    }
+    w.t0 = s0 << p.span_shift;
+    w.t1 = s1 == spans_of(p, w.seq) ? w.seq.kv_len : s1 << p.span_shift;
+    return true;
+  }
+};
+
+// The tile's query rows first .. last (at least one), and how much of the cache they see.
+struct Rows {
+  int32_t first, last;  // of the sequence's q_len * group rows; row i is query i / group
+  int32_t before;       // tokens that query 0 sees with `causal`
+
+  __device__ __forceinline__ Rows(const Kv4AttnParams& p, const Work& w, int rows) {
+    first = w.tile * rows;
+    last = min(first + rows, w.seq.q_len * p.group) - 1;
+    before = w.seq.kv_len - w.seq.q_len + 1;
+  }
+  // Tokens that row i sees.
+  __device__ __forceinline__ int32_t seen(const Kv4AttnParams& p, const Seq& s, int32_t i) const {
+    return p.causal ? before + static_cast<int32_t>(static_cast<uint32_t>(i) / static_cast<uint32_t>(p.group)) : s.kv_len;
+  }
+};
 
 // ------------------------------------------------------------------ cached rows
 // A lane's part of one token's row: D / 4 elements.
@@ -183,26 +282,29 @@ struct Codes {
 };
 
 template <int D>
-__device__ __forceinline__ void load_codes(const uint8_t* codes, const uint8_t* scales, int h, Codes<D>& c) {
+__device__ __forceinline__ void load_codes(const uint8_t* codes, uint32_t code_lane, const uint8_t* scales,
+                                           uint32_t scale_lane, int h, Codes<D>& c) {
+  codes += code_lane + D / 8 * h;
+  scales += scale_lane + (D == 64 ? h >> 1 : D / 128 * h);
   if constexpr (D == 64) {
-    const u32x2 a = *reinterpret_cast<const u32x2*>(codes + 8 * h);
+    const u32x2 a = *reinterpret_cast<const u32x2*>(codes);
     c.w[0] = a[0];
     c.w[1] = a[1];
-    c.scale = scales[h >> 1];
+    c.scale = *scales;
   } else if constexpr (D == 128) {
-    const u32x4 a = *reinterpret_cast<const u32x4*>(codes + 16 * h);
+    const u32x4 a = *reinterpret_cast<const u32x4*>(codes);
 #pragma unroll
     for (int i = 0; i < 4; i++) c.w[i] = a[i];
-    c.scale = scales[h];
+    c.scale = *scales;
   } else {
-    const u32x4 a = *reinterpret_cast<const u32x4*>(codes + 32 * h);
-    const u32x4 b = *reinterpret_cast<const u32x4*>(codes + 32 * h + 16);
+    const u32x4 a = *reinterpret_cast<const u32x4*>(codes);
+    const u32x4 b = *reinterpret_cast<const u32x4*>(codes + 16);
 #pragma unroll
     for (int i = 0; i < 4; i++) {
       c.w[i] = a[i];
       c.w[4 + i] = b[i];
     }
-    c.scale = *reinterpret_cast<const uint16_t*>(scales + 2 * h);
+    c.scale = *reinterpret_cast<const uint16_t*>(scales);
   }
 }
 
@@ -239,52 +341,74 @@ struct Pages {
 };
 
 template <bool PAGE16>
-__device__ __forceinline__ Pages load_pages(const Kv4AttnParams& p, const int32_t* table, int32_t t, int32_t t_end) {
-  Pages g;
-#pragma unroll
-  for (int s = 0; s < 2; s++) {
-    // past the end: the last token's page, which is there to be read
-    const int32_t tok = min(t + 16 * s + (PAGE16 ? 0 : static_cast<int>(threadIdx.x & 15)), t_end - 1);
-    g.n[s] = table[tok >> p.c.page_shift];
-  }
-  return g;
+__device__ __forceinline__ int32_t load_page(const Kv4AttnParams& p, const int32_t* table, int32_t t, int32_t t_end) {
+  // past the end: the last token's entry, which is there to be read
+  const int32_t at = min(t + (PAGE16 ? 0 : static_cast<int>(threadIdx.x & 15)), t_end - 1) >> p.c.page_shift;
+  return PAGE16 ? read_int(table, at) : table[at];
 }
 
-// Loads a step's codes and scales. Every address is inside the cache: a page that is not there
-// is replaced by page 0, and tokens past the end lie in the last token's page or in a valid
-// one; what is loaded for them is not used (`there`).
+template <bool PAGE16>
+__device__ __forceinline__ Pages load_pages(const Kv4AttnParams& p, const int32_t* table, int32_t t, int32_t t_end) {
+  return Pages{{load_page<PAGE16>(p, table, t, t_end), load_page<PAGE16>(p, table, t + 16, t_end)}};
+}
+
+// Where the rows of tokens t .. t + 15 lie in a page `n`, and which of them are there (bit i:
+// token t + i is before t_end and its page is in the cache). Every address is inside the cache: a page that
+// is not there is replaced by page 0, and tokens past the end lie in the last token's page or in
+// a valid one; what is loaded for them is not used.
+struct Half {
+  int64_t c, s;             // of the lane's token, without its head; PAGE16: wave-uniform,
+  uint32_t c_lane, s_lane;  // and the lane's part
+  uint32_t there;
+};
+
+template <bool PAGE16>
+__device__ __forceinline__ Half locate(const Kv4AttnParams& p, int32_t n, int32_t t, int32_t t_end) {
+  const int r = threadIdx.x & 15;
+  const int32_t mask = (1 << p.c.page_shift) - 1, left = t_end - t;
+  const bool ok = n >= 0 && n < p.c.pages;
+  const int64_t page = ok ? n : 0;
+  Half a;
+  if constexpr (PAGE16) {  // page strides and page extents fit 32 bits
+    const uint32_t in = t & mask, c_st = static_cast<uint32_t>(p.c.c_st), s_st = static_cast<uint32_t>(p.c.s_st);
+    a.there = !ok || left <= 0 ? 0u : left >= 16 ? 0xFFFFu : (1u << left) - 1u;
+    a.c = static_cast<uint64_t>(static_cast<uint32_t>(page)) * static_cast<uint32_t>(p.c.c_sp) + in * c_st;
+    a.s = static_cast<uint64_t>(static_cast<uint32_t>(page)) * static_cast<uint32_t>(p.c.s_sp) + in * s_st;
+    a.c_lane = r * c_st;
+    a.s_lane = r * s_st;
+  } else {
+    const int64_t in = min(t + r, t_end - 1) & mask;
+    a.there = static_cast<uint32_t>(__builtin_amdgcn_ballot_w64(ok && r < left) & 0xFFFFu);
+    a.c = page * p.c.c_sp + in * p.c.c_st;
+    a.s = page * p.c.s_sp + in * p.c.s_st;
+    a.c_lane = a.s_lane = 0;
+  }
+  return a;
+}
+
+// Loads a step's codes and scales; k and v (with their scales) start at the unit's head.
 template <int D, bool PAGE16>
-__device__ __forceinline__ void load_step(const Kv4AttnParams& p, const Pages& g, int64_t head_c, int64_t head_s,
-                                          int32_t t, int32_t t_end, Step<D>& st) {
-  const int lane = threadIdx.x & 63, r = lane & 15, h = lane >> 4;
-  const int32_t mask = (1 << p.c.page_shift) - 1;
-  uint32_t there = 0;
+__device__ __forceinline__ void load_step(const Kv4AttnParams& p, const Kv4Cache& at, const Pages& g, int32_t t,
+                                          int32_t t_end, Step<D>& st) {
+  const int h = (threadIdx.x & 63) >> 4;
+  st.there = 0;
 #pragma unroll
   for (int s = 0; s < 2; s++) {
-    const int32_t left = t_end - (t + 16 * s);  // tokens of this half inside the range
-    int64_t c = head_c, b = head_s;
-    if constexpr (PAGE16) {
-      const bool ok = g.n[s] >= 0 && g.n[s] < p.c.pages;
-      const int64_t page = ok ? g.n[s] : 0;
-      const int64_t in = (t + 16 * s) & mask;
-      c += page * p.c.c_sp + in * p.c.c_st;
-      b += page * p.c.s_sp + in * p.c.s_st;
-      const uint32_t bits = !ok || left <= 0 ? 0u : left >= 16 ? 0xFFFFu : (1u << left) - 1u;
-      there |= bits << (16 * s);
-      load_codes<D>(p.c.k + c + r * static_cast<uint32_t>(p.c.c_st), p.c.ks + b + r * static_cast<uint32_t>(p.c.s_st), h, st.k[s]);
-      load_codes<D>(p.c.v + c + r * static_cast<uint32_t>(p.c.c_st), p.c.vs + b + r * static_cast<uint32_t>(p.c.s_st), h, st.v[s]);
-    } else {
-      const bool ok = g.n[s] >= 0 && g.n[s] < p.c.pages;
-      const int64_t page = ok ? g.n[s] : 0;
-      const int64_t in = min(t + 16 * s + r, t_end - 1) & mask;
-      c += page * p.c.c_sp + in * p.c.c_st;
-      b += page * p.c.s_sp + in * p.c.s_st;
-      there |= static_cast<uint32_t>(__builtin_amdgcn_ballot_w64(ok && r < left) & 0xFFFFu) << (16 * s);
-      load_codes<D>(p.c.k + c, p.c.ks + b, h, st.k[s]);
-      load_codes<D>(p.c.v + c, p.c.vs + b, h, st.v[s]);
-    }
+    const Half a = locate<PAGE16>(p, g.n[s], t + 16 * s, t_end);
+    st.there |= a.there << (16 * s);
+    load_codes<D>(at.k + a.c, a.c_lane, at.ks + a.s, a.s_lane, h, st.k[s]);
+    load_codes<D>(at.v + a.c, a.c_lane, at.vs + a.s, a.s_lane, h, st.v[s]);
   }
-  st.there = there;
+}
+
+// The cache from cached head `head` on.
+__device__ __forceinline__ Kv4Cache at_head(const Kv4Cache& c, int32_t head) {
+  Kv4Cache a = c;
+  a.k += head * c.c_sh;
+  a.v += head * c.c_sh;
+  a.ks += head * c.s_sh;
+  a.vs += head * c.s_sh;
+  return a;
 }
 
 // ------------------------------------------------------------------ the kernel
@@ -294,9 +418,12 @@ __device__ __forceinline__ float to_f32(uint32_t half) {
   else return f16_lo(half);
 }
 
-// bf16: one part. fp16: high and low parts whose sum is the value.
+// bf16: one part. fp16: high and low parts whose sum is the value. `sign`: 0, or 0x80008000 to
+// negate (the scale's sign: scores are then multiplied by its magnitude, after their maximum).
 template <int DT, int PARTS>
-__device__ __forceinline__ void split8(const u32x4 raw, bf16x8 (&out)[PARTS]) {
+__device__ __forceinline__ void split8(u32x4 raw, uint32_t sign, bf16x8 (&out)[PARTS]) {
+#pragma unroll
+  for (int i = 0; i < 4; i++) raw[i] ^= sign;
   if constexpr (DT == FP8Q_DTYPE_BF16) {
     out[0] = __builtin_bit_cast(bf16x8, raw);
   } else {
@@ -322,86 +449,30 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, DT)) void kv4_attention
   static_assert(kRows * kRowO * 4 <= kTile * kRowV * 2, "the joined output reuses V's LDS");
   __shared__ __align__(16) uint16_t lds_v[kWaves][kTile * kRowV];
   __shared__ float lds_m[kWaves][kRows], lds_l[kWaves][kRows];
-  extern __shared__ __align__(16) uint8_t lds_plan[];
+  extern __shared__ int32_t lds_plan[];
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_index();
   const int r = lane & 15, h = lane >> 4;
-  const int32_t B = static_cast<int32_t>(p.B);
-  const Plan plan{reinterpret_cast<int64_t*>(lds_plan), reinterpret_cast<int32_t*>(lds_plan + (B + 1) * 8)};
-
-  // one unit per sequence and cached head, in order, unless something is split or has several tiles
-  const bool direct = !SPLIT && p.q_indptr == nullptr && p.group <= kRows;
-  if (!direct) make_plan(p, plan);
-
-  // this block's places on the line: of spans when splitting, else of units
-  int64_t at, stop;
-  if constexpr (SPLIT) {
-    const int64_t total = plan.line[B] * p.Hkv, run = run_length(total, p.blocks);
-    at = min(blockIdx.x * run, total);
-    stop = min(at + run, total);
-    if (blockIdx.x == 0) {
-      for (int32_t b = tid; b <= B; b += kThreads) {
-        p.plan_line[b] = plan.line[b];
-        p.plan_first[b] = plan.first[b];
-      }
-    }
-  } else {
-    at = blockIdx.x;
-    stop = (direct ? p.B : static_cast<int64_t>(plan.first[B])) * p.Hkv;
-  }
-
-  while (at < stop) {
-    // the unit at this place, and its spans [s0, s1) of this run
-    int32_t b, tile = 0, head, s0 = 0, s1;
-    Seq seq;
-    int64_t next, piece = 0;
-    bool whole = true;
-    if constexpr (SPLIT) {
-      b = __builtin_amdgcn_readfirstlane(find_seq(plan.line, B, at / p.Hkv));
-      seq = sequence(p, b);
-      const int32_t spans = spans_of(seq);
-      const int64_t in = at - plan.line[b] * p.Hkv;
-      const int32_t unit = __builtin_amdgcn_readfirstlane(static_cast<int32_t>(in / spans));
-      tile = unit / p.Hkv;
-      head = unit - tile * p.Hkv;
-      s0 = __builtin_amdgcn_readfirstlane(static_cast<int32_t>(in - static_cast<int64_t>(unit) * spans));
-      s1 = __builtin_amdgcn_readfirstlane(static_cast<int32_t>(min(static_cast<int64_t>(spans), s0 + (stop - at))));
-      next = at + (s1 - s0);
-      whole = s0 == 0 && s1 == spans;
-      piece = blockIdx.x + static_cast<int64_t>(plan.first[b]) * p.Hkv + unit;
-    } else {
-      const int32_t u = __builtin_amdgcn_readfirstlane(static_cast<int32_t>(at / p.Hkv));
-      head = __builtin_amdgcn_readfirstlane(static_cast<int32_t>(at - static_cast<int64_t>(u) * p.Hkv));
-      b = direct ? u : __builtin_amdgcn_readfirstlane(find_seq(plan.first, B, u));
-      seq = sequence(p, b);
-      if (!direct) tile = u - __builtin_amdgcn_readfirstlane(plan.first[b]);
-      s1 = spans_of(seq);
-      next = at + gridDim.x;
-    }
-    at = next;
-
-    // this lane's query row; rows [first, last] of the tile exist
-    const int64_t first = static_cast<int64_t>(tile) * kRows;
-    const int64_t rows = static_cast<int64_t>(seq.q_len) * p.group;
-    const int64_t last = min(first + kRows, rows) - 1;
+  Walk<kRows, SPLIT> walk(p, lds_plan);
+  Work w;
+  while (walk.next(w)) {
+    const Seq seq = w.seq;
+    const int32_t head = w.head;
+    const Rows tr(p, w, kRows);
+    const int32_t first = tr.first, last = tr.last;
     const bool row_there = first + r <= last;
-    const int64_t idx = row_there ? first + r : last;
-    const int32_t qi = static_cast<int32_t>(idx / p.group);
-    const int32_t qh = head * p.group + static_cast<int32_t>(idx - static_cast<int64_t>(qi) * p.group);
-    const int32_t before = seq.kv_len - seq.q_len + 1;  // tokens that query 0 sees
-    const int32_t limit = p.causal ? min(before + qi, seq.kv_len) : seq.kv_len;
-    const int32_t low = p.causal ? before + static_cast<int32_t>(first / p.group) : seq.kv_len;  // of the first row
-    const int32_t high = p.causal ? before + static_cast<int32_t>(last / p.group) : seq.kv_len;  // of the last
-    const int32_t t_end = min(min(s1 * kSpan, seq.kv_len), high);
+    const int32_t idx = row_there ? first + r : last, qi = idx / p.group, qh = head * p.group + idx - qi * p.group;
+    const int32_t limit = tr.seen(p, seq, idx), low = tr.seen(p, seq, first);
+    const int32_t t_end = min(w.t1, tr.seen(p, seq, last));
 
-    const int32_t* table = p.table + b * p.table_sb;
-    const int64_t head_c = head * p.c.c_sh, head_s = head * p.c.s_sh;
-    int32_t t = s0 * kSpan + kTile * wave;
+    const int32_t* table = p.table + w.b * p.table_sb;
+    const Kv4Cache cache = at_head(p.c, head);
+    int32_t t = w.t0 + kTile * wave;
     Step<D> st;
     Pages pages;
     if (t < t_end) {
       pages = load_pages<PAGE16>(p, table, t, t_end);
-      load_step<D, PAGE16>(p, pages, head_c, head_s, t, t_end, st);
-      pages = load_pages<PAGE16>(p, table, t + kSpan, t_end);
+      load_step<D, PAGE16>(p, cache, pages, t, t_end, st);
+      pages = load_pages<PAGE16>(p, table, t + kStep, t_end);
     }
 
     bf16x8 q[PARTS][kSteps];
@@ -412,7 +483,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, DT)) void kv4_attention
         u32x4 raw = {0u, 0u, 0u, 0u};
         if (row_there) raw = *reinterpret_cast<const u32x4*>(src + 8 * j);
         bf16x8 part[PARTS];
-        split8<DT, PARTS>(raw, part);
+        split8<DT, PARTS>(raw, p.q_sign, part);
 #pragma unroll
         for (int a = 0; a < PARTS; a++) q[a][j] = part[a];
       }
@@ -424,7 +495,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, DT)) void kv4_attention
     for (int d = 0; d < kDims; d++) o[d] = f32x4{0.f, 0.f, 0.f, 0.f};
     float m = kNegInf, l = 0.0f;  // l: this lane's share of the row's sum
 
-    for (; t < t_end; t += kSpan) {
+    for (; t < t_end; t += kStep) {
       f32x4 s[2];
 #pragma unroll
       for (int c = 0; c < 2; c++) {
@@ -445,47 +516,42 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, DT)) void kv4_attention
         for (int j = 0; j < kSteps; j++)
           *reinterpret_cast<bf16x8*>(vt + (16 * c + r) * kRowV + D / 4 * h + 8 * j) = widen_codes<D>(st.v[c], j);
       }
-      // the next step's codes come in while this one's softmax and second product run
-      if (t + kSpan < t_end) {
-        load_step<D, PAGE16>(p, pages, head_c, head_s, t + kSpan, t_end, st);
-        pages = load_pages<PAGE16>(p, table, t + 2 * kSpan, t_end);
-      }
+      // the next step's codes come in while this one's softmax and second product run (past the
+      // end: rows of the last page, not used)
+      load_step<D, PAGE16>(p, cache, pages, t + kStep, t_end, st);
+      pages = load_pages<PAGE16>(p, table, t + 2 * kStep, t_end);
 
-      float x[2][4], mx = kNegInf;
-#pragma unroll
-      for (int c = 0; c < 2; c++)
-#pragma unroll
-        for (int i = 0; i < 4; i++) x[c][i] = s[c][i] * p.scale_log2;
       if (part) {
 #pragma unroll
         for (int c = 0; c < 2; c++)
 #pragma unroll
           for (int i = 0; i < 4; i++) {
             const int n = 16 * c + 4 * h + i;
-            if (((there >> n) & 1u) == 0u || t + n >= limit) x[c][i] = kNegInf;
+            if (((there >> n) & 1u) == 0u || t + n >= limit) s[c][i] = kNegInf;
           }
       }
+      float mx = kNegInf;
 #pragma unroll
       for (int c = 0; c < 2; c++)
 #pragma unroll
-        for (int i = 0; i < 4; i++) mx = fmaxf(mx, x[c][i]);
-      mx = fmaxf(quad_max(mx), m);
-      const float ms = mx == kNegInf ? 0.0f : mx;  // nothing seen yet: every p is 0
-      if (__builtin_amdgcn_ballot_w64(mx > m) != 0) {
-        const float alpha = exp2_fast(m - ms);
-        m = mx;
+        for (int i = 0; i < 4; i++) mx = fmaxf(mx, s[c][i]);
+      mx = quad_max(mx) * p.scale_log2;
+      if (__builtin_amdgcn_ballot_w64(mx > m + kHeadroom) != 0) {
+        const float top = fmaxf(mx, m), alpha = exp2_fast(m - (top == kNegInf ? 0.0f : top));
+        m = top;
         l *= alpha;
 #pragma unroll
         for (int d = 0; d < kDims; d++)
 #pragma unroll
           for (int i = 0; i < 4; i++) o[d][i] *= alpha;
       }
+      const float ms = m == kNegInf ? 0.0f : m;  // nothing seen yet: every p is 0
       bf16x8 pr[PARTS];
 #pragma unroll
       for (int c = 0; c < 2; c++)
 #pragma unroll
         for (int i = 0; i < 4; i++) {
-          const float e = exp2_fast(x[c][i] - ms);
+          const float e = exp2_fast(fmaf(s[c][i], p.scale_log2, -ms));
           l += e;
           pr[0][4 * c + i] = static_cast<__bf16>(e);
           if constexpr (PARTS == 2) pr[1][4 * c + i] = static_cast<__bf16>(e - static_cast<float>(pr[0][4 * c + i]));
@@ -518,7 +584,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, DT)) void kv4_attention
     __syncthreads();
     float top = kNegInf;
 #pragma unroll
-    for (int w = 0; w < kWaves; w++) top = fmaxf(top, lds_m[w][r]);
+    for (int n = 0; n < kWaves; n++) top = fmaxf(top, lds_m[n][r]);
     {
       const float f = exp2_fast(m - (top == kNegInf ? 0.0f : top));
       float* dst = reinterpret_cast<float*>(vt) + r * kRowO + 4 * h;
@@ -534,16 +600,16 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, DT)) void kv4_attention
       for (int i = 0; i < 8; i++) v[i] = 0.0f;
       float mm = kNegInf, ll = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWaves; w++) {
-        const float* src = reinterpret_cast<const float*>(lds_v[w]) + row * kRowO + col;
+      for (int n = 0; n < kWaves; n++) {
+        const float* src = reinterpret_cast<const float*>(lds_v[n]) + row * kRowO + col;
 #pragma unroll
         for (int i = 0; i < 8; i++) v[i] += src[i];
-        mm = fmaxf(mm, lds_m[w][row]);
+        mm = fmaxf(mm, lds_m[n][row]);
       }
 #pragma unroll
-      for (int w = 0; w < kWaves; w++) ll += lds_l[w][row] * exp2_fast(lds_m[w][row] - (mm == kNegInf ? 0.0f : mm));
-      if (SPLIT && !whole) {
-        float* part = p.parts + piece * (kRows * (D + 2));
+      for (int n = 0; n < kWaves; n++) ll += lds_l[n][row] * exp2_fast(lds_m[n][row] - (mm == kNegInf ? 0.0f : mm));
+      if (SPLIT && !w.whole) {
+        float* part = p.parts + static_cast<int64_t>(w.piece) * (kRows * (D + 2));
 #pragma unroll
         for (int i = 0; i < 8; i += 4)
           *reinterpret_cast<f32x4*>(part + row * D + col + i) = f32x4{v[i], v[i + 1], v[i + 2], v[i + 3]};
@@ -552,159 +618,420 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, DT)) void kv4_attention
           part[kRows * D + 2 * row + 1] = ll;
         }
       } else {
-        const int64_t ri = first + row;
-        const int32_t i = static_cast<int32_t>(ri / p.group);
-        const int64_t row_t = seq.q0 + i, hh = head * p.group + static_cast<int32_t>(ri - static_cast<int64_t>(i) * p.group);
+        const int32_t i = (first + row) / p.group;
+        const int64_t row_t = seq.q0 + i, hh = head * p.group + first + row - i * p.group;
         const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
-        u32x4 w;
+        u32x4 bits;
 #pragma unroll
-        for (int j = 0; j < 4; j++) w[j] = pack16<DT>(v[2 * j] * inv, v[2 * j + 1] * inv);
-        *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p.out) + row_t * p.o_st + hh * p.o_sh + col) = w;
+        for (int j = 0; j < 4; j++) bits[j] = pack16<DT>(v[2 * j] * inv, v[2 * j + 1] * inv);
+        *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p.out) + row_t * p.o_st + hh * p.o_sh + col) = bits;
         if (p.lse && col == 0)
-          p.lse[row_t * p.l_st + hh] = ll > 0.0f ? (mm + __builtin_amdgcn_logf(ll)) * 0.6931471805599453f : kNegInf;
+          p.lse[row_t * p.l_st + hh] = ll > 0.0f ? (mm + __builtin_amdgcn_logf(ll)) * kLn2 : kNegInf;
       }
     }
     __syncthreads();
   }
 }
 
-// Joins the pieces of one query row: a block per (token, query head). The waves take the pieces
-// in turn, every lane D / 64 elements.
-template <int D, int DT>
+// ------------------------------------------------------------------ many query rows
+// The same products for tiles of 64 QT rows: every wave has 16 QT rows of its own and all the
+// tokens, 64 at a time. K's codes are converted in registers by every wave (they serve QT
+// products each); V is converted once per block into LDS, a quarter of the tokens per wave, one
+// step ahead of its use (two buffers, one barrier per step).
+constexpr int kStepW = 64;
+
+template <int D, int DT, int QT, bool SPLIT, bool PAGE16>
+__global__ __launch_bounds__(kThreads, 2) void kv4_attention_wide_kernel(Kv4AttnParams p) {
+  constexpr int PARTS = DT == FP8Q_DTYPE_F16 ? 2 : 1;
+  constexpr int kSteps = D / 32, kDims = D / 16, kRowV = D + kPadV;
+  constexpr int kHalves = kStepW / 16;
+  constexpr int ROWS = 16 * QT * kWaves;
+  static_assert(kHalves == kWaves, "every wave converts 16 tokens of V");
+  __shared__ __align__(16) uint16_t lds_v[2][kStepW * kRowV];
+  extern __shared__ int32_t lds_plan[];
+  const int lane = threadIdx.x & 63, wave = wave_index();
+  const int r = lane & 15, h = lane >> 4;
+  Walk<ROWS, SPLIT> walk(p, lds_plan);
+  Work w;
+  while (walk.next(w)) {
+    const Seq seq = w.seq;
+    const int32_t head = w.head;
+    const Rows tr(p, w, ROWS);
+    const int32_t wfirst = tr.first + 16 * QT * wave;  // this wave's rows
+    const int32_t low = tr.seen(p, seq, min(wfirst, tr.last));
+    const int32_t t0 = w.t0, t_end = min(w.t1, tr.seen(p, seq, tr.last));
+
+    const int32_t* table = p.table + w.b * p.table_sb;
+    const Kv4Cache cache = at_head(p.c, head);
+    Codes<D> k[kHalves], v;
+    uint64_t k_there = 0;
+    uint32_t v_there = 0;
+    int32_t k_page[kHalves], v_page = 0;
+    auto load_k = [&](int32_t t) {
+      k_there = 0;
+#pragma unroll
+      for (int c = 0; c < kHalves; c++) {
+        const Half a = locate<PAGE16>(p, k_page[c], t + 16 * c, t_end);
+        k_there |= static_cast<uint64_t>(a.there) << (16 * c);
+        load_codes<D>(cache.k + a.c, a.c_lane, cache.ks + a.s, a.s_lane, h, k[c]);
+      }
+    };
+    auto load_v = [&](int32_t t) {
+      const Half a = locate<PAGE16>(p, v_page, t + 16 * wave, t_end);
+      v_there = a.there;
+      load_codes<D>(cache.v + a.c, a.c_lane, cache.vs + a.s, a.s_lane, h, v);
+    };
+    auto page_k = [&](int32_t t) {
+#pragma unroll
+      for (int c = 0; c < kHalves; c++) k_page[c] = load_page<PAGE16>(p, table, t + 16 * c, t_end);
+    };
+    auto put_v = [&](int buf) {
+      if (((v_there >> r) & 1u) == 0u) zero_codes<D>(v);
+#pragma unroll
+      for (int j = 0; j < kSteps; j++)
+        *reinterpret_cast<bf16x8*>(&lds_v[buf][(16 * wave + r) * kRowV + D / 4 * h + 8 * j]) = widen_codes<D>(v, j);
+    };
+    if (t0 < t_end) {
+      page_k(t0);
+      v_page = load_page<PAGE16>(p, table, t0 + 16 * wave, t_end);
+      load_k(t0);
+      load_v(t0);
+      page_k(t0 + kStepW);
+      v_page = load_page<PAGE16>(p, table, t0 + kStepW + 16 * wave, t_end);
+    }
+
+    bf16x8 q[QT][PARTS][kSteps];
+    int32_t limit[QT];
+#pragma unroll
+    for (int n = 0; n < QT; n++) {
+      const int32_t row = wfirst + 16 * n + r;
+      const bool there = row <= tr.last;
+      const int32_t idx = there ? row : tr.last, qi = idx / p.group, qh = head * p.group + idx - qi * p.group;
+      limit[n] = tr.seen(p, seq, idx);
+      const uint16_t* src = static_cast<const uint16_t*>(p.q) + (seq.q0 + qi) * p.q_st + qh * p.q_sh + D / 4 * h;
+#pragma unroll
+      for (int j = 0; j < kSteps; j++) {
+        u32x4 raw = {0u, 0u, 0u, 0u};
+        if (there) raw = *reinterpret_cast<const u32x4*>(src + 8 * j);
+        bf16x8 part[PARTS];
+        split8<DT, PARTS>(raw, p.q_sign, part);
+#pragma unroll
+        for (int a = 0; a < PARTS; a++) q[n][a][j] = part[a];
+      }
+    }
+
+    f32x4 o[QT][kDims];
+    float m[QT], l[QT];
+#pragma unroll
+    for (int n = 0; n < QT; n++) {
+      m[n] = kNegInf;
+      l[n] = 0.0f;
+#pragma unroll
+      for (int d = 0; d < kDims; d++) o[n][d] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+
+    if (t0 < t_end) {
+      put_v(0);
+      load_v(t0 + kStepW);
+      v_page = load_page<PAGE16>(p, table, t0 + 2 * kStepW + 16 * wave, t_end);
+    }
+    __syncthreads();
+    int buf = 0;
+    for (int32_t t = t0; t < t_end; t += kStepW, buf ^= 1) {
+      f32x4 s[QT][kHalves];
+      const uint64_t there = k_there;
+#pragma unroll
+      for (int c = 0; c < kHalves; c++) {
+#pragma unroll
+        for (int n = 0; n < QT; n++) s[n][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < kSteps; j++) {
+          const bf16x8 kk = widen_codes<D>(k[c], j);
+#pragma unroll
+          for (int n = 0; n < QT; n++)
+#pragma unroll
+            for (int a = 0; a < PARTS; a++)
+              s[n][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kk, q[n][a][j], s[n][c], 0, 0, 0);
+        }
+      }
+      // loads past the end bring rows of the last page, which are not used
+      load_k(t + kStepW);
+      page_k(t + 2 * kStepW);
+      put_v(buf ^ 1);
+      load_v(t + 2 * kStepW);
+      v_page = load_page<PAGE16>(p, table, t + 3 * kStepW + 16 * wave, t_end);
+      {
+        const bool part = there != ~0ull || t + kStepW > low;  // wave-uniform
+        bf16x8 pr[QT][PARTS][kHalves / 2];
+#pragma unroll
+        for (int n = 0; n < QT; n++) {
+          if (part) {
+#pragma unroll
+            for (int c = 0; c < kHalves; c++)
+#pragma unroll
+              for (int i = 0; i < 4; i++) {
+                const int at = 16 * c + 4 * h + i;
+                if (((there >> at) & 1u) == 0u || t + at >= limit[n]) s[n][c][i] = kNegInf;
+              }
+          }
+          float mx = kNegInf;
+#pragma unroll
+          for (int c = 0; c < kHalves; c++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) mx = fmaxf(mx, s[n][c][i]);
+          mx = quad_max(mx) * p.scale_log2;
+          if (__builtin_amdgcn_ballot_w64(mx > m[n] + kHeadroom) != 0) {
+            const float top = fmaxf(mx, m[n]), alpha = exp2_fast(m[n] - (top == kNegInf ? 0.0f : top));
+            m[n] = top;
+            l[n] *= alpha;
+#pragma unroll
+            for (int d = 0; d < kDims; d++)
+#pragma unroll
+              for (int i = 0; i < 4; i++) o[n][d][i] *= alpha;
+          }
+          const float ms = m[n] == kNegInf ? 0.0f : m[n];
+#pragma unroll
+          for (int c = 0; c < kHalves; c++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+              const float e = exp2_fast(fmaf(s[n][c][i], p.scale_log2, -ms));
+              l[n] += e;
+              const __bf16 hi = static_cast<__bf16>(e);
+              pr[n][0][c / 2][4 * (c % 2) + i] = hi;
+              if constexpr (PARTS == 2) pr[n][1][c / 2][4 * (c % 2) + i] = static_cast<__bf16>(e - static_cast<float>(hi));
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < kHalves / 2; c++) {
+#pragma unroll
+          for (int d = 0; d < kDims; d++) {
+            const uint16_t* src = &lds_v[buf][(32 * c + 4 * h + (r >> 2)) * kRowV + 16 * d + 4 * (r & 3)];
+            const s16x4 a0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(src));
+            const s16x4 a1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(src + 16 * kRowV));
+            const auto av = __builtin_shufflevector(a0, a1, 0, 1, 2, 3, 4, 5, 6, 7);
+#pragma unroll
+            for (int n = 0; n < QT; n++)
+#pragma unroll
+              for (int a = 0; a < PARTS; a++)
+                o[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, av), pr[n][a][c], o[n][d], 0, 0, 0);
+          }
+        }
+      }
+      __syncthreads();
+    }
+
+#pragma unroll
+    for (int n = 0; n < QT; n++) {
+      const float sum = quad_sum(l[n]);
+      const int32_t row = wfirst + 16 * n + r;
+      if (row > tr.last) continue;
+      if (SPLIT && !w.whole) {
+        float* part = p.parts + static_cast<int64_t>(w.piece) * (ROWS * (D + 2));
+        const int at = row - tr.first;
+#pragma unroll
+        for (int d = 0; d < kDims; d++) *reinterpret_cast<f32x4*>(part + at * D + 16 * d + 4 * h) = o[n][d];
+        if (h == 0) {
+          part[ROWS * D + 2 * at] = m[n];
+          part[ROWS * D + 2 * at + 1] = sum;
+        }
+      } else {
+        const int32_t i = row / p.group;
+        const int64_t row_t = seq.q0 + i, hh = head * p.group + row - i * p.group;
+        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+        uint16_t* dst = static_cast<uint16_t*>(p.out) + row_t * p.o_st + hh * p.o_sh + 4 * h;
+#pragma unroll
+        for (int d = 0; d < kDims; d++)
+          *reinterpret_cast<u32x2*>(dst + 16 * d) =
+              u32x2{pack16<DT>(o[n][d][0] * inv, o[n][d][1] * inv), pack16<DT>(o[n][d][2] * inv, o[n][d][3] * inv)};
+        if (p.lse && h == 0)
+          p.lse[row_t * p.l_st + hh] = sum > 0.0f ? (m[n] + __builtin_amdgcn_logf(sum)) * kLn2 : kNegInf;
+      }
+    }
+  }
+}
+
+// Joins the pieces of query rows, WAVES waves for each: they take the pieces in turn, every
+// lane D / 64 elements.
+template <int D, int DT, int ROWS, int WAVES>
 __global__ __launch_bounds__(kThreads) void kv4_join_kernel(Kv4AttnParams p) {
   constexpr int kPer = D / 64;
-  __shared__ float lds_o[kWaves][D], lds_l[kWaves];
+  constexpr int kStepF = ROWS * (D + 2);  // floats of a piece
+  __shared__ float lds_o[WAVES][D], lds_l[WAVES];
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_index();
-  const int32_t t = static_cast<int32_t>(blockIdx.x / p.Hq), qh = static_cast<int32_t>(blockIdx.x % p.Hq);
+  const int32_t row = blockIdx.x * (kWaves / WAVES) + (WAVES == 1 ? wave : 0);  // of T * Hq
+  if (row >= static_cast<int32_t>(p.T) * p.Hq) return;
+  const int32_t t = row / p.Hq, qh = row - t * p.Hq;
   int32_t b = t;
-  if (p.q_indptr) {
-    // the sequence that holds row t: the last one whose clamped start is not after it
+  if (p.q_indptr) {  // the sequence that holds row t: the last one whose clamped start is not after it
     int32_t lo = 0, hi = static_cast<int32_t>(p.B);
     while (hi - lo > 1) {
       const int32_t mid = (lo + hi) >> 1;
-      if (clamp32(p.q_indptr[mid], p.T) <= t) lo = mid; else hi = mid;
+      if (clamp32(read_int(p.q_indptr, mid), p.T) <= t) lo = mid; else hi = mid;
     }
     b = lo;
   }
   const Seq seq = sequence(p, b);
-  if (t < seq.q0 || t >= seq.q0 + seq.q_len) return;
-  const int32_t head = qh / p.group, spans = spans_of(seq);
-  const int64_t idx = static_cast<int64_t>(t - seq.q0) * p.group + (qh - head * p.group);
-  const int64_t unit = idx / kRows * p.Hkv + head;
-  const int row = static_cast<int>(idx % kRows);
+  const int32_t total = p.plan[p.B] * p.Hkv;
+  if (t < seq.q0 || t >= seq.q0 + seq.q_len || total == 0) return;
+  const int32_t head = qh / p.group, spans = spans_of(p, seq);
+  const int32_t idx = (t - seq.q0) * p.group + qh - head * p.group;
+  const int32_t unit = idx / ROWS * p.Hkv + head, at = idx % ROWS;
   // the runs that hold a part of this unit
-  const int64_t total = p.plan_line[p.B] * p.Hkv;
-  if (total == 0) return;
-  const int64_t run = run_length(total, p.blocks), from = p.plan_line[b] * p.Hkv + unit * spans;
-  const int64_t run0 = from / run, run1 = (from + spans - 1) / run;
-  if (run0 == run1) return;
-  const int32_t chunks = static_cast<int32_t>(run1 - run0) + 1;
-  constexpr int64_t step = kRows * (D + 2);
-  const float* base = p.parts + (run0 + static_cast<int64_t>(p.plan_first[b]) * p.Hkv + unit) * step;
+  const int32_t run = run_length(total, p.blocks), from = p.plan[b] * p.Hkv + unit * spans;
+  const int32_t run0 = from / run, pieces = (from + spans - 1) / run - run0 + 1;
+  if (pieces == 1) return;
+  const float* base = p.parts + static_cast<int64_t>(run0 + p.plan[p.B + 1 + b] * p.Hkv + unit) * kStepF;
+  const float* ml = base + ROWS * D + 2 * at;
 
   float top = kNegInf;
-  for (int32_t c = lane; c < chunks; c += 64) top = fmaxf(top, base[c * step + kRows * D + 2 * row]);
+  for (int32_t c = lane; c < pieces; c += 64) top = fmaxf(top, ml[static_cast<int64_t>(c) * kStepF]);
   top = wave_max(top);
   const float ts = top == kNegInf ? 0.0f : top;
   float acc[kPer], l = 0.0f;
 #pragma unroll
   for (int i = 0; i < kPer; i++) acc[i] = 0.0f;
 #pragma unroll 4
-  for (int32_t c = wave; c < chunks; c += kWaves) {
-    const float* part = base + c * step;
-    const float f = exp2_fast(part[kRows * D + 2 * row] - ts);
-    l += part[kRows * D + 2 * row + 1] * f;
+  for (int32_t c = WAVES == 1 ? 0 : wave; c < pieces; c += WAVES) {
+    const int64_t off = static_cast<int64_t>(c) * kStepF;
+    const float f = exp2_fast(ml[off] - ts);
+    l += ml[off + 1] * f;
 #pragma unroll
-    for (int i = 0; i < kPer; i++) acc[i] += part[row * D + kPer * lane + i] * f;
+    for (int i = 0; i < kPer; i++) acc[i] += base[off + at * D + kPer * lane + i] * f;
   }
+  if constexpr (WAVES > 1) {
 #pragma unroll
-  for (int i = 0; i < kPer; i++) lds_o[wave][kPer * lane + i] = acc[i];
-  if (lane == 0) lds_l[wave] = l;
-  __syncthreads();
-  float ll = 0.0f;
+    for (int i = 0; i < kPer; i++) lds_o[wave][kPer * lane + i] = acc[i];
+    if (lane == 0) lds_l[wave] = l;
+    __syncthreads();
+    if (wave != 0) return;
+    l = 0.0f;
 #pragma unroll
-  for (int w = 0; w < kWaves; w++) ll += lds_l[w];
-  const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
-  for (int d = 2 * tid; d < D; d += 2 * kThreads) {
-    float a = 0.0f, c = 0.0f;
+    for (int i = 0; i < kPer; i++) acc[i] = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kWaves; w++) {
-      a += lds_o[w][d];
-      c += lds_o[w][d + 1];
+    for (int w = 0; w < WAVES; w++) {
+      l += lds_l[w];
+#pragma unroll
+      for (int i = 0; i < kPer; i++) acc[i] += lds_o[w][kPer * lane + i];
     }
-    *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + t * p.o_st + qh * p.o_sh + d) = pack16<DT>(a * inv, c * inv);
   }
-  if (p.lse && tid == 0)
-    p.lse[t * p.l_st + qh] = ll > 0.0f ? (ts + __builtin_amdgcn_logf(ll)) * 0.6931471805599453f : kNegInf;
+  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  uint16_t* dst = static_cast<uint16_t*>(p.out) + t * p.o_st + qh * p.o_sh + kPer * lane;
+  if constexpr (kPer == 1) {
+    *dst = static_cast<uint16_t>(pack16<DT>(acc[0] * inv, 0.0f));
+  } else {
+#pragma unroll
+    for (int i = 0; i < kPer; i += 2) *reinterpret_cast<uint32_t*>(dst + i) = pack16<DT>(acc[i] * inv, acc[i + 1] * inv);
+  }
+  if (p.lse && lane == 0) p.lse[t * p.l_st + qh] = l > 0.0f ? (ts + __builtin_amdgcn_logf(l)) * kLn2 : kNegInf;
 }
 
 // ------------------------------------------------------------------ launch
+// Rows of the widest tile whose queries and outputs the registers hold.
+constexpr int widest(int dtype, int64_t D) { return D * (dtype == FP8Q_DTYPE_F16 ? 2 : 1) <= 128 ? 128 : 64; }
+
+// Query rows of a tile. Up to two tiles of 16 rows per sequence (of mean length) and cached head
+// take the kernel whose waves share the tokens; more take the one whose waves share the rows.
+int tile_rows(int dtype, int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D) {
+  const int64_t rows = (T * (Hq / Hkv) + B - 1) / B;
+  return rows <= 2 * kRows ? kRows : rows <= 64 ? 64 : widest(dtype, D);
+}
+
 struct Shape {
+  int rows;        // of a tile
   int64_t units;   // at most
-  int64_t blocks;  // that a split call's work is cut for
-  int64_t line_bytes, plan_bytes, bytes;
+  int64_t blocks;  // that a split call's work is cut for: those that run at once
+  int span_shift;
+  int64_t plan_bytes, bytes;  // workspace; 0: no split
 };
 
-Shape shape_of(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D) {
+Shape shape_of(int dtype, int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_tokens) {
   Shape s;
-  s.units = Hkv * ((T * (Hq / Hkv) + kRows - 1) / kRows + B);
-  s.blocks = static_cast<int64_t>(current_device_shape().cus) * 4;
-  s.line_bytes = (B + 1) * 8;
-  s.plan_bytes = (s.line_bytes + (B + 1) * 4 + 255) / 256 * 256;
-  s.bytes = s.plan_bytes + (s.units + s.blocks) * (kRows * (D + 2)) * 4;
+  s.rows = tile_rows(dtype, B, T, Hq, Hkv, D);
+  s.units = Hkv * ((T * (Hq / Hkv) + s.rows - 1) / s.rows + B);
+  const bool narrow = s.rows == kRows;
+  s.blocks = static_cast<int64_t>(current_device_shape().cus) * (narrow ? 4 : 2);
+  // spans of 128 tokens, or longer ones where the line could have 2^31 places
+  s.span_shift = 7;
+  while (s.units * ((max_tokens >> s.span_shift) + 1) >= (int64_t(1) << 31)) s.span_shift++;
+  s.plan_bytes = (2 * (B + 1) * 4 + 255) / 256 * 256;
+  // With many units the device is full without splitting; ragged lengths balance better with
+  // it, which the narrow kernel's small pieces are worth up to some rounds of blocks.
+  const bool split = max_tokens > (int64_t(kMinRun) << s.span_shift) && s.units < s.blocks * (narrow ? 8 : 1);
+  s.bytes = split ? s.plan_bytes + (s.units + s.blocks) * (s.rows * (D + 2)) * 4 : 0;
   return s;
 }
 
-template <int D, int DT, bool PAGE16>
-void launch_d(const Kv4AttnParams& p, bool split, unsigned grid, hipStream_t stream) {
-  const size_t lds = (p.B + 1) * 12;
-  if (split) {
-    hipLaunchKernelGGL((kv4_attention_kernel<D, DT, true, PAGE16>), dim3(grid), dim3(kThreads), lds, stream, p);
-    hipLaunchKernelGGL((kv4_join_kernel<D, DT>), dim3(static_cast<unsigned>(p.T * p.Hq)), dim3(kThreads), 0, stream, p);
-  } else {
-    hipLaunchKernelGGL((kv4_attention_kernel<D, DT, false, PAGE16>), dim3(grid), dim3(kThreads), lds, stream, p);
-  }
-}
+struct Launch {
+  const Kv4AttnParams& p;
+  bool split, page16;
+  const Shape& shape;
+  unsigned grid;
+  hipStream_t stream;
 
-template <int D>
-void launch_dt(int dtype, bool page16, const Kv4AttnParams& p, bool split, unsigned grid, hipStream_t stream) {
-  if (dtype == FP8Q_DTYPE_BF16) {
-    if (page16) launch_d<D, FP8Q_DTYPE_BF16, true>(p, split, grid, stream);
-    else launch_d<D, FP8Q_DTYPE_BF16, false>(p, split, grid, stream);
-  } else {
-    if (page16) launch_d<D, FP8Q_DTYPE_F16, true>(p, split, grid, stream);
-    else launch_d<D, FP8Q_DTYPE_F16, false>(p, split, grid, stream);
+  template <int D, int DT, int ROWS, bool SPLIT, bool PAGE16>
+  void run() const {
+    const size_t lds = 2 * (p.B + 1) * sizeof(int32_t);
+    if constexpr (ROWS == kRows)
+      hipLaunchKernelGGL((kv4_attention_kernel<D, DT, SPLIT, PAGE16>), dim3(grid), dim3(kThreads), lds, stream, p);
+    else
+      hipLaunchKernelGGL((kv4_attention_wide_kernel<D, DT, ROWS / 64, SPLIT, PAGE16>), dim3(grid), dim3(kThreads), lds,
+                         stream, p);
+    if constexpr (SPLIT) {
+      const int64_t rows = p.T * p.Hq;
+      // a wave per row, or where the units are cut into many pieces a block
+      if (shape.blocks < 8 * shape.units)
+        hipLaunchKernelGGL((kv4_join_kernel<D, DT, ROWS, 1>), dim3(static_cast<unsigned>((rows + kWaves - 1) / kWaves)),
+                           dim3(kThreads), 0, stream, p);
+      else
+        hipLaunchKernelGGL((kv4_join_kernel<D, DT, ROWS, kWaves>), dim3(static_cast<unsigned>(rows)), dim3(kThreads), 0,
+                           stream, p);
+    }
   }
-}
+  template <int D, int DT, int ROWS>
+  void by_kind() const {
+    if (split) page16 ? run<D, DT, ROWS, true, true>() : run<D, DT, ROWS, true, false>();
+    else page16 ? run<D, DT, ROWS, false, true>() : run<D, DT, ROWS, false, false>();
+  }
+  template <int D, int DT>
+  void by_rows() const {
+    if (shape.rows == kRows) by_kind<D, DT, kRows>();
+    else if (shape.rows == 64) by_kind<D, DT, 64>();
+    else if constexpr (widest(DT, D) == 128) by_kind<D, DT, 128>();
+  }
+  template <int D>
+  void by_type(int dtype) const {
+    if (dtype == FP8Q_DTYPE_BF16) by_rows<D, FP8Q_DTYPE_BF16>();
+    else by_rows<D, FP8Q_DTYPE_F16>();
+  }
+};
 
 }  // namespace
 
-int64_t kv4_attention_workspace(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_tokens) {
-  const Shape s = shape_of(B, T, Hq, Hkv, D);
-  if (max_tokens <= kSpan * kMinRun || s.units >= 16 * s.blocks) return 0;
-  return s.bytes;
+int64_t kv4_attention_workspace(int dtype, int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_tokens) {
+  return shape_of(dtype, B, T, Hq, Hkv, D, max_tokens).bytes;
 }
 
 int launch_kv4_attention(int dtype, int64_t D, Kv4AttnParams p, void* ws, int64_t ws_bytes, hipStream_t stream) {
-  const Shape s = shape_of(p.B, p.T, p.Hq, p.Hkv, D);
-  const int64_t need = kv4_attention_workspace(p.B, p.T, p.Hq, p.Hkv, D, p.max_tokens);
-  const bool split = need > 0 && ws && ws_bytes >= need;
+  const Shape s = shape_of(dtype, p.B, p.T, p.Hq, p.Hkv, D, p.max_tokens);
+  const bool split = s.bytes > 0 && ws && ws_bytes >= s.bytes;
   p.max_units = s.units;
+  p.span_shift = s.span_shift;
   if (split) {
-    uint8_t* base = static_cast<uint8_t*>(ws);
     p.blocks = static_cast<int32_t>(s.blocks);
-    p.plan_line = reinterpret_cast<int64_t*>(base);
-    p.plan_first = reinterpret_cast<int32_t*>(base + s.line_bytes);
-    p.parts = reinterpret_cast<float*>(base + s.plan_bytes);
+    p.plan = static_cast<int32_t*>(ws);
+    p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + s.plan_bytes);
   }
-  // a page of 16 tokens or more holds every 16 tokens that a wave loads together; a lane's
-  // offset in them has 32 bits
-  const bool page16 = p.c.page_shift >= 4 && p.c.c_st < (int64_t(1) << 27) && p.c.s_st < (int64_t(1) << 27);
+  // a page of 16 tokens or more holds every 16 tokens that a wave loads together; their offsets
+  // are computed in 32 bits
+  const int64_t page = int64_t(1) << p.c.page_shift, most = int64_t(1) << 32;
+  const bool page16 = p.c.page_shift >= 4 && p.c.c_sp < most && p.c.s_sp < most && p.c.c_st < most / page &&
+                      p.c.s_st < most / page;
   // unsplit: blocks walk the units in turn
-  const unsigned grid = static_cast<unsigned>(split ? s.blocks : std::min<int64_t>(s.units, s.blocks * 4));
-  if (D == 64) launch_dt<64>(dtype, page16, p, split, grid, stream);
-  else if (D == 128) launch_dt<128>(dtype, page16, p, split, grid, stream);
-  else launch_dt<256>(dtype, page16, p, split, grid, stream);
+  const unsigned grid = static_cast<unsigned>(split ? s.blocks : std::min<int64_t>(s.units, int64_t(1) << 20));
+  const Launch run{p, split, page16, s, grid, stream};
+  if (D == 64) run.by_type<64>(dtype);
+  else if (D == 128) run.by_type<128>(dtype);
+  else run.by_type<256>(dtype);
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess) return fail(FP8Q_ELAUNCH, std::string("kv4 attention launch: ") + hipGetErrorString(err));
   return FP8Q_OK;

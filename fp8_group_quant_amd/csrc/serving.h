@@ -69,18 +69,19 @@ struct Kv4AttnParams {
   const int32_t* q_indptr;   // [B + 1], or nullptr: sequence b is row b
   int64_t B, T;
   int32_t Hq, Hkv, group;    // group = Hq / Hkv
-  float scale_log2;          // softmax scale times log2(e)
+  float scale_log2;          // magnitude of the softmax scale times log2(e)
+  uint32_t q_sign;           // 0x80008000 where the scale is negative
   int32_t causal;
+  int32_t span_shift;        // log2 of the tokens of a span
   int64_t max_units;         // query tiles x cached heads, at most
-  int32_t blocks;            // split only, as the next three: blocks that share the line of spans
-  int64_t* plan_line;        // [B + 1] spans before each sequence
-  int32_t* plan_first;       // [B + 1] query tiles before each sequence
+  int32_t blocks;            // split only, as the next two: blocks that share the line of spans
+  int32_t* plan;             // [2][B + 1] spans and query tiles before each sequence
   float* parts;              // partial outputs, maxima and sums by piece
 };
 
 // Bytes of workspace with which attention of this shape splits the cache axis on the current
 // device (0: it never does).
-int64_t kv4_attention_workspace(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_tokens);
+int64_t kv4_attention_workspace(int dtype, int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_tokens);
 int launch_kv4_attention(int dtype, int64_t D, Kv4AttnParams p, void* ws, int64_t ws_bytes, hipStream_t stream);
 
 }  // namespace fp8q

@@ -425,7 +425,7 @@ int fp8q_kv4_read(void* k, int64_t k_st, int64_t k_sh,
  * aligned, the index arrays and lse 4-byte [EALIGN]; out rows not overlapping, sm_scale finite,
  * workspace_bytes >= 0 [EINVAL]; and the cache's.
  */
-int64_t fp8q_kv4_attention_workspace_size(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+int64_t fp8q_kv4_attention_workspace_size(int dtype, int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
                                           int64_t max_tokens);
 
 int fp8q_kv4_attention(const void* q, int dtype, int64_t q_st, int64_t q_sh,

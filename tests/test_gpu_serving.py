@@ -329,9 +329,22 @@ def test_chunk_of_a_prompt(split):
     check_attention([70, 129], [513, 129], 8, 2, 128, 64, split=split)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("D,page", [(64, 1), (64, 16), (128, 64), (256, 8), (256, 32)])
+@pytest.mark.parametrize("q_lens,kv_lens,G", [
+    ([17, 9, 0, 1], [300, 9, 40, 1000], 4),       # tiles of 64 rows, most of them part filled
+    ([130, 65, 1, 200], [400, 70, 500, 150], 1),  # of 128 (or 64): waves without rows, rows without tokens
+])
+def test_many_query_rows(q_lens, kv_lens, G, D, page, dtype):
+    check_attention(q_lens, kv_lens, 2 * G, 2, D, page, dtype=dtype)
+    check_attention(q_lens, kv_lens, 2 * G, 2, D, page, causal=False, dtype=dtype, split=False, q_scale=0.02)
+
+
 def test_pages_missing_from_the_table():
     check_attention([3, 2], [100, 70], 4, 2, 128, 16, drop_page=True)
     check_attention([1], [9], 4, 2, 64, 16, drop_page=True)  # the only page: nothing is seen
+    check_attention([90, 70], [300, 170], 4, 2, 128, 16, drop_page=True)
+    check_attention([40, 70], [300, 170], 2, 2, 64, 4, drop_page=True)
 
 
 def test_scales_of_the_scores():

@@ -120,8 +120,9 @@ def test_attention_validation(kw, status):
 @no_gpu
 def test_workspace_size_without_a_device_or_with_refused_sizes():
     size = fq.load_library().fp8q_kv4_attention_workspace_size
-    assert size(1, 1, 32, 8, 128, 100000) == 0
-    assert size(1, 1, 32, 8, 96, 100000) == 0 and size(-1, 1, 32, 8, 128, 100) == 0
+    assert size(0, 1, 1, 32, 8, 128, 100000) == 0
+    assert size(0, 1, 1, 32, 8, 96, 100000) == 0 and size(0, -1, 1, 32, 8, 128, 100) == 0
+    assert size(2, 1, 1, 32, 8, 128, 100000) == 0
 
 
 def test_binding_refuses_tensors_that_do_not_fit():
