@@ -114,7 +114,8 @@ def _check(status: int) -> None:
 
 def _stream(stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the handle alone (a Stream object around it costs about 2 us)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -397,29 +398,38 @@ def fp8q_rms_norm_group_quant(x: torch.Tensor, weight: torch.Tensor, q: torch.Te
     fp8q_group_quant into q (uint8 or float8_e4m3fn) and s (a [M, K/G] view, whose type and strides
     choose the format and layout). x, residual, residual_out [M, K] and weight [K] have one type;
     residual_out receives h rounded to it (it may be the residual's or x's own tensor)."""
-    if x.dim() != 2 or x.dtype not in _DTYPES:
+    # written for few interpreter steps: with one token the checks are most of the call's time
+    dt = _DTYPES.get(x.dtype)
+    if dt is None or x.dim() != 2:
         raise ValueError("x must be a 2-D bf16, fp16 or fp32 tensor")
-    M, K = x.shape
-    rows = [x] + [t for t in (residual, residual_out) if t is not None]
-    for t in rows:
-        if t.dtype != x.dtype or tuple(t.shape) != (M, K):
+    shape = x.shape
+    M, K = shape
+    xs, qs, ss = x.stride(), q.stride(), s.stride()
+    inner = K <= 1 or (xs[1] == 1 and qs[-1] == 1)
+    r_ptr = ro_ptr = None
+    r_sm = ro_sm = 0
+    for t in (residual, residual_out):
+        if t is not None and (t.dtype != x.dtype or t.shape != shape):
             raise ValueError("residual and residual_out must have x's shape and type")
-    if weight.dtype != x.dtype or tuple(weight.shape) != (K,) or (K > 1 and weight.stride(0) != 1):
+    if residual is not None:
+        r_ptr, (r_sm, r_sk) = residual.data_ptr(), residual.stride()
+        inner = inner and (K <= 1 or r_sk == 1)
+    if residual_out is not None:
+        ro_ptr, (ro_sm, ro_sk) = residual_out.data_ptr(), residual_out.stride()
+        inner = inner and (K <= 1 or ro_sk == 1)
+    if weight.dtype != x.dtype or weight.dim() != 1 or weight.numel() != K or (K > 1 and weight.stride(0) != 1):
         raise ValueError("weight must be a contiguous [K] tensor of x's type")
-    if q.element_size() != 1 or tuple(q.shape) != (M, K):
+    if q.element_size() != 1 or q.shape != shape:
         raise ValueError(f"q has shape {tuple(q.shape)} of {q.dtype}, expected e4m3 bytes of {(M, K)}")
-    if K > 1 and any(t.stride(1) != 1 for t in (*rows, q)):
+    if not inner:
         raise ValueError("innermost dimensions must be contiguous")
     fmt = _scale_fmt_of(s)
     ng = K // group_size // (4 if fmt == SCALE_UE8M0_PACKED else 1) if group_size > 0 else 0
-    if tuple(s.shape) != (M, ng):
+    if s.shape != (M, ng):
         raise ValueError(f"s has shape {tuple(s.shape)}, expected {(M, ng)}")
     _check(load_library().fp8q_rms_norm_group_quant(
-        x.data_ptr(), _DTYPES[x.dtype], M, K, x.stride(0),
-        _ptr(residual), 0 if residual is None else residual.stride(0),
-        _ptr(residual_out), 0 if residual_out is None else residual_out.stride(0),
-        weight.data_ptr(), eps, q.data_ptr(), q.stride(0), s.data_ptr(), fmt, s.stride(0), s.stride(1),
-        group_size, _stream(stream)))
+        x.data_ptr(), dt, M, K, xs[0], r_ptr, r_sm, ro_ptr, ro_sm, weight.data_ptr(), eps, q.data_ptr(), qs[0],
+        s.data_ptr(), fmt, ss[0], ss[1], group_size, _stream(stream)))
 
 
 def rms_norm_group_quant(x: torch.Tensor, weight: torch.Tensor, group_size: int = 128, scale_fmt: str = "ue8m0",
@@ -463,35 +473,36 @@ def alloc_kv4_cache(pages: int, page_size: int, heads: int, head_dim: int, layou
 def _kv4_args(cache: Kv4Cache, heads: int, head_dim: int) -> tuple:
     """The cache's C arguments: pointers, sizes and strides."""
     k, ks, v, vs = cache
-    if k.dim() != 4 or ks.dim() != 4:
-        raise ValueError("cached tensors must be [pages, page_size, heads, ...]")
-    pages, page = k.shape[:2]
-    if k.shape != v.shape or ks.shape != vs.shape or tuple(k.shape) != (pages, page, heads, head_dim // 2) \
-            or tuple(ks.shape) != (pages, page, heads, head_dim // 32):
-        raise ValueError(f"cached tensors do not fit {heads} heads of {head_dim}: codes {tuple(k.shape)}, "
-                         f"scales {tuple(ks.shape)}")
-    cs, ss = k.stride(), ks.stride()
+    codes, scales = k.shape, ks.shape
+    if codes != v.shape or scales != vs.shape or len(codes) != 4 or codes[2:] != (heads, head_dim // 2) \
+            or scales != codes[:3] + (head_dim // 32,):
+        raise ValueError(f"cached tensors do not fit {heads} heads of {head_dim}: codes {tuple(codes)}, "
+                         f"scales {tuple(scales)}")
+    c_sp, c_st, c_sh, c_in = cs = k.stride()
+    s_sp, s_st, s_sh, s_in = ss = ks.stride()
     if cs != v.stride() or ss != vs.stride():
         raise ValueError("keys and values must have the same strides")
-    if cs[3] != 1 or ss[3] != 1:
+    if c_in != 1 or s_in != 1:
         raise ValueError("innermost dimensions must be contiguous")
     if not (k.dtype == ks.dtype == v.dtype == vs.dtype == torch.uint8):
         raise ValueError("cached tensors must be uint8")
-    return (k.data_ptr(), ks.data_ptr(), v.data_ptr(), vs.data_ptr(), pages, page,
-            cs[0], cs[1], cs[2], ss[0], ss[1], ss[2])
+    return (k.data_ptr(), ks.data_ptr(), v.data_ptr(), vs.data_ptr(), codes[0], codes[1], c_sp, c_st, c_sh, s_sp, s_st, s_sh)
 
 
 def _kv4_rows(entry: str, k, v, slots, cache, stream) -> None:
-    if k.dim() != 3 or k.shape != v.shape or k.dtype != v.dtype or k.dtype not in _DTYPES:
+    shape, dt = k.shape, _DTYPES.get(k.dtype)
+    if len(shape) != 3 or shape != v.shape or k.dtype != v.dtype or dt is None:
         raise ValueError("k and v must be [T, heads, D] tensors of one type (bf16, fp16 or fp32)")
-    T, H, D = k.shape
-    if k.numel() > 0 and (k.stride(2) != 1 or v.stride(2) != 1):
+    T, H, D = shape
+    k_st, k_sh, k_in = k.stride()
+    v_st, v_sh, v_in = v.stride()
+    if (k_in != 1 or v_in != 1) and k.numel() > 0:
         raise ValueError("innermost dimensions must be contiguous")
     if _dev_i32(slots, "slots").numel() != T:
         raise ValueError("slots needs one entry per token")
     _check(getattr(load_library(), entry)(
-        k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1), _DTYPES[k.dtype], T, H, D,
-        slots.data_ptr(), *_kv4_args(cache, H, D), _stream(stream)))
+        k.data_ptr(), k_st, k_sh, v.data_ptr(), v_st, v_sh, dt, T, H, D, slots.data_ptr(),
+        *_kv4_args(cache, H, D), _stream(stream)))
 
 
 def fp8q_kv4_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache: Kv4Cache, stream=None) -> None:
@@ -534,30 +545,43 @@ def fp8q_kv4_attention(q: torch.Tensor, cache: Kv4Cache, block_table: torch.Tens
     b, T == B). causal: the last query of a sequence sees all its cached tokens, the one before it
     one less, ... lse [T, heads] fp32 receives the logarithm of each row's softmax sum.
     When the shape can use a workspace and none is given, one is taken from torch's allocator."""
-    if q.dim() != 3 or q.dtype not in (torch.bfloat16, torch.float16):
+    shape, dt = q.shape, _DTYPES.get(q.dtype, DTYPE_F32)
+    if len(shape) != 3 or dt == DTYPE_F32:
         raise ValueError("q must be a [T, heads, D] bf16 or fp16 tensor")
-    T, H, D = q.shape
-    if out.dtype != q.dtype or out.shape != q.shape:
+    T, H, D = shape
+    if out.dtype != q.dtype or out.shape != shape:
         raise ValueError("out must have q's shape and type")
-    if q.numel() > 0 and (q.stride(2) != 1 or out.stride(2) != 1):
+    q_st, q_sh, q_in = q.stride()
+    o_st, o_sh, o_in = out.stride()
+    if (q_in != 1 or o_in != 1) and q.numel() > 0:
         raise ValueError("innermost dimensions must be contiguous")
     B = _dev_i32(kv_lens, "kv_lens").numel()
-    if block_table.dtype != torch.int32 or not block_table.is_cuda or block_table.dim() != 2 \
-            or block_table.shape[0] != B or (block_table.numel() > 0 and block_table.stride(1) != 1):
-        raise ValueError("block_table must be a device int32 [B, max_pages] tensor with contiguous rows")
-    if q_indptr is not None and _dev_i32(q_indptr, "q_indptr").numel() != B + 1:
-        raise ValueError("q_indptr needs B + 1 entries")
-    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (T, H) or (H > 1 and lse.stride(1) != 1)):
-        raise ValueError("lse must be a float32 [T, heads] tensor with contiguous rows")
-    kv_heads, max_pages = cache.k.shape[2], block_table.shape[1]
+    if block_table.dtype != torch.int32 or not block_table.is_cuda or block_table.dim() != 2:
+        raise ValueError("block_table must be a device int32 [B, max_pages] tensor")
+    rows, max_pages = block_table.shape
+    table_sb, table_in = block_table.stride()
+    if rows != B or (table_in != 1 and max_pages > 1):
+        raise ValueError("block_table must have contiguous rows, one per sequence")
+    ip_ptr = lse_ptr = None
+    l_st = 0
+    if q_indptr is not None:
+        if _dev_i32(q_indptr, "q_indptr").numel() != B + 1:
+            raise ValueError("q_indptr needs B + 1 entries")
+        ip_ptr = q_indptr.data_ptr()
+    if lse is not None:
+        if lse.dtype != torch.float32 or lse.shape != (T, H) or (H > 1 and lse.stride(1) != 1):
+            raise ValueError("lse must be a float32 [T, heads] tensor with contiguous rows")
+        lse_ptr, l_st = lse.data_ptr(), lse.stride(0)
+    page, kv_heads = cache.k.shape[1:3]
+    args = _kv4_args(cache, kv_heads, D)
+    lib = load_library()
     if workspace is None:
-        workspace = _alloc_workspace(fp8q_kv4_attention_workspace_size(
-            q.dtype, B, T, H, kv_heads, D, max_pages * cache.k.shape[1]), q.device, stream)
-    _check(load_library().fp8q_kv4_attention(
-        q.data_ptr(), _DTYPES[q.dtype], q.stride(0), q.stride(1), *_kv4_args(cache, kv_heads, D),
-        block_table.data_ptr(), block_table.stride(0), max_pages, kv_lens.data_ptr(), _ptr(q_indptr),
-        out.data_ptr(), out.stride(0), out.stride(1), _ptr(lse), 0 if lse is None else lse.stride(0),
-        B, T, H, kv_heads, D, sm_scale, int(causal), _ptr(workspace),
+        workspace = _alloc_workspace(
+            lib.fp8q_kv4_attention_workspace_size(dt, B, T, H, kv_heads, D, max_pages * page), q.device, stream)
+    _check(lib.fp8q_kv4_attention(
+        q.data_ptr(), dt, q_st, q_sh, *args, block_table.data_ptr(), table_sb, max_pages, kv_lens.data_ptr(), ip_ptr,
+        out.data_ptr(), o_st, o_sh, lse_ptr, l_st, B, T, H, kv_heads, D, sm_scale, causal,
+        None if workspace is None else workspace.data_ptr(),
         0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)))
 
 

@@ -44,11 +44,10 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
-constexpr int kWaves = 4;
-constexpr int kThreads = 64 * kWaves;
 constexpr int kRows = 16;   // query rows of an item
 constexpr int kTile = 32;   // tokens of a wave's step
-constexpr int kStep = kTile * kWaves;  // tokens of a block's step
+constexpr int kWideWaves = 4;  // of a block of the wide kernel
+constexpr int kJoinWaves = 4;
 constexpr int kPadV = 16;   // elements between the V rows in LDS
 constexpr int kMinRun = 2;  // spans of a block's run at least
 constexpr float kLn2 = 0.6931471805599453f;
@@ -117,6 +116,7 @@ struct Plan {
 };
 
 // Inclusive sum over the block's threads; `lds` holds one value per wave.
+template <int WAVES>
 __device__ __forceinline__ long long block_scan(long long v, long long* lds, long long& total) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
@@ -128,7 +128,7 @@ __device__ __forceinline__ long long block_scan(long long v, long long* lds, lon
   __syncthreads();
   total = 0;
 #pragma unroll
-  for (int w = 0; w < kWaves; w++) {
+  for (int w = 0; w < WAVES; w++) {
     if (w < wave) v += lds[w];
     total += lds[w];
   }
@@ -137,9 +137,10 @@ __device__ __forceinline__ long long block_scan(long long v, long long* lds, lon
 
 // Fills the plan in LDS; every block computes the same from the lengths. A q_indptr that does
 // not ascend can name more rows than there are: then the plan is empty and nothing is run.
-template <int ROWS>
+template <int ROWS, int WAVES>
 __device__ __forceinline__ void make_plan(const Kv4AttnParams& p, const Plan& plan) {
-  __shared__ long long tot_line[kWaves], tot_first[kWaves];
+  constexpr int kThreads = 64 * WAVES;
+  __shared__ long long tot_line[WAVES], tot_first[WAVES];
   const int tid = threadIdx.x;
   const int32_t B = static_cast<int32_t>(p.B);
   const int32_t per = (B + kThreads - 1) / kThreads;
@@ -152,8 +153,8 @@ __device__ __forceinline__ void make_plan(const Kv4AttnParams& p, const Plan& pl
     my_line += tiles * spans_of(p, s);
   }
   long long all_line, all_first;
-  long long at_first = block_scan(my_first, tot_first, all_first) - my_first;
-  long long at_line = block_scan(my_line, tot_line, all_line) - my_line;
+  long long at_first = block_scan<WAVES>(my_first, tot_first, all_first) - my_first;
+  long long at_line = block_scan<WAVES>(my_line, tot_line, all_line) - my_line;
   const bool fits = all_first * p.Hkv <= p.max_units;
   for (int32_t b = beg; b < end; b++) {
     const Seq s = sequence(p, b);
@@ -197,7 +198,7 @@ struct Work {
 
 // A block's places [at, stop) on the line: of spans when splitting, else of units in steps of the
 // grid. `direct`: one unit per sequence and cached head, in order, so that no plan is needed.
-template <int ROWS, bool SPLIT>
+template <int ROWS, int WAVES, bool SPLIT>
 struct Walk {
   const Kv4AttnParams& p;
   const Plan plan;
@@ -208,13 +209,13 @@ struct Walk {
       : p(params), plan{lds, lds + params.B + 1},
         direct(!SPLIT && params.q_indptr == nullptr && params.group <= ROWS) {
     const int32_t B = static_cast<int32_t>(p.B);
-    if (!direct) make_plan<ROWS>(p, plan);
+    if (!direct) make_plan<ROWS, WAVES>(p, plan);
     if constexpr (SPLIT) {
       const int32_t total = uniform(plan.line[B]) * p.Hkv, run = run_length(total, p.blocks);
       at = static_cast<int32_t>(min(static_cast<int64_t>(blockIdx.x) * run, static_cast<int64_t>(total)));
       stop = at + min(run, total - at);
       if (blockIdx.x == 0) {  // for the join
-        for (int32_t b = threadIdx.x; b <= B; b += kThreads) {
+        for (int32_t b = threadIdx.x; b <= B; b += 64 * WAVES) {
           p.plan[b] = plan.line[b];
           p.plan[B + 1 + b] = plan.first[b];
         }
@@ -437,22 +438,23 @@ __device__ __forceinline__ void split8(u32x4 raw, uint32_t sign, bf16x8 (&out)[P
 }
 
 // Waves per SIMD that the registers are kept to (O^T and Q take D / 4 + D / 8 of them per lane).
-constexpr int waves_per_simd(int D, int DT) { return D == 256 ? 2 : DT == FP8Q_DTYPE_F16 && D == 128 ? 3 : 4; }
+constexpr int waves_per_simd(int64_t D, int DT) { return D == 256 ? 2 : DT == FP8Q_DTYPE_F16 && D == 128 ? 3 : 4; }
 
-template <int D, int DT, bool SPLIT, bool PAGE16>
-__global__ __launch_bounds__(kThreads, waves_per_simd(D, DT)) void kv4_attention_kernel(Kv4AttnParams p) {
+template <int D, int DT, int WAVES, bool SPLIT, bool PAGE16>
+__global__ __launch_bounds__(64 * WAVES, waves_per_simd(D, DT)) void kv4_attention_kernel(Kv4AttnParams p) {
   constexpr int PARTS = DT == FP8Q_DTYPE_F16 ? 2 : 1;
+  constexpr int kStep = kTile * WAVES;  // tokens of the block's step
   constexpr int kSteps = D / 32;   // contraction steps of S^T
   constexpr int kDims = D / 16;    // dim tiles of O^T
   constexpr int kRowV = D + kPadV;  // LDS row of V (bf16 elements)
   constexpr int kRowO = D + 4;      // LDS row of the joined output (floats)
   static_assert(kRows * kRowO * 4 <= kTile * kRowV * 2, "the joined output reuses V's LDS");
-  __shared__ __align__(16) uint16_t lds_v[kWaves][kTile * kRowV];
-  __shared__ float lds_m[kWaves][kRows], lds_l[kWaves][kRows];
+  __shared__ __align__(16) uint16_t lds_v[WAVES][kTile * kRowV];
+  __shared__ float lds_m[WAVES][kRows], lds_l[WAVES][kRows];
   extern __shared__ int32_t lds_plan[];
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_index();
   const int r = lane & 15, h = lane >> 4;
-  Walk<kRows, SPLIT> walk(p, lds_plan);
+  Walk<kRows, WAVES, SPLIT> walk(p, lds_plan);
   Work w;
   while (walk.next(w)) {
     const Seq seq = w.seq;
@@ -584,7 +586,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, DT)) void kv4_attention
     __syncthreads();
     float top = kNegInf;
 #pragma unroll
-    for (int n = 0; n < kWaves; n++) top = fmaxf(top, lds_m[n][r]);
+    for (int n = 0; n < WAVES; n++) top = fmaxf(top, lds_m[n][r]);
     {
       const float f = exp2_fast(m - (top == kNegInf ? 0.0f : top));
       float* dst = reinterpret_cast<float*>(vt) + r * kRowO + 4 * h;
@@ -592,7 +594,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, DT)) void kv4_attention
       for (int d = 0; d < kDims; d++) *reinterpret_cast<f32x4*>(dst + 16 * d) = o[d] * f;
     }
     __syncthreads();
-    for (int e = tid; e < kRows * (D / 8); e += kThreads) {
+    for (int e = tid; e < kRows * (D / 8); e += 64 * WAVES) {
       const int row = e / (D / 8), col = e % (D / 8) * 8;
       if (first + row > last) continue;
       float v[8];
@@ -600,14 +602,14 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, DT)) void kv4_attention
       for (int i = 0; i < 8; i++) v[i] = 0.0f;
       float mm = kNegInf, ll = 0.0f;
 #pragma unroll
-      for (int n = 0; n < kWaves; n++) {
+      for (int n = 0; n < WAVES; n++) {
         const float* src = reinterpret_cast<const float*>(lds_v[n]) + row * kRowO + col;
 #pragma unroll
         for (int i = 0; i < 8; i++) v[i] += src[i];
         mm = fmaxf(mm, lds_m[n][row]);
       }
 #pragma unroll
-      for (int n = 0; n < kWaves; n++) ll += lds_l[n][row] * exp2_fast(lds_m[n][row] - (mm == kNegInf ? 0.0f : mm));
+      for (int n = 0; n < WAVES; n++) ll += lds_l[n][row] * exp2_fast(lds_m[n][row] - (mm == kNegInf ? 0.0f : mm));
       if (SPLIT && !w.whole) {
         float* part = p.parts + static_cast<int64_t>(w.piece) * (kRows * (D + 2));
 #pragma unroll
@@ -641,17 +643,17 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, DT)) void kv4_attention
 constexpr int kStepW = 64;
 
 template <int D, int DT, int QT, bool SPLIT, bool PAGE16>
-__global__ __launch_bounds__(kThreads, 2) void kv4_attention_wide_kernel(Kv4AttnParams p) {
+__global__ __launch_bounds__(64 * kWideWaves, 2) void kv4_attention_wide_kernel(Kv4AttnParams p) {
   constexpr int PARTS = DT == FP8Q_DTYPE_F16 ? 2 : 1;
   constexpr int kSteps = D / 32, kDims = D / 16, kRowV = D + kPadV;
   constexpr int kHalves = kStepW / 16;
-  constexpr int ROWS = 16 * QT * kWaves;
-  static_assert(kHalves == kWaves, "every wave converts 16 tokens of V");
+  constexpr int ROWS = 16 * QT * kWideWaves;
+  static_assert(kHalves == kWideWaves, "every wave converts 16 tokens of V");
   __shared__ __align__(16) uint16_t lds_v[2][kStepW * kRowV];
   extern __shared__ int32_t lds_plan[];
   const int lane = threadIdx.x & 63, wave = wave_index();
   const int r = lane & 15, h = lane >> 4;
-  Walk<ROWS, SPLIT> walk(p, lds_plan);
+  Walk<ROWS, kWideWaves, SPLIT> walk(p, lds_plan);
   Work w;
   while (walk.next(w)) {
     const Seq seq = w.seq;
@@ -853,12 +855,12 @@ __global__ __launch_bounds__(kThreads, 2) void kv4_attention_wide_kernel(Kv4Attn
 // Joins the pieces of query rows, WAVES waves for each: they take the pieces in turn, every
 // lane D / 64 elements.
 template <int D, int DT, int ROWS, int WAVES>
-__global__ __launch_bounds__(kThreads) void kv4_join_kernel(Kv4AttnParams p) {
+__global__ __launch_bounds__(64 * kJoinWaves) void kv4_join_kernel(Kv4AttnParams p) {
   constexpr int kPer = D / 64;
   constexpr int kStepF = ROWS * (D + 2);  // floats of a piece
   __shared__ float lds_o[WAVES][D], lds_l[WAVES];
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_index();
-  const int32_t row = blockIdx.x * (kWaves / WAVES) + (WAVES == 1 ? wave : 0);  // of T * Hq
+  const int32_t row = blockIdx.x * (kJoinWaves / WAVES) + (WAVES == 1 ? wave : 0);  // of T * Hq
   if (row >= static_cast<int32_t>(p.T) * p.Hq) return;
   const int32_t t = row / p.Hq, qh = row - t * p.Hq;
   int32_t b = t;
@@ -936,6 +938,11 @@ int tile_rows(int dtype, int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t 
   return rows <= 2 * kRows ? kRows : rows <= 64 ? 64 : widest(dtype, D);
 }
 
+// Waves of the narrow kernel's blocks, and the blocks that a CU holds: 8 waves (fewer pieces to
+// join than with 4) where two such blocks fit its registers and LDS.
+constexpr int narrow_waves(int DT, int64_t D) { return D == 256 || waves_per_simd(D, DT) < 4 ? 4 : 8; }
+constexpr int narrow_blocks(int DT, int64_t D) { return waves_per_simd(D, DT) * 4 / narrow_waves(DT, D); }
+
 struct Shape {
   int rows;        // of a tile
   int64_t units;   // at most
@@ -949,7 +956,7 @@ Shape shape_of(int dtype, int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t
   s.rows = tile_rows(dtype, B, T, Hq, Hkv, D);
   s.units = Hkv * ((T * (Hq / Hkv) + s.rows - 1) / s.rows + B);
   const bool narrow = s.rows == kRows;
-  s.blocks = static_cast<int64_t>(current_device_shape().cus) * (narrow ? 4 : 2);
+  s.blocks = static_cast<int64_t>(current_device_shape().cus) * (narrow ? narrow_blocks(dtype, D) : 2);
   // spans of 128 tokens, or longer ones where the line could have 2^31 places
   s.span_shift = 7;
   while (s.units * ((max_tokens >> s.span_shift) + 1) >= (int64_t(1) << 31)) s.span_shift++;
@@ -972,19 +979,20 @@ struct Launch {
   void run() const {
     const size_t lds = 2 * (p.B + 1) * sizeof(int32_t);
     if constexpr (ROWS == kRows)
-      hipLaunchKernelGGL((kv4_attention_kernel<D, DT, SPLIT, PAGE16>), dim3(grid), dim3(kThreads), lds, stream, p);
+      hipLaunchKernelGGL((kv4_attention_kernel<D, DT, narrow_waves(DT, D), SPLIT, PAGE16>), dim3(grid),
+                         dim3(64 * narrow_waves(DT, D)), lds, stream, p);
     else
-      hipLaunchKernelGGL((kv4_attention_wide_kernel<D, DT, ROWS / 64, SPLIT, PAGE16>), dim3(grid), dim3(kThreads), lds,
-                         stream, p);
+      hipLaunchKernelGGL((kv4_attention_wide_kernel<D, DT, ROWS / 64, SPLIT, PAGE16>), dim3(grid),
+                         dim3(64 * kWideWaves), lds, stream, p);
     if constexpr (SPLIT) {
       const int64_t rows = p.T * p.Hq;
       // a wave per row, or where the units are cut into many pieces a block
       if (shape.blocks < 8 * shape.units)
-        hipLaunchKernelGGL((kv4_join_kernel<D, DT, ROWS, 1>), dim3(static_cast<unsigned>((rows + kWaves - 1) / kWaves)),
-                           dim3(kThreads), 0, stream, p);
+        hipLaunchKernelGGL((kv4_join_kernel<D, DT, ROWS, 1>), dim3(static_cast<unsigned>((rows + kJoinWaves - 1) / kJoinWaves)),
+                           dim3(64 * kJoinWaves), 0, stream, p);
       else
-        hipLaunchKernelGGL((kv4_join_kernel<D, DT, ROWS, kWaves>), dim3(static_cast<unsigned>(rows)), dim3(kThreads), 0,
-                           stream, p);
+        hipLaunchKernelGGL((kv4_join_kernel<D, DT, ROWS, kJoinWaves>), dim3(static_cast<unsigned>(rows)),
+                           dim3(64 * kJoinWaves), 0, stream, p);
     }
   }
   template <int D, int DT, int ROWS>
