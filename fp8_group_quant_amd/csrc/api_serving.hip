@@ -91,6 +91,7 @@ int norm_entry(const void* x, int in_dtype, int64_t M, int64_t K, int64_t x_sm, 
   p.eps = eps;
   p.inv_k = 1.0f / static_cast<float>(K);
   p.group = grouped ? group_size : 0;
+  p.group_shift = group_size == 32 ? 5 : group_size == 64 ? 6 : group_size == 128 ? 7 : 30;
   p.ue8m0 = scale_fmt != FP8Q_SCALE_F32;
   p.packed = packed;
   return launch_rms_norm_quant(in_dtype, p, static_cast<hipStream_t>(stream));
@@ -182,6 +183,7 @@ int rows_entry(bool write, const void* k, int64_t k_st, int64_t k_sh, const void
   p.T = T;
   p.H = static_cast<int32_t>(H);
   p.D = static_cast<int32_t>(D);
+  p.d_shift = log2_exact(D);
   const hipStream_t st = static_cast<hipStream_t>(stream);
   return write ? launch_kv4_write(dtype, p, st) : launch_kv4_read(dtype, p, st);
 }

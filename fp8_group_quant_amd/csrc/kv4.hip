@@ -7,7 +7,9 @@
 // element saturates: the rounding to e2m1 (nearest, ties to even) is the only one.
 //
 // Both directions are bound by HBM traffic: 2 bytes per element on the model's side (bf16),
-// 0.53 on the cache's. A lane owns 16 consecutive elements (half a scale block).
+// 0.53 on the cache's. A lane owns 8 consecutive elements (a quarter of a scale block) of 4
+// tokens in a row: 16 bytes per lane and access on the model's side, next to the neighbour's,
+// and the index arithmetic is done once for the four.
 #include <algorithm>
 
 #include "quant_device.h"
@@ -20,8 +22,30 @@ namespace fp8q {
 namespace {
 
 constexpr int kThreads = 256;
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+constexpr int kEl = 8;   // elements of a lane
+constexpr int kTok = 4;  // tokens of a lane
 typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+
+// Division of u < 2^30 by a constant d: (mulhi(u, mul) + u) >> shift with shift = ceil(log2 d)
+// and mul = floor(2^32 (2^shift - d) / d) + 1 (Granlund and Montgomery, "Division by invariant
+// integers using multiplication", PLDI'94).
+struct Divider {
+  uint32_t mul, shift;
+};
+Divider divider(uint32_t d) {
+  uint32_t s = 0;
+  while ((uint64_t(1) << s) < d) s++;
+  return Divider{static_cast<uint32_t>((((uint64_t(1) << s) - d) << 32) / d + 1), s};
+}
+__device__ __forceinline__ uint32_t divide(uint32_t u, Divider d) { return (__umulhi(u, d.mul) + u) >> d.shift; }
+
+struct Grid {
+  uint32_t units, per;  // lanes with work per tensor; those of one group of tokens
+  Divider by_per;
+};
 
 // Biased exponent of the smallest power of two >= amax / 6 for a normal amax = m * 2^e with m
 // in [1, 2): 6 * 2^(e - 2) = 1.5 * 2^e reaches amax when m <= 1.5, else one exponent more.
@@ -30,105 +54,198 @@ __device__ __forceinline__ uint32_t e2m1_scale_byte(float amax) {
   return (bits >> 23) - 2u + ((bits & 0x7FFFFFu) > 0x400000u ? 1u : 0u);
 }
 
-// Byte offset of row (slot, head) in a cached tensor; slot is in [0, pages << page_shift).
-__device__ __forceinline__ int64_t row_at(const Kv4Cache& c, int32_t slot, int32_t head, int64_t sp, int64_t st,
-                                          int64_t sh) {
-  const int32_t page = slot >> c.page_shift, tok = slot & ((1 << c.page_shift) - 1);
-  return page * sp + tok * st + head * sh;
-}
-
+// The 8 elements of a lane, as stored.
 template <int DT>
-__global__ __launch_bounds__(kThreads) void kv4_write_kernel(Kv4RowsParams p, uint32_t units, uint32_t per_token) {
-  const uint32_t u = blockIdx.x * kThreads + threadIdx.x;  // 16 elements of one row
-  const int which = blockIdx.y;                            // keys, values
-  if (u >= units) return;
-  const uint32_t t = u / per_token, rest = u - t * per_token;
-  const int32_t el = static_cast<int32_t>(rest) * kPerLane;
-  const int32_t head = el / p.D, d = el - head * p.D;
-  const int32_t slot = p.slots[t];
-  // slots outside the cache (a padding token's -1) are skipped; both lanes of a block agree
-  if (slot < 0 || slot >= (p.c.pages << p.c.page_shift)) return;
-  Raw16<DT> raw;
-  load_raw<DT>(p.x[which], t * p.x_st[which] + head * p.x_sh[which] + d, raw);
-  float v[16];
-  widen<DT>(raw, v);
-  float amax = kEps;
-#pragma unroll
-  for (int j = 0; j < 16; j++) amax = fmaxf(amax, fabsf(v[j]));
-  amax = fmaxf(amax, dpp<0xB1>(amax));  // the block's other half
-  const uint32_t byte = e2m1_scale_byte(amax);
-  const float scale = __uint_as_float(byte << 23);
-  u32x2 w = {0u, 0u};
-#pragma unroll
-  for (int j = 0; j < 2; j++) {
-    w[j] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w[j], v[8 * j], v[8 * j + 1], scale, 0);
-    w[j] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w[j], v[8 * j + 2], v[8 * j + 3], scale, 1);
-    w[j] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w[j], v[8 * j + 4], v[8 * j + 5], scale, 2);
-    w[j] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w[j], v[8 * j + 6], v[8 * j + 7], scale, 3);
-  }
-  uint8_t* codes = (which ? p.c.v : p.c.k) + row_at(p.c, slot, head, p.c.c_sp, p.c.c_st, p.c.c_sh);
-  *reinterpret_cast<u32x2*>(codes + d / 2) = w;
-  if ((d & 16) == 0) {
-    uint8_t* scales = (which ? p.c.vs : p.c.ks) + row_at(p.c, slot, head, p.c.s_sp, p.c.s_st, p.c.s_sh);
-    scales[d / kKv4Block] = static_cast<uint8_t>(byte);
-  }
-}
+struct Raw8 {
+  u32x4 w[DT == FP8Q_DTYPE_F32 ? 2 : 1];
+};
 
+// Largest magnitude of the 8. bf16 and fp16 magnitudes order like their bits.
 template <int DT>
-__global__ __launch_bounds__(kThreads) void kv4_read_kernel(Kv4RowsParams p, uint32_t units, uint32_t per_token) {
-  const uint32_t u = blockIdx.x * kThreads + threadIdx.x;
-  const int which = blockIdx.y;
-  if (u >= units) return;
-  const uint32_t t = u / per_token, rest = u - t * per_token;
-  const int32_t el = static_cast<int32_t>(rest) * kPerLane;
-  const int32_t head = el / p.D, d = el - head * p.D;
-  const int32_t slot = p.slots[t];
-  float v[16];
-  if (slot < 0 || slot >= (p.c.pages << p.c.page_shift)) {  // no such row: zeros
+__device__ __forceinline__ float amax8(const Raw8<DT>& r) {
+  if constexpr (DT == FP8Q_DTYPE_F32) {
+    float a = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 16; j++) v[j] = 0.0f;
+    for (int i = 0; i < 8; i++) a = fmaxf(a, fabsf(__uint_as_float(r.w[i >> 2][i & 3])));
+    return a;
   } else {
-    const uint8_t* codes = (which ? p.c.v : p.c.k) + row_at(p.c, slot, head, p.c.c_sp, p.c.c_st, p.c.c_sh);
-    const uint8_t* scales = (which ? p.c.vs : p.c.ks) + row_at(p.c, slot, head, p.c.s_sp, p.c.s_st, p.c.s_sh);
-    const u32x2 w = *reinterpret_cast<const u32x2*>(codes + d / 2);
-    const float scale = __uint_as_float(static_cast<uint32_t>(scales[d / kKv4Block]) << 23);
+    u16x2 a = __builtin_bit_cast(u16x2, r.w[0][0] & 0x7FFF7FFFu);
 #pragma unroll
-    for (int j = 0; j < 2; j++) {
-      const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[j], scale, 0);
-      const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[j], scale, 1);
-      const f32x2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[j], scale, 2);
-      const f32x2 e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[j], scale, 3);
-      v[8 * j] = a.x; v[8 * j + 1] = a.y; v[8 * j + 2] = b.x; v[8 * j + 3] = b.y;
-      v[8 * j + 4] = c.x; v[8 * j + 5] = c.y; v[8 * j + 6] = e.x; v[8 * j + 7] = e.y;
+    for (int i = 1; i < 4; i++)
+      a = __builtin_elementwise_max(a, __builtin_bit_cast(u16x2, r.w[0][i] & 0x7FFF7FFFu));
+    const uint32_t top = max(static_cast<uint32_t>(a[0]), static_cast<uint32_t>(a[1]));
+    return DT == FP8Q_DTYPE_BF16 ? bf16_lo(top) : f16_lo(top);
+  }
+}
+
+// A word as a pair of 16-bit floats. (A function: a bit cast of a vector's element itself takes
+// the vector's first one.)
+template <typename T>
+__device__ __forceinline__ T pair(uint32_t w) { return __builtin_bit_cast(T, w); }
+
+// The 8 codes at this scale.
+template <int DT>
+__device__ __forceinline__ uint32_t encode8(const Raw8<DT>& r, float scale) {
+  uint32_t c = 0;
+  if constexpr (DT == FP8Q_DTYPE_BF16) {
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, pair<bf16x2>(r.w[0][0]), scale, 0);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, pair<bf16x2>(r.w[0][1]), scale, 1);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, pair<bf16x2>(r.w[0][2]), scale, 2);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, pair<bf16x2>(r.w[0][3]), scale, 3);
+  } else if constexpr (DT == FP8Q_DTYPE_F16) {
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(c, pair<f16x2>(r.w[0][0]), scale, 0);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(c, pair<f16x2>(r.w[0][1]), scale, 1);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(c, pair<f16x2>(r.w[0][2]), scale, 2);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(c, pair<f16x2>(r.w[0][3]), scale, 3);
+  } else {
+    auto f = [&](int i) { return __uint_as_float(r.w[i >> 2][i & 3]); };
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, f(0), f(1), scale, 0);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, f(2), f(3), scale, 1);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, f(4), f(5), scale, 2);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, f(6), f(7), scale, 3);
+  }
+  return c;
+}
+
+// The values of 8 codes. Exact in bf16 and fp32; fp16 is rounded from the exact value.
+template <int DT>
+__device__ __forceinline__ Raw8<DT> decode8(uint32_t c, float scale) {
+  Raw8<DT> r;
+  if constexpr (DT == FP8Q_DTYPE_BF16) {
+    r.w[0][0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 0));
+    r.w[0][1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 1));
+    r.w[0][2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 2));
+    r.w[0][3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 3));
+  } else {
+    const f32x2 v[4] = {__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, scale, 0), __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, scale, 1),
+                        __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, scale, 2), __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, scale, 3)};
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      if constexpr (DT == FP8Q_DTYPE_F16) {
+        r.w[0][i] = pack16<DT>(v[i].x, v[i].y);
+      } else {
+        r.w[i >> 1][2 * (i & 1)] = __float_as_uint(v[i].x);
+        r.w[i >> 1][2 * (i & 1) + 1] = __float_as_uint(v[i].y);
+      }
     }
   }
-  store16<DT>(p.x[which], t * p.x_st[which] + head * p.x_sh[which] + d, v);
+  return r;
 }
 
-// Calls `one` with token ranges whose 16-element units count at most 2^30 (one launch for any
-// call of up to 2^34 elements per tensor).
+// Where a lane's elements lie: the first of its tokens, head and element of the row.
+struct Place {
+  int32_t t, head, d;
+};
+__device__ __forceinline__ Place place_of(const Kv4RowsParams& p, const Grid& g, uint32_t u) {
+  const uint32_t group = divide(u, g.by_per), el = (u - group * g.per) * kEl;
+  return Place{static_cast<int32_t>(group) * kTok, static_cast<int32_t>(el >> p.d_shift),
+               static_cast<int32_t>(el & ((1u << p.d_shift) - 1u))};
+}
+
+// Slots of the lane's tokens, -1 for one that is not there or lies outside the cache.
+__device__ __forceinline__ void slots_of(const Kv4RowsParams& p, int32_t t, int32_t (&slot)[kTok]) {
+#pragma unroll
+  for (int i = 0; i < kTok; i++) {
+    slot[i] = t + i < p.T ? p.slots[t + i] : -1;
+    if (slot[i] >= (p.c.pages << p.c.page_shift)) slot[i] = -1;
+  }
+}
+
+template <int DT>
+__global__ __launch_bounds__(kThreads) void kv4_write_kernel(Kv4RowsParams p, Grid g) {
+  constexpr int kEsz = DT == FP8Q_DTYPE_F32 ? 4 : 2;
+  const uint32_t u = blockIdx.x * kThreads + threadIdx.x;
+  const int which = blockIdx.y;  // keys, values
+  if (u >= g.units) return;
+  const Place at = place_of(p, g, u);
+  const uint8_t* x = static_cast<const uint8_t*>(p.x[which]) + (at.t * p.x_st[which] + at.head * p.x_sh[which] + at.d) * kEsz;
+  int32_t slot[kTok];
+  slots_of(p, at.t, slot);
+  Raw8<DT> raw[kTok];
+#pragma unroll
+  for (int i = 0; i < kTok; i++) {
+#pragma unroll
+    for (int j = 0; j < kEsz / 2; j++) {
+      raw[i].w[j] = u32x4{0u, 0u, 0u, 0u};
+      if (slot[i] >= 0) raw[i].w[j] = reinterpret_cast<const u32x4*>(x + i * p.x_st[which] * kEsz)[j];
+    }
+  }
+  uint8_t* codes = (which ? p.c.v : p.c.k) + at.head * p.c.c_sh + at.d / 2;
+  uint8_t* scales = (which ? p.c.vs : p.c.ks) + at.head * p.c.s_sh + at.d / kKv4Block;
+  const int32_t mask = (1 << p.c.page_shift) - 1;
+#pragma unroll
+  for (int i = 0; i < kTok; i++) {
+    // a scale block's four lanes are neighbours in a quad and have the same token
+    float amax = amax8<DT>(raw[i]);
+    amax = fmaxf(amax, dpp<0xB1>(amax));
+    amax = fmaxf(amax, dpp<0x4E>(amax));
+    const uint32_t byte = e2m1_scale_byte(fmaxf(amax, kEps));
+    const uint32_t c = encode8<DT>(raw[i], __uint_as_float(byte << 23));
+    if (slot[i] >= 0) {
+      const int64_t page = slot[i] >> p.c.page_shift, tok = slot[i] & mask;
+      *reinterpret_cast<uint32_t*>(codes + page * p.c.c_sp + tok * p.c.c_st) = c;
+      if ((at.d & (kKv4Block - 1)) == 0) scales[page * p.c.s_sp + tok * p.c.s_st] = static_cast<uint8_t>(byte);
+    }
+  }
+}
+
+template <int DT>
+__global__ __launch_bounds__(kThreads) void kv4_read_kernel(Kv4RowsParams p, Grid g) {
+  constexpr int kEsz = DT == FP8Q_DTYPE_F32 ? 4 : 2;
+  const uint32_t u = blockIdx.x * kThreads + threadIdx.x;
+  const int which = blockIdx.y;
+  if (u >= g.units) return;
+  const Place at = place_of(p, g, u);
+  int32_t slot[kTok];
+  slots_of(p, at.t, slot);
+  const uint8_t* codes = (which ? p.c.v : p.c.k) + at.head * p.c.c_sh + at.d / 2;
+  const uint8_t* scales = (which ? p.c.vs : p.c.ks) + at.head * p.c.s_sh + at.d / kKv4Block;
+  const int32_t mask = (1 << p.c.page_shift) - 1;
+  uint32_t c[kTok], byte[kTok];
+#pragma unroll
+  for (int i = 0; i < kTok; i++) {
+    c[i] = 0;  // a slot outside the cache: zeros
+    byte[i] = 127;
+    if (slot[i] >= 0) {
+      const int64_t page = slot[i] >> p.c.page_shift, tok = slot[i] & mask;
+      c[i] = *reinterpret_cast<const uint32_t*>(codes + page * p.c.c_sp + tok * p.c.c_st);
+      byte[i] = scales[page * p.c.s_sp + tok * p.c.s_st];
+    }
+  }
+  uint8_t* x = static_cast<uint8_t*>(p.x[which]) + (at.t * p.x_st[which] + at.head * p.x_sh[which] + at.d) * kEsz;
+#pragma unroll
+  for (int i = 0; i < kTok; i++) {
+    if (at.t + i >= p.T) break;
+    const Raw8<DT> r = decode8<DT>(c[i], __uint_as_float(byte[i] << 23));
+#pragma unroll
+    for (int j = 0; j < kEsz / 2; j++) reinterpret_cast<u32x4*>(x + i * p.x_st[which] * kEsz)[j] = r.w[j];
+  }
+}
+
+// Calls `one` with token ranges whose lanes count at most 2^30 (one launch for any call of up
+// to 2^35 elements per tensor).
 template <typename F>
 void by_ranges(const Kv4RowsParams& p, int esz, F one) {
-  const int64_t per_token = static_cast<int64_t>(p.H) * p.D / kPerLane;
-  const int64_t most = std::max<int64_t>(1, (int64_t(1) << 30) / per_token);
+  const int64_t per = static_cast<int64_t>(p.H) * p.D / kEl;
+  const int64_t most = std::max<int64_t>(1, (int64_t(1) << 30) / per) * kTok;
   for (int64_t t = 0; t < p.T; t += most) {
     Kv4RowsParams r = p;
     r.T = std::min(most, p.T - t);
     r.slots = p.slots + t;
     for (int i = 0; i < 2; i++) r.x[i] = static_cast<uint8_t*>(p.x[i]) + t * p.x_st[i] * esz;
-    const int64_t units = r.T * per_token;
-    one(r, dim3(static_cast<unsigned>((units + kThreads - 1) / kThreads), 2), static_cast<uint32_t>(units),
-        static_cast<uint32_t>(per_token));
+    const Grid g{static_cast<uint32_t>((r.T + kTok - 1) / kTok * per), static_cast<uint32_t>(per),
+                 divider(static_cast<uint32_t>(per))};
+    one(r, dim3((g.units + kThreads - 1) / kThreads, 2), g);
   }
 }
 
 template <int DT>
 void launch_rows(bool write, const Kv4RowsParams& p, hipStream_t stream) {
-  by_ranges(p, DT == FP8Q_DTYPE_F32 ? 4 : 2, [&](const Kv4RowsParams& r, dim3 grid, uint32_t units, uint32_t per_token) {
+  by_ranges(p, DT == FP8Q_DTYPE_F32 ? 4 : 2, [&](const Kv4RowsParams& r, dim3 grid, const Grid& g) {
     if (write)
-      hipLaunchKernelGGL((kv4_write_kernel<DT>), grid, dim3(kThreads), 0, stream, r, units, per_token);
+      hipLaunchKernelGGL((kv4_write_kernel<DT>), grid, dim3(kThreads), 0, stream, r, g);
     else
-      hipLaunchKernelGGL((kv4_read_kernel<DT>), grid, dim3(kThreads), 0, stream, r, units, per_token);
+      hipLaunchKernelGGL((kv4_read_kernel<DT>), grid, dim3(kThreads), 0, stream, r, g);
   });
 }
 

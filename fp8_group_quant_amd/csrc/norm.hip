@@ -20,40 +20,60 @@
 namespace fp8q {
 namespace {
 
-// Sum over all 64 lanes, returned wave-uniform (the steps of wave_max).
-__device__ __forceinline__ float wave_sum(float v) {
-  v = v + dpp<0xB1>(v);
-  v = v + dpp<0x4E>(v);
-  v = v + dpp<0x141>(v);
-  v = v + dpp<0x140>(v);
+// Reductions over the LANES (16 or 64) lanes that share a row, or a wave's part of one: the steps
+// of group_max within 16 lanes, then the wave's four rows of lanes through readlane.
+template <int LANES, typename F>
+__device__ __forceinline__ float row_reduce(float v, F f) {
+  v = f(v, dpp<0xB1>(v));
+  v = f(v, dpp<0x4E>(v));
+  v = f(v, dpp<0x141>(v));
+  v = f(v, dpp<0x140>(v));
+  if constexpr (LANES == 16) return v;
   const float r0 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 0));
   const float r1 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 16));
   const float r2 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 32));
   const float r3 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 48));
-  return (r0 + r1) + (r2 + r3);
+  return f(f(r0, r1), f(r2, r3));
+}
+__device__ __forceinline__ float add(float a, float b) { return a + b; }
+__device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
+
+// 16 values times their groups' multiplier as e4m3 codes. Nothing is clamped: the scale is amax / 448
+// or more up to its rounding and the multiplier's, so a product stays below 448 * (1 + 2^-21),
+// which rounds to 448 (from 464 on it would not).
+__device__ __forceinline__ u32x4 encode16_below448(const float (&v)[16], float inv) {
+  u32x4 w;
+#pragma unroll
+  for (int q = 0; q < 4; q++)
+    w[q] = cvt4(v[4 * q] * inv, v[4 * q + 1] * inv, v[4 * q + 2] * inv, v[4 * q + 3] * inv);
+  return w;
 }
 
-// WPR waves share a row, each holding CH chunks of 1024 elements (wave w: chunks w, w + WPR,
-// ...). Fewer than 4 waves to a row: a block of 4 waves takes several rows.
-template <int DT, int WPR, int CH>
+// LANES lanes of each of WPR waves share a row (64, or 16 of one wave), each lane holding CH times
+// 16 elements: lane and wave i take the elements [16 i, 16 i + 16) of every 16 * LANES * WPR.
+template <int DT, int LANES, int WPR, int CH>
 __global__ __launch_bounds__(WPR < 4 ? 256 : 64 * WPR) void rms_norm_quant_kernel(NormParams p) {
-  constexpr int kRows = WPR < 4 ? 4 / WPR : 1;
-  __shared__ float part[2][2][kRows][WPR];  // by iteration parity: sums of squares, maxima
+  static_assert(LANES == 64 || WPR == 1, "a row of 16 lanes is one wave's");
+  constexpr int kWaves = WPR < 4 ? 4 : WPR;
+  constexpr int kRows = kWaves / WPR * (64 / LANES);  // of a block
+  constexpr int kPass = LANES * WPR * kPerLane;       // elements of a row that its lanes hold at a time
+  __shared__ float part[2][2][kWaves / WPR][WPR];  // by iteration parity: sums of squares, maxima
   const int lane = threadIdx.x & 63;
   const int wave = wave_index();
   const int wr = wave / WPR, wi = wave % WPR;
+  const int at = (LANES == 64 ? wi * 64 + lane : lane & 15) * kPerLane;
   int par = 0;
   for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * kRows; row0 < p.M;
        row0 += static_cast<int64_t>(gridDim.x) * kRows, par ^= 1) {
-    const int64_t m = row0 + wr;
-    const bool live = m < p.M;  // wave-uniform
+    const int64_t m = row0 + (LANES == 64 ? wr : wave * 4 + (lane >> 4));
+    const bool live = m < p.M;
     Raw16<DT> xr[CH], rr[CH], gr[CH];
 #pragma unroll
     for (int i = 0; i < CH; i++) {
       zero_raw<DT>(xr[i]);
       zero_raw<DT>(rr[i]);
       zero_raw<DT>(gr[i]);
-      const int64_t k = static_cast<int64_t>(wi + WPR * i) * kChunk + lane * kPerLane;
+      const int32_t k = at + kPass * i;
       if (live && k < p.K) {
         load_raw<DT>(p.x, m * p.x_sm + k, xr[i]);
         if (p.res) load_raw<DT>(p.res, m * p.r_sm + k, rr[i]);
@@ -73,10 +93,10 @@ __global__ __launch_bounds__(WPR < 4 ? 256 : 64 * WPR) void rms_norm_quant_kerne
       }
 #pragma unroll
       for (int j = 0; j < 16; j++) ss = fmaf(h[i][j], h[i][j], ss);
-      const int64_t k = static_cast<int64_t>(wi + WPR * i) * kChunk + lane * kPerLane;
+      const int32_t k = at + kPass * i;
       if (p.res_out && live && k < p.K) store16<DT>(p.res_out, m * p.ro_sm + k, h[i]);
     }
-    ss = wave_sum(ss);
+    ss = row_reduce<LANES>(ss, add);
     if constexpr (WPR > 1) {
       if (lane == 0) part[par][0][wr][wi] = ss;
       __syncthreads();
@@ -105,7 +125,7 @@ __global__ __launch_bounds__(WPR < 4 ? 256 : 64 * WPR) void rms_norm_quant_kerne
       }
     }
     if (p.group == 0) {  // one group per row
-      row_max = wave_max(row_max);
+      row_max = row_reduce<LANES>(row_max, larger);
       if constexpr (WPR > 1) {
         if (lane == 0) part[par][1][wr][wi] = row_max;
         __syncthreads();
@@ -117,43 +137,51 @@ __global__ __launch_bounds__(WPR < 4 ? 256 : 64 * WPR) void rms_norm_quant_kerne
     }
 #pragma unroll
     for (int i = 0; i < CH; i++) {
-      const int64_t k = static_cast<int64_t>(wi + WPR * i) * kChunk + lane * kPerLane;
+      const int32_t k = at + kPass * i;
       uint32_t sbits;
       float inv;
       if (p.ue8m0) inv = group_multiplier<FP8Q_SCALE_UE8M0, false>(fmaxf(amax[i], kEps), sbits);
       else inv = group_multiplier<FP8Q_SCALE_F32, false>(fmaxf(amax[i], kEps), sbits);
       if (live && k < p.K) {
-        *reinterpret_cast<u32x4*>(p.q + m * p.q_sm + k) = encode16<false>(h[i], inv);
-        const bool first = p.group != 0 ? (k & (p.group - 1)) == 0 : k == 0;
-        if (first) {
-          const int64_t g = p.group != 0 ? k / p.group : 0;
-          const int64_t at = p.packed ? 4 * (m * p.s_sm + (g >> 2) * p.s_sg) + (g & 3) : m * p.s_sm + g * p.s_sg;
-          if (p.ue8m0) static_cast<uint8_t*>(p.s)[at] = static_cast<uint8_t>(sbits);
-          else static_cast<uint32_t*>(p.s)[at] = sbits;
+        *reinterpret_cast<u32x4*>(p.q + m * p.q_sm + k) = encode16_below448(h[i], inv);
+        // the group's first lane stores its scale
+        if (p.group != 0 ? (k & (p.group - 1)) == 0 : k == 0) {
+          const int32_t g = k >> p.group_shift;
+          const int64_t to = p.packed ? 4 * (m * p.s_sm + (g >> 2) * p.s_sg) + (g & 3) : m * p.s_sm + g * p.s_sg;
+          if (p.ue8m0) static_cast<uint8_t*>(p.s)[to] = static_cast<uint8_t>(sbits);
+          else static_cast<uint32_t*>(p.s)[to] = sbits;
         }
       }
     }
   }
 }
 
-template <int DT, int WPR, int CH>
+template <int DT, int LANES, int WPR, int CH>
 void launch_one(const NormParams& p, hipStream_t stream) {
-  constexpr int rows = WPR < 4 ? 4 / WPR : 1;
+  constexpr int rows = (WPR < 4 ? 4 / WPR : 1) * (64 / LANES);
   const int64_t grid = std::min<int64_t>((p.M + rows - 1) / rows, 65535);
-  hipLaunchKernelGGL((rms_norm_quant_kernel<DT, WPR, CH>), dim3(static_cast<unsigned>(grid)),
+  hipLaunchKernelGGL((rms_norm_quant_kernel<DT, LANES, WPR, CH>), dim3(static_cast<unsigned>(grid)),
                      dim3(WPR < 4 ? 256 : 64 * WPR), 0, stream, p);
 }
 
-// Waves per row by the row's length.
+// Lanes per row by its length: short rows share a wave, four to one (each lane's fixed work, about
+// 60 instructions for sums and scales, then serves up to 48 elements: 60000 x 256 takes 21.8 us,
+// 38 us with a wave per row); longer ones have 16 elements per lane and as many waves as that
+// takes, which is the most loads in flight (4096 x 7168: 8 waves 41.8 us, 4 waves of 32 elements
+// 42.7; one row of 7168: 3.2 and 3.7 us). Between 512 and 768 elements the registers decide: three
+// passes with a residual leave 4 waves per SIMD (30000 x 768: 35.7 us against 33.1 with a wave per
+// row; without a residual 15.0 against 15.7).
 template <int DT>
 void launch_dt(const NormParams& p, hipStream_t s) {
-  const int64_t chunks = (p.K + kChunk - 1) / kChunk;
-  if (chunks <= 1) launch_one<DT, 1, 1>(p, s);
-  else if (chunks <= 2) launch_one<DT, 2, 1>(p, s);
-  else if (chunks <= 4) launch_one<DT, 4, 1>(p, s);
-  else if (chunks <= 8) launch_one<DT, 4, 2>(p, s);
-  else if (chunks <= 16) launch_one<DT, 8, 2>(p, s);
-  else launch_one<DT, 16, 4>(p, s);
+  if (p.K <= 256) launch_one<DT, 16, 1, 1>(p, s);
+  else if (p.K <= 512) launch_one<DT, 16, 1, 2>(p, s);
+  else if (p.K <= 768 && !p.res) launch_one<DT, 16, 1, 3>(p, s);
+  else if (p.K <= 1024) launch_one<DT, 64, 1, 1>(p, s);
+  else if (p.K <= 2048) launch_one<DT, 64, 2, 1>(p, s);
+  else if (p.K <= 4096) launch_one<DT, 64, 4, 1>(p, s);
+  else if (p.K <= 8192) launch_one<DT, 64, 8, 1>(p, s);
+  else if (p.K <= 16384) launch_one<DT, 64, 16, 1>(p, s);
+  else launch_one<DT, 64, 16, 4>(p, s);
 }
 
 }  // namespace

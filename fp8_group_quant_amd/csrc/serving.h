@@ -20,6 +20,7 @@ struct NormParams {
   int64_t s_sm, s_sg;          // scale elements (packed UE8M0: words of 4 groups)
   float eps, inv_k;
   int32_t group;               // 32, 64, 128, or 0 (one group per row)
+  int32_t group_shift;         // log2 of it (one group per row: any shift past the row)
   int32_t ue8m0, packed;
 };
 
@@ -48,7 +49,7 @@ struct Kv4RowsParams {
   int64_t x_st[2], x_sh[2];
   const int32_t* slots;
   int64_t T;
-  int32_t H, D;
+  int32_t H, D, d_shift;  // D = 1 << d_shift
 };
 
 int launch_kv4_write(int dtype, const Kv4RowsParams& p, hipStream_t stream);
