@@ -279,33 +279,22 @@ struct Rows {
 template <int D>
 struct Codes {
   uint32_t w[D / 32];
-  uint32_t scale;  // byte i: the scale of elements 32i .. (one for D <= 128, two for D = 256)
 };
 
 template <int D>
-__device__ __forceinline__ void load_codes(const uint8_t* codes, uint32_t code_lane, const uint8_t* scales,
-                                           uint32_t scale_lane, int h, Codes<D>& c) {
-  codes += code_lane + D / 8 * h;
-  scales += scale_lane + (D == 64 ? h >> 1 : D / 128 * h);
+__device__ __forceinline__ void load_codes(const uint8_t* codes, uint32_t lane_offset, int h, Codes<D>& c) {
+  codes += lane_offset + D / 8 * h;
   if constexpr (D == 64) {
     const u32x2 a = *reinterpret_cast<const u32x2*>(codes);
     c.w[0] = a[0];
     c.w[1] = a[1];
-    c.scale = *scales;
-  } else if constexpr (D == 128) {
-    const u32x4 a = *reinterpret_cast<const u32x4*>(codes);
-#pragma unroll
-    for (int i = 0; i < 4; i++) c.w[i] = a[i];
-    c.scale = *scales;
   } else {
-    const u32x4 a = *reinterpret_cast<const u32x4*>(codes);
-    const u32x4 b = *reinterpret_cast<const u32x4*>(codes + 16);
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      c.w[i] = a[i];
-      c.w[4 + i] = b[i];
+    for (int j = 0; j < D / 128; j++) {
+      const u32x4 a = reinterpret_cast<const u32x4*>(codes)[j];
+#pragma unroll
+      for (int i = 0; i < 4; i++) c.w[4 * j + i] = a[i];
     }
-    c.scale = *reinterpret_cast<const uint16_t*>(scales);
   }
 }
 
@@ -313,14 +302,73 @@ template <int D>
 __device__ __forceinline__ void zero_codes(Codes<D>& c) {
 #pragma unroll
   for (int i = 0; i < D / 32; i++) c.w[i] = 0u;
-  c.scale = 0x7F7Fu;
+}
+
+// All scale bytes of one token's row, in one load per lane.
+template <int D>
+struct Scales {
+  uint32_t w[D == 256 ? 2 : 1];
+};
+
+template <int D>
+__device__ __forceinline__ void load_scales(const uint8_t* scales, Scales<D>& s) {
+  if constexpr (D == 64) {
+    s.w[0] = *reinterpret_cast<const uint16_t*>(scales);
+  } else {
+#pragma unroll
+    for (int i = 0; i < D / 128; i++) s.w[i] = reinterpret_cast<const uint32_t*>(scales)[i];
+  }
+}
+
+// The scales of a lane's part: of its one block, or for D = 256 its two.
+template <int D>
+struct Mult {
+  float f[D == 256 ? 2 : 1];
+};
+
+// Byte b of w as the exponent of a power of two: a rotation puts it at bits 23-30.
+__device__ __forceinline__ float pow2_of_byte(uint32_t w, uint32_t b) {
+  return __uint_as_float(__builtin_amdgcn_alignbit(w, w, (8 * b + 9) & 31) & 0x7F800000u);
+}
+
+template <int D>
+__device__ __forceinline__ Mult<D> mult_of(const Scales<D>& s, int h) {
+  Mult<D> m;
+  if constexpr (D == 256) {
+    const uint32_t w = h & 2 ? s.w[1] : s.w[0];
+    m.f[0] = pow2_of_byte(w, 2 * (h & 1));
+    m.f[1] = pow2_of_byte(w, 2 * (h & 1) + 1);
+  } else {
+    m.f[0] = pow2_of_byte(s.w[0], D == 64 ? h >> 1 : h);
+  }
+  return m;
+}
+
+// Scales of 32 tokens were loaded by lanes (r, h) for token r of half h & 1: both halves' for this
+// lane's r, from the neighbouring rows of 16 lanes.
+template <int D>
+__device__ __forceinline__ void mults_of(const Scales<D>& s, int h, Mult<D> (&m)[2]) {
+  Scales<D> a, b;
+#pragma unroll
+  for (int i = 0; i < (D == 256 ? 2 : 1); i++) {
+    const auto x = __builtin_amdgcn_permlane16_swap(s.w[i], s.w[i], false, false);
+    a.w[i] = x[0];
+    b.w[i] = x[1];
+  }
+  m[0] = mult_of<D>(a, h);
+  m[1] = mult_of<D>(b, h);
+}
+
+template <int D>
+__device__ __forceinline__ void one_mult(Mult<D>& m) {
+#pragma unroll
+  for (int i = 0; i < (D == 256 ? 2 : 1); i++) m.f[i] = 1.0f;
 }
 
 // Word i of a lane's part as 8 bf16 values (exact).
 template <int D>
-__device__ __forceinline__ bf16x8 widen_codes(const Codes<D>& c, int i) {
-  const uint32_t byte = D == 256 && i >= 4 ? c.scale >> 8 : c.scale & 0xFFu;
-  const float s = __uint_as_float(byte << 23);
+__device__ __forceinline__ bf16x8 widen_codes(const Codes<D>& c, const Mult<D>& m, int i) {
+  const float s = m.f[D == 256 ? i / 4 : 0];
   const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c.w[i], s, 0);
   const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c.w[i], s, 1);
   const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c.w[i], s, 2);
@@ -332,6 +380,7 @@ __device__ __forceinline__ bf16x8 widen_codes(const Codes<D>& c, int i) {
 template <int D>
 struct Step {
   Codes<D> k[2], v[2];
+  Scales<D> ks, vs;  // of token r of half h & 1
   uint32_t there;  // bit i: token i is inside the range and its page is in the cache
 };
 
@@ -392,14 +441,15 @@ template <int D, bool PAGE16>
 __device__ __forceinline__ void load_step(const Kv4AttnParams& p, const Kv4Cache& at, const Pages& g, int32_t t,
                                           int32_t t_end, Step<D>& st) {
   const int h = (threadIdx.x & 63) >> 4;
-  st.there = 0;
-#pragma unroll
-  for (int s = 0; s < 2; s++) {
-    const Half a = locate<PAGE16>(p, g.n[s], t + 16 * s, t_end);
-    st.there |= a.there << (16 * s);
-    load_codes<D>(at.k + a.c, a.c_lane, at.ks + a.s, a.s_lane, h, st.k[s]);
-    load_codes<D>(at.v + a.c, a.c_lane, at.vs + a.s, a.s_lane, h, st.v[s]);
-  }
+  const Half a = locate<PAGE16>(p, g.n[0], t, t_end), b = locate<PAGE16>(p, g.n[1], t + 16, t_end);
+  st.there = a.there | b.there << 16;
+  load_codes<D>(at.k + a.c, a.c_lane, h, st.k[0]);
+  load_codes<D>(at.k + b.c, b.c_lane, h, st.k[1]);
+  const int64_t s = (h & 1 ? b.s : a.s) + a.s_lane;
+  load_scales<D>(at.ks + s, st.ks);
+  load_codes<D>(at.v + a.c, a.c_lane, h, st.v[0]);
+  load_codes<D>(at.v + b.c, b.c_lane, h, st.v[1]);
+  load_scales<D>(at.vs + s, st.vs);
 }
 
 // The cache from cached head `head` on.
@@ -499,24 +549,30 @@ __global__ __launch_bounds__(64 * WAVES, waves_per_simd(D, DT)) void kv4_attenti
 
     for (; t < t_end; t += kStep) {
       f32x4 s[2];
+      Mult<D> mk[2], mv[2];
+      mults_of<D>(st.ks, h, mk);
 #pragma unroll
       for (int c = 0; c < 2; c++) {
         s[c] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < kSteps; j++) {
-          const bf16x8 k = widen_codes<D>(st.k[c], j);
+          const bf16x8 k = widen_codes<D>(st.k[c], mk[c], j);
 #pragma unroll
           for (int a = 0; a < PARTS; a++) s[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, q[a][j], s[c], 0, 0, 0);
         }
       }
       const uint32_t there = st.there;
       const bool part = there != 0xFFFFFFFFu || t + kTile > low;  // wave-uniform
+      mults_of<D>(st.vs, h, mv);
 #pragma unroll
       for (int c = 0; c < 2; c++) {
-        if (there != 0xFFFFFFFFu && ((there >> (16 * c + r)) & 1u) == 0u) zero_codes<D>(st.v[c]);
+        if (there != 0xFFFFFFFFu && ((there >> (16 * c + r)) & 1u) == 0u) {
+          zero_codes<D>(st.v[c]);
+          one_mult<D>(mv[c]);
+        }
 #pragma unroll
         for (int j = 0; j < kSteps; j++)
-          *reinterpret_cast<bf16x8*>(vt + (16 * c + r) * kRowV + D / 4 * h + 8 * j) = widen_codes<D>(st.v[c], j);
+          *reinterpret_cast<bf16x8*>(vt + (16 * c + r) * kRowV + D / 4 * h + 8 * j) = widen_codes<D>(st.v[c], mv[c], j);
       }
       // the next step's codes come in while this one's softmax and second product run (past the
       // end: rows of the last page, not used)
@@ -666,32 +722,41 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void kv4_attention_wide_kernel(
     const int32_t* table = p.table + w.b * p.table_sb;
     const Kv4Cache cache = at_head(p.c, head);
     Codes<D> k[kHalves], v;
+    Scales<D> ks[kHalves / 2], vs;
     uint64_t k_there = 0;
     uint32_t v_there = 0;
     int32_t k_page[kHalves], v_page = 0;
     auto load_k = [&](int32_t t) {
       k_there = 0;
 #pragma unroll
-      for (int c = 0; c < kHalves; c++) {
+      for (int c = 0; c < kHalves; c += 2) {
         const Half a = locate<PAGE16>(p, k_page[c], t + 16 * c, t_end);
-        k_there |= static_cast<uint64_t>(a.there) << (16 * c);
-        load_codes<D>(cache.k + a.c, a.c_lane, cache.ks + a.s, a.s_lane, h, k[c]);
+        const Half b = locate<PAGE16>(p, k_page[c + 1], t + 16 * c + 16, t_end);
+        k_there |= static_cast<uint64_t>(a.there | b.there << 16) << (16 * c);
+        load_codes<D>(cache.k + a.c, a.c_lane, h, k[c]);
+        load_codes<D>(cache.k + b.c, b.c_lane, h, k[c + 1]);
+        load_scales<D>(cache.ks + (h & 1 ? b.s : a.s) + a.s_lane, ks[c / 2]);
       }
     };
     auto load_v = [&](int32_t t) {
       const Half a = locate<PAGE16>(p, v_page, t + 16 * wave, t_end);
       v_there = a.there;
-      load_codes<D>(cache.v + a.c, a.c_lane, cache.vs + a.s, a.s_lane, h, v);
+      load_codes<D>(cache.v + a.c, a.c_lane, h, v);
+      load_scales<D>(cache.vs + a.s + a.s_lane, vs);
     };
     auto page_k = [&](int32_t t) {
 #pragma unroll
       for (int c = 0; c < kHalves; c++) k_page[c] = load_page<PAGE16>(p, table, t + 16 * c, t_end);
     };
     auto put_v = [&](int buf) {
-      if (((v_there >> r) & 1u) == 0u) zero_codes<D>(v);
+      Mult<D> mv = mult_of<D>(vs, h);
+      if (((v_there >> r) & 1u) == 0u) {
+        zero_codes<D>(v);
+        one_mult<D>(mv);
+      }
 #pragma unroll
       for (int j = 0; j < kSteps; j++)
-        *reinterpret_cast<bf16x8*>(&lds_v[buf][(16 * wave + r) * kRowV + D / 4 * h + 8 * j]) = widen_codes<D>(v, j);
+        *reinterpret_cast<bf16x8*>(&lds_v[buf][(16 * wave + r) * kRowV + D / 4 * h + 8 * j]) = widen_codes<D>(v, mv, j);
     };
     if (t0 < t_end) {
       page_k(t0);
@@ -744,11 +809,13 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void kv4_attention_wide_kernel(
       const uint64_t there = k_there;
 #pragma unroll
       for (int c = 0; c < kHalves; c++) {
+        Mult<D> mk[2];
+        mults_of<D>(ks[c / 2], h, mk);
 #pragma unroll
         for (int n = 0; n < QT; n++) s[n][c] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < kSteps; j++) {
-          const bf16x8 kk = widen_codes<D>(k[c], j);
+          const bf16x8 kk = widen_codes<D>(k[c], mk[c % 2], j);
 #pragma unroll
           for (int n = 0; n < QT; n++)
 #pragma unroll
