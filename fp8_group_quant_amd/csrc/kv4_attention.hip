@@ -275,33 +275,26 @@ struct Rows {
 };
 
 // ------------------------------------------------------------------ cached rows
-// A lane's part of one token's row: D / 4 elements.
+// A lane's part of one token's row: D / 4 elements, in the vectors that they are loaded as (taken
+// apart, they are copied as soon as they arrive, and waited for there).
 template <int D>
 struct Codes {
-  uint32_t w[D / 32];
+  static constexpr int kWords = D == 64 ? 2 : 4;
+  typedef uint32_t Vec __attribute__((ext_vector_type(kWords)));
+  Vec v[D / 32 / kWords];
 };
 
 template <int D>
 __device__ __forceinline__ void load_codes(const uint8_t* codes, uint32_t lane_offset, int h, Codes<D>& c) {
   codes += lane_offset + D / 8 * h;
-  if constexpr (D == 64) {
-    const u32x2 a = *reinterpret_cast<const u32x2*>(codes);
-    c.w[0] = a[0];
-    c.w[1] = a[1];
-  } else {
 #pragma unroll
-    for (int j = 0; j < D / 128; j++) {
-      const u32x4 a = reinterpret_cast<const u32x4*>(codes)[j];
-#pragma unroll
-      for (int i = 0; i < 4; i++) c.w[4 * j + i] = a[i];
-    }
-  }
+  for (int j = 0; j < D / 32 / Codes<D>::kWords; j++) c.v[j] = reinterpret_cast<const typename Codes<D>::Vec*>(codes)[j];
 }
 
 template <int D>
 __device__ __forceinline__ void zero_codes(Codes<D>& c) {
 #pragma unroll
-  for (int i = 0; i < D / 32; i++) c.w[i] = 0u;
+  for (int j = 0; j < D / 32 / Codes<D>::kWords; j++) c.v[j] = typename Codes<D>::Vec(0u);
 }
 
 // All scale bytes of one token's row, in one load per lane.
@@ -335,7 +328,7 @@ template <int D>
 __device__ __forceinline__ Mult<D> mult_of(const Scales<D>& s, int h) {
   Mult<D> m;
   if constexpr (D == 256) {
-    const uint32_t w = h & 2 ? s.w[1] : s.w[0];
+    const uint32_t lo = s.w[0], hi = s.w[1], w = h & 2 ? hi : lo;
     m.f[0] = pow2_of_byte(w, 2 * (h & 1));
     m.f[1] = pow2_of_byte(w, 2 * (h & 1) + 1);
   } else {
@@ -369,10 +362,11 @@ __device__ __forceinline__ void one_mult(Mult<D>& m) {
 template <int D>
 __device__ __forceinline__ bf16x8 widen_codes(const Codes<D>& c, const Mult<D>& m, int i) {
   const float s = m.f[D == 256 ? i / 4 : 0];
-  const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c.w[i], s, 0);
-  const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c.w[i], s, 1);
-  const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c.w[i], s, 2);
-  const bf16x2 e = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c.w[i], s, 3);
+  const uint32_t w = c.v[i / Codes<D>::kWords][i % Codes<D>::kWords];
+  const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0);
+  const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1);
+  const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2);
+  const bf16x2 e = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3);
   return bf16x8{a[0], a[1], b[0], b[1], d[0], d[1], e[0], e[1]};
 }
 
@@ -384,72 +378,118 @@ struct Step {
   uint32_t there;  // bit i: token i is inside the range and its page is in the cache
 };
 
-// Page numbers of a step's two halves: of the whole half where a page holds 16 tokens or more
-// (PAGE16, wave-uniform), else of the lane's token.
+// How a wave looks up the pages of the tokens that it loads together: for every token; for every
+// 16 where a page holds that many; or once where a page holds all of them (the pages of the last
+// two are wave-uniform: scalar loads and arithmetic).
+constexpr int kByToken = 0, kBy16 = 1, kByStep = 2;
+
+// Page numbers of N times 16 tokens.
+template <int PAGE, int N>
 struct Pages {
-  int32_t n[2];
+  int32_t n[PAGE == kByStep ? 1 : N];
 };
 
-template <bool PAGE16>
-__device__ __forceinline__ int32_t load_page(const Kv4AttnParams& p, const int32_t* table, int32_t t, int32_t t_end) {
-  // past the end: the last token's entry, which is there to be read
-  const int32_t at = min(t + (PAGE16 ? 0 : static_cast<int>(threadIdx.x & 15)), t_end - 1) >> p.c.page_shift;
-  return PAGE16 ? read_int(table, at) : table[at];
+template <int PAGE, int N>
+__device__ __forceinline__ Pages<PAGE, N> load_pages(const Kv4AttnParams& p, const int32_t* table, int32_t t, int32_t t_end) {
+  Pages<PAGE, N> g;
+#pragma unroll
+  for (int i = 0; i < (PAGE == kByStep ? 1 : N); i++) {
+    // past the end: the last token's entry, which is there to be read
+    const int32_t at = min(t + 16 * i + (PAGE == kByToken ? static_cast<int>(threadIdx.x & 15) : 0), t_end - 1) >> p.c.page_shift;
+    g.n[i] = PAGE == kByToken ? table[at] : read_int(table, at);
+  }
+  return g;
 }
 
-template <bool PAGE16>
-__device__ __forceinline__ Pages load_pages(const Kv4AttnParams& p, const int32_t* table, int32_t t, int32_t t_end) {
-  return Pages{{load_page<PAGE16>(p, table, t, t_end), load_page<PAGE16>(p, table, t + 16, t_end)}};
+// Makes the wave wait for pages that it has asked for.
+template <int PAGE, int N>
+__device__ __forceinline__ void settle(Pages<PAGE, N>& g) {
+  if constexpr (PAGE != kByToken) {
+#pragma unroll
+    for (int i = 0; i < (PAGE == kByStep ? 1 : N); i++) g.n[i] = uniform(g.n[i]);
+  }
 }
 
-// Where the rows of tokens t .. t + 15 lie in a page `n`, and which of them are there (bit i:
-// token t + i is before t_end and its page is in the cache). Every address is inside the cache: a page that
-// is not there is replaced by page 0, and tokens past the end lie in the last token's page or in
-// a valid one; what is loaded for them is not used.
-struct Half {
-  int64_t c, s;             // of the lane's token, without its head; PAGE16: wave-uniform,
-  uint32_t c_lane, s_lane;  // and the lane's part
-  uint32_t there;
+// Where the rows of N times 16 tokens from t on lie, without their head, and which of them are there
+// (bit i: token t + i is before t_end and its page is in the cache). Every address is inside the
+// cache: a page that is not there is replaced by page 0, and tokens past the end lie in the last
+// token's page or in a valid one; what is loaded for them is not used.
+template <int N>
+struct Spots {
+  int64_t c[N], s[N];             // of the lane's token; of the first token where pages are uniform,
+  uint32_t c_lane[N], s_lane[N];  // and the lane's offset from it
+  uint64_t there;
 };
 
-template <bool PAGE16>
-__device__ __forceinline__ Half locate(const Kv4AttnParams& p, int32_t n, int32_t t, int32_t t_end) {
+template <int PAGE, int N>
+__device__ __forceinline__ Spots<N> locate(const Kv4AttnParams& p, const Pages<PAGE, N>& g, int32_t t, int32_t t_end) {
   const int r = threadIdx.x & 15;
-  const int32_t mask = (1 << p.c.page_shift) - 1, left = t_end - t;
-  const bool ok = n >= 0 && n < p.c.pages;
-  const int64_t page = ok ? n : 0;
-  Half a;
-  if constexpr (PAGE16) {  // page strides and page extents fit 32 bits
-    const uint32_t in = t & mask, c_st = static_cast<uint32_t>(p.c.c_st), s_st = static_cast<uint32_t>(p.c.s_st);
-    a.there = !ok || left <= 0 ? 0u : left >= 16 ? 0xFFFFu : (1u << left) - 1u;
-    a.c = static_cast<uint64_t>(static_cast<uint32_t>(page)) * static_cast<uint32_t>(p.c.c_sp) + in * c_st;
-    a.s = static_cast<uint64_t>(static_cast<uint32_t>(page)) * static_cast<uint32_t>(p.c.s_sp) + in * s_st;
-    a.c_lane = r * c_st;
-    a.s_lane = r * s_st;
-  } else {
-    const int64_t in = min(t + r, t_end - 1) & mask;
-    a.there = static_cast<uint32_t>(__builtin_amdgcn_ballot_w64(ok && r < left) & 0xFFFFu);
-    a.c = page * p.c.c_sp + in * p.c.c_st;
-    a.s = page * p.c.s_sp + in * p.c.s_st;
-    a.c_lane = a.s_lane = 0;
+  const int32_t mask = (1 << p.c.page_shift) - 1;
+  const uint32_t pages = static_cast<uint32_t>(p.c.pages);
+  Spots<N> a;
+  if constexpr (PAGE == kByToken) {
+    a.there = 0;
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+      const bool ok = static_cast<uint32_t>(g.n[i]) < pages;
+      const int64_t page = ok ? g.n[i] : 0, in = min(t + 16 * i + r, t_end - 1) & mask;
+      a.there |= (__builtin_amdgcn_ballot_w64(ok && t + 16 * i + r < t_end) & 0xFFFFull) << (16 * i);
+      a.c[i] = page * p.c.c_sp + in * p.c.c_st;
+      a.s[i] = page * p.c.s_sp + in * p.c.s_st;
+      a.c_lane[i] = a.s_lane[i] = 0;
+    }
+  } else {  // page strides and page extents fit 32 bits
+    const uint32_t c_sp = static_cast<uint32_t>(p.c.c_sp), c_st = static_cast<uint32_t>(p.c.c_st);
+    const uint32_t s_sp = static_cast<uint32_t>(p.c.s_sp), s_st = static_cast<uint32_t>(p.c.s_st);
+    const int32_t left = t_end - t;
+    constexpr uint64_t kAll = N == 4 ? ~0ull : (1ull << (16 * N % 64)) - 1;
+    a.there = left >= 16 * N ? kAll : left <= 0 ? 0 : (1ull << left) - 1;
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+      if (PAGE == kBy16 || i == 0) {
+        const uint32_t n = static_cast<uint32_t>(g.n[i]), page = n < pages ? n : 0, in = (t + 16 * i) & mask;
+        a.there &= n < pages ? ~0ull : PAGE == kByStep ? 0ull : ~(0xFFFFull << (16 * i));
+        a.c[i] = static_cast<uint64_t>(page) * c_sp + in * c_st;
+        a.s[i] = static_cast<uint64_t>(page) * s_sp + in * s_st;
+        a.c_lane[i] = r * c_st;
+        a.s_lane[i] = r * s_st;
+      } else {
+        a.c[i] = a.c[0];
+        a.s[i] = a.s[0];
+        a.c_lane[i] = (r + 16 * i) * c_st;
+        a.s_lane[i] = (r + 16 * i) * s_st;
+      }
+    }
   }
   return a;
 }
 
+// The scales of tokens 16 i .. 16 i + 31: lane (r, h) loads token r of half h & 1. (The choice is made
+// between values: between an array's elements it would put the array into memory.)
+template <int D, int PAGE, int N>
+__device__ __forceinline__ void load_scales_of(const uint8_t* scales, const Spots<N>& a, int i, int h, Scales<D>& s) {
+  if constexpr (PAGE == kByStep) {
+    const uint32_t x = a.s_lane[i], y = a.s_lane[i + 1];
+    load_scales<D>(scales + a.s[0] + (h & 1 ? y : x), s);
+  } else {
+    const int64_t x = a.s[i] + a.s_lane[i], y = a.s[i + 1] + a.s_lane[i + 1];
+    load_scales<D>(scales + (h & 1 ? y : x), s);
+  }
+}
+
 // Loads a step's codes and scales; k and v (with their scales) start at the unit's head.
-template <int D, bool PAGE16>
-__device__ __forceinline__ void load_step(const Kv4AttnParams& p, const Kv4Cache& at, const Pages& g, int32_t t,
+template <int D, int PAGE>
+__device__ __forceinline__ void load_step(const Kv4AttnParams& p, const Kv4Cache& at, const Pages<PAGE, 2>& g, int32_t t,
                                           int32_t t_end, Step<D>& st) {
   const int h = (threadIdx.x & 63) >> 4;
-  const Half a = locate<PAGE16>(p, g.n[0], t, t_end), b = locate<PAGE16>(p, g.n[1], t + 16, t_end);
-  st.there = a.there | b.there << 16;
-  load_codes<D>(at.k + a.c, a.c_lane, h, st.k[0]);
-  load_codes<D>(at.k + b.c, b.c_lane, h, st.k[1]);
-  const int64_t s = (h & 1 ? b.s : a.s) + a.s_lane;
-  load_scales<D>(at.ks + s, st.ks);
-  load_codes<D>(at.v + a.c, a.c_lane, h, st.v[0]);
-  load_codes<D>(at.v + b.c, b.c_lane, h, st.v[1]);
-  load_scales<D>(at.vs + s, st.vs);
+  const Spots<2> a = locate<PAGE, 2>(p, g, t, t_end);
+  st.there = static_cast<uint32_t>(a.there);
+  load_codes<D>(at.k + a.c[0], a.c_lane[0], h, st.k[0]);
+  load_codes<D>(at.k + a.c[1], a.c_lane[1], h, st.k[1]);
+  load_scales_of<D, PAGE>(at.ks, a, 0, h, st.ks);
+  load_codes<D>(at.v + a.c[0], a.c_lane[0], h, st.v[0]);
+  load_codes<D>(at.v + a.c[1], a.c_lane[1], h, st.v[1]);
+  load_scales_of<D, PAGE>(at.vs, a, 0, h, st.vs);
 }
 
 // The cache from cached head `head` on.
@@ -490,7 +530,7 @@ __device__ __forceinline__ void split8(u32x4 raw, uint32_t sign, bf16x8 (&out)[P
 // Waves per SIMD that the registers are kept to (O^T and Q take D / 4 + D / 8 of them per lane).
 constexpr int waves_per_simd(int64_t D, int DT) { return D == 256 ? 2 : DT == FP8Q_DTYPE_F16 && D == 128 ? 3 : 4; }
 
-template <int D, int DT, int WAVES, bool SPLIT, bool PAGE16>
+template <int D, int DT, int WAVES, bool SPLIT, int PAGE>
 __global__ __launch_bounds__(64 * WAVES, waves_per_simd(D, DT)) void kv4_attention_kernel(Kv4AttnParams p) {
   constexpr int PARTS = DT == FP8Q_DTYPE_F16 ? 2 : 1;
   constexpr int kStep = kTile * WAVES;  // tokens of the block's step
@@ -520,11 +560,11 @@ __global__ __launch_bounds__(64 * WAVES, waves_per_simd(D, DT)) void kv4_attenti
     const Kv4Cache cache = at_head(p.c, head);
     int32_t t = w.t0 + kTile * wave;
     Step<D> st;
-    Pages pages;
+    Pages<PAGE, 2> pages;
     if (t < t_end) {
-      pages = load_pages<PAGE16>(p, table, t, t_end);
-      load_step<D, PAGE16>(p, cache, pages, t, t_end, st);
-      pages = load_pages<PAGE16>(p, table, t + kStep, t_end);
+      pages = load_pages<PAGE, 2>(p, table, t, t_end);
+      load_step<D, PAGE>(p, cache, pages, t, t_end, st);
+      pages = load_pages<PAGE, 2>(p, table, t + kStep, t_end);
     }
 
     bf16x8 q[PARTS][kSteps];
@@ -576,8 +616,8 @@ __global__ __launch_bounds__(64 * WAVES, waves_per_simd(D, DT)) void kv4_attenti
       }
       // the next step's codes come in while this one's softmax and second product run (past the
       // end: rows of the last page, not used)
-      load_step<D, PAGE16>(p, cache, pages, t + kStep, t_end, st);
-      pages = load_pages<PAGE16>(p, table, t + 2 * kStep, t_end);
+      load_step<D, PAGE>(p, cache, pages, t + kStep, t_end, st);
+      pages = load_pages<PAGE, 2>(p, table, t + 2 * kStep, t_end);
 
       if (part) {
 #pragma unroll
@@ -691,6 +731,15 @@ __global__ __launch_bounds__(64 * WAVES, waves_per_simd(D, DT)) void kv4_attenti
   }
 }
 
+// V^T's operand for dims 16 d .. + 15 and the 32 tokens whose rows start at `src` (of lane (r, h): row
+// 4h + r / 4, element 4 (r % 4)).
+template <int ROW>
+__device__ __forceinline__ bf16x8 read_v(const uint16_t* src, int d) {
+  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(src + 16 * d));
+  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(src + 16 * d + 16 * ROW));
+  return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
 // ------------------------------------------------------------------ many query rows
 // The same products for tiles of 64 QT rows: every wave has 16 QT rows of its own and all the
 // tokens, 64 at a time. K's codes are converted in registers by every wave (they serve QT
@@ -698,7 +747,7 @@ __global__ __launch_bounds__(64 * WAVES, waves_per_simd(D, DT)) void kv4_attenti
 // step ahead of its use (two buffers, one barrier per step).
 constexpr int kStepW = 64;
 
-template <int D, int DT, int QT, bool SPLIT, bool PAGE16>
+template <int D, int DT, int QT, bool SPLIT, int PAGE>
 __global__ __launch_bounds__(64 * kWideWaves, 2) void kv4_attention_wide_kernel(Kv4AttnParams p) {
   constexpr int PARTS = DT == FP8Q_DTYPE_F16 ? 2 : 1;
   constexpr int kSteps = D / 32, kDims = D / 16, kRowV = D + kPadV;
@@ -725,29 +774,25 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void kv4_attention_wide_kernel(
     Scales<D> ks[kHalves / 2], vs;
     uint64_t k_there = 0;
     uint32_t v_there = 0;
-    int32_t k_page[kHalves], v_page = 0;
+    Pages<PAGE, kHalves> k_page{};
+    Pages<PAGE, 1> v_page{};
     auto load_k = [&](int32_t t) {
-      k_there = 0;
+      const Spots<kHalves> a = locate<PAGE, kHalves>(p, k_page, t, t_end);
+      k_there = a.there;
 #pragma unroll
       for (int c = 0; c < kHalves; c += 2) {
-        const Half a = locate<PAGE16>(p, k_page[c], t + 16 * c, t_end);
-        const Half b = locate<PAGE16>(p, k_page[c + 1], t + 16 * c + 16, t_end);
-        k_there |= static_cast<uint64_t>(a.there | b.there << 16) << (16 * c);
-        load_codes<D>(cache.k + a.c, a.c_lane, h, k[c]);
-        load_codes<D>(cache.k + b.c, b.c_lane, h, k[c + 1]);
-        load_scales<D>(cache.ks + (h & 1 ? b.s : a.s) + a.s_lane, ks[c / 2]);
+        load_codes<D>(cache.k + a.c[c], a.c_lane[c], h, k[c]);
+        load_codes<D>(cache.k + a.c[c + 1], a.c_lane[c + 1], h, k[c + 1]);
+        load_scales_of<D, PAGE>(cache.ks, a, c, h, ks[c / 2]);
       }
     };
     auto load_v = [&](int32_t t) {
-      const Half a = locate<PAGE16>(p, v_page, t + 16 * wave, t_end);
-      v_there = a.there;
-      load_codes<D>(cache.v + a.c, a.c_lane, h, v);
-      load_scales<D>(cache.vs + a.s + a.s_lane, vs);
+      const Spots<1> a = locate<PAGE, 1>(p, v_page, t + 16 * wave, t_end);
+      v_there = static_cast<uint32_t>(a.there);
+      load_codes<D>(cache.v + a.c[0], a.c_lane[0], h, v);
+      load_scales<D>(cache.vs + a.s[0] + a.s_lane[0], vs);
     };
-    auto page_k = [&](int32_t t) {
-#pragma unroll
-      for (int c = 0; c < kHalves; c++) k_page[c] = load_page<PAGE16>(p, table, t + 16 * c, t_end);
-    };
+    auto pages_v = [&](int32_t t) { return load_pages<PAGE, 1>(p, table, t + 16 * wave, t_end); };
     auto put_v = [&](int buf) {
       Mult<D> mv = mult_of<D>(vs, h);
       if (((v_there >> r) & 1u) == 0u) {
@@ -759,12 +804,12 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void kv4_attention_wide_kernel(
         *reinterpret_cast<bf16x8*>(&lds_v[buf][(16 * wave + r) * kRowV + D / 4 * h + 8 * j]) = widen_codes<D>(v, mv, j);
     };
     if (t0 < t_end) {
-      page_k(t0);
-      v_page = load_page<PAGE16>(p, table, t0 + 16 * wave, t_end);
+      k_page = load_pages<PAGE, kHalves>(p, table, t0, t_end);
+      v_page = pages_v(t0);
       load_k(t0);
       load_v(t0);
-      page_k(t0 + kStepW);
-      v_page = load_page<PAGE16>(p, table, t0 + kStepW + 16 * wave, t_end);
+      k_page = load_pages<PAGE, kHalves>(p, table, t0 + kStepW, t_end);
+      v_page = pages_v(t0 + kStepW);
     }
 
     bf16x8 q[QT][PARTS][kSteps];
@@ -797,16 +842,31 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void kv4_attention_wide_kernel(
       for (int d = 0; d < kDims; d++) o[n][d] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
 
+        constexpr int kAhead = 1, kGroups = kHalves / 2 * kDims / kAhead;
+    const int v_at = (4 * h + (r >> 2)) * kRowV + 4 * (r & 3);
+    auto read_group = [&](int buf, int g, bf16x8 (&f)[kAhead]) {
+#pragma unroll
+      for (int i = 0; i < kAhead; i++) {
+        const int at = g * kAhead + i;
+        f[i] = read_v<kRowV>(&lds_v[buf][32 * (at / kDims) * kRowV + v_at], at % kDims);
+      }
+    };
     if (t0 < t_end) {
       put_v(0);
       load_v(t0 + kStepW);
-      v_page = load_page<PAGE16>(p, table, t0 + 2 * kStepW + 16 * wave, t_end);
+      v_page = pages_v(t0 + 2 * kStepW);
     }
     __syncthreads();
     int buf = 0;
     for (int32_t t = t0; t < t_end; t += kStepW, buf ^= 1) {
       f32x4 s[QT][kHalves];
       const uint64_t there = k_there;
+      // the pages after next, waited for (below) before any LDS read is under way: scalar loads
+      // return in no order, so that with one outstanding every LDS read would wait for all
+      Pages<PAGE, kHalves> next_k;
+      if constexpr (PAGE == kByStep) next_k.n[0] = v_page.n[0];  // V is a step ahead
+      else next_k = load_pages<PAGE, kHalves>(p, table, t + 2 * kStepW, t_end);
+      Pages<PAGE, 1> next_v = pages_v(t + 3 * kStepW);
 #pragma unroll
       for (int c = 0; c < kHalves; c++) {
         Mult<D> mk[2];
@@ -825,10 +885,14 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void kv4_attention_wide_kernel(
       }
       // loads past the end bring rows of the last page, which are not used
       load_k(t + kStepW);
-      page_k(t + 2 * kStepW);
       put_v(buf ^ 1);
       load_v(t + 2 * kStepW);
-      v_page = load_page<PAGE16>(p, table, t + 3 * kStepW + 16 * wave, t_end);
+      settle<PAGE, kHalves>(next_k);
+      settle<PAGE, 1>(next_v);
+      k_page = next_k;
+      v_page = next_v;
+      bf16x8 vf[2][kAhead];
+      read_group(buf, 0, vf[0]);
       {
         const bool part = there != ~0ull || t + kStepW > low;  // wave-uniform
         bf16x8 pr[QT][PARTS][kHalves / 2];
@@ -870,20 +934,21 @@ __global__ __launch_bounds__(64 * kWideWaves, 2) void kv4_attention_wide_kernel(
               if constexpr (PARTS == 2) pr[n][1][c / 2][4 * (c % 2) + i] = static_cast<__bf16>(e - static_cast<float>(hi));
             }
         }
+        // operands are read kAhead dim tiles ahead of their products
 #pragma unroll
-        for (int c = 0; c < kHalves / 2; c++) {
+        for (int g = 0; g < kGroups; g++) {
+          if (g + 1 < kGroups) read_group(buf, g + 1, vf[(g + 1) & 1]);
+          __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-          for (int d = 0; d < kDims; d++) {
-            const uint16_t* src = &lds_v[buf][(32 * c + 4 * h + (r >> 2)) * kRowV + 16 * d + 4 * (r & 3)];
-            const s16x4 a0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(src));
-            const s16x4 a1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(src + 16 * kRowV));
-            const auto av = __builtin_shufflevector(a0, a1, 0, 1, 2, 3, 4, 5, 6, 7);
+          for (int i = 0; i < kAhead; i++) {
+            const int at = g * kAhead + i, c = at / kDims, d = at % kDims;
 #pragma unroll
             for (int n = 0; n < QT; n++)
 #pragma unroll
               for (int a = 0; a < PARTS; a++)
-                o[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, av), pr[n][a][c], o[n][d], 0, 0, 0);
+                o[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[g & 1][i], pr[n][a][c], o[n][d], 0, 0, 0);
           }
+          __builtin_amdgcn_sched_barrier(0);
         }
       }
       __syncthreads();
@@ -1037,19 +1102,20 @@ Shape shape_of(int dtype, int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t
 
 struct Launch {
   const Kv4AttnParams& p;
-  bool split, page16;
+  bool split;
+  int page;  // kByToken, kBy16, kByStep
   const Shape& shape;
   unsigned grid;
   hipStream_t stream;
 
-  template <int D, int DT, int ROWS, bool SPLIT, bool PAGE16>
+  template <int D, int DT, int ROWS, bool SPLIT, int PAGE>
   void run() const {
     const size_t lds = 2 * (p.B + 1) * sizeof(int32_t);
     if constexpr (ROWS == kRows)
-      hipLaunchKernelGGL((kv4_attention_kernel<D, DT, narrow_waves(DT, D), SPLIT, PAGE16>), dim3(grid),
+      hipLaunchKernelGGL((kv4_attention_kernel<D, DT, narrow_waves(DT, D), SPLIT, PAGE>), dim3(grid),
                          dim3(64 * narrow_waves(DT, D)), lds, stream, p);
     else
-      hipLaunchKernelGGL((kv4_attention_wide_kernel<D, DT, ROWS / 64, SPLIT, PAGE16>), dim3(grid),
+      hipLaunchKernelGGL((kv4_attention_wide_kernel<D, DT, ROWS / 64, SPLIT, PAGE>), dim3(grid),
                          dim3(64 * kWideWaves), lds, stream, p);
     if constexpr (SPLIT) {
       const int64_t rows = p.T * p.Hq;
@@ -1062,10 +1128,15 @@ struct Launch {
                            dim3(64 * kJoinWaves), 0, stream, p);
     }
   }
+  template <int D, int DT, int ROWS, bool SPLIT>
+  void by_page() const {
+    if (page == kByStep) run<D, DT, ROWS, SPLIT, kByStep>();
+    else if (page == kBy16) run<D, DT, ROWS, SPLIT, kBy16>();
+    else run<D, DT, ROWS, SPLIT, kByToken>();
+  }
   template <int D, int DT, int ROWS>
   void by_kind() const {
-    if (split) page16 ? run<D, DT, ROWS, true, true>() : run<D, DT, ROWS, true, false>();
-    else page16 ? run<D, DT, ROWS, false, true>() : run<D, DT, ROWS, false, false>();
+    split ? by_page<D, DT, ROWS, true>() : by_page<D, DT, ROWS, false>();
   }
   template <int D, int DT>
   void by_rows() const {
@@ -1096,14 +1167,14 @@ int launch_kv4_attention(int dtype, int64_t D, Kv4AttnParams p, void* ws, int64_
     p.plan = static_cast<int32_t*>(ws);
     p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + s.plan_bytes);
   }
-  // a page of 16 tokens or more holds every 16 tokens that a wave loads together; their offsets
-  // are computed in 32 bits
-  const int64_t page = int64_t(1) << p.c.page_shift, most = int64_t(1) << 32;
-  const bool page16 = p.c.page_shift >= 4 && p.c.c_sp < most && p.c.s_sp < most && p.c.c_st < most / page &&
-                      p.c.s_st < most / page;
+  // Uniform pages where their offsets can be computed in 32 bits.
+  const int64_t most = int64_t(1) << 32, most_row = most >> p.c.page_shift;
+  const bool fits = p.c.c_sp < most && p.c.s_sp < most && p.c.c_st < most_row && p.c.s_st < most_row;
+  const int step = s.rows == kRows ? kTile : kStepW;
+  const int page = !fits || p.c.page_shift < 4 ? kByToken : (1 << p.c.page_shift) < step ? kBy16 : kByStep;
   // unsplit: blocks walk the units in turn
   const unsigned grid = static_cast<unsigned>(split ? s.blocks : std::min<int64_t>(s.units, int64_t(1) << 20));
-  const Launch run{p, split, page16, s, grid, stream};
+  const Launch run{p, split, page, s, grid, stream};
   if (D == 64) run.by_type<64>(dtype);
   else if (D == 128) run.by_type<128>(dtype);
   else run.by_type<256>(dtype);
