@@ -747,8 +747,16 @@ __device__ __forceinline__ bf16x8 read_v(const uint16_t* src, int d) {
 // step ahead of its use (two buffers, one barrier per step).
 constexpr int kStepW = 64;
 
+// Waves per SIMD that the registers are kept to (fp16, D = 128, 64 rows: 451 us at 3, 468 at 2, for 2 x
+// 1024 queries of 32 heads over 8192 tokens; bf16, D = 64, 128 rows: 350 and 388 for 2 x 2048).
+constexpr int wide_waves_per_simd(int D, int DT, int QT, bool split) {
+  const int parts = DT == FP8Q_DTYPE_F16 ? 2 : 1;
+  if (D * QT * parts <= 64) return 4;
+  return (D * QT * parts <= 128 && !(D == 64 && split)) || (D == 128 && QT == 1) ? 3 : 2;
+}
+
 template <int D, int DT, int QT, bool SPLIT, int PAGE>
-__global__ __launch_bounds__(64 * kWideWaves, 2) void kv4_attention_wide_kernel(Kv4AttnParams p) {
+__global__ __launch_bounds__(64 * kWideWaves, wide_waves_per_simd(D, DT, QT, SPLIT)) void kv4_attention_wide_kernel(Kv4AttnParams p) {
   constexpr int PARTS = DT == FP8Q_DTYPE_F16 ? 2 : 1;
   constexpr int kSteps = D / 32, kDims = D / 16, kRowV = D + kPadV;
   constexpr int kHalves = kStepW / 16;
@@ -1075,8 +1083,23 @@ int tile_rows(int dtype, int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t 
 constexpr int narrow_waves(int DT, int64_t D) { return D == 256 || waves_per_simd(D, DT) < 4 ? 4 : 8; }
 constexpr int narrow_blocks(int DT, int64_t D) { return waves_per_simd(D, DT) * 4 / narrow_waves(DT, D); }
 
+// Blocks for short caches: all the waves that a CU holds, so that a unit needs no second block and
+// no join.
+constexpr int tall_waves(int DT, int64_t D) { return waves_per_simd(D, DT) * 4; }
+
+// Whether every unit has a tall block of its own. That costs about 7 us and 1.6 us for each of the
+// block's steps (one sequence, 8 cached heads of 128: 500 tokens 8.7 us, 1000 10.3, 2000 13.6, 4000
+// 19.6), the split 10.1 us with its join, and as much for each of its fewer steps (11.7, 11.7,
+// 12.1 and 11.8 us; 16 sequences of 4000 tokens 24.3 us against 21.8).
+bool tall_is_faster(int dtype, int64_t D, int64_t units, int64_t max_tokens, int64_t blocks) {
+  const int64_t tall = (max_tokens + kTile * tall_waves(dtype, D) - 1) / (kTile * tall_waves(dtype, D));
+  const int64_t split = units * max_tokens / (blocks * kTile * narrow_waves(dtype, D)) + 1;
+  return units <= current_device_shape().cus && (tall <= 2 || tall <= 2 * split);
+}
+
 struct Shape {
   int rows;        // of a tile
+  bool tall;
   int64_t units;   // at most
   int64_t blocks;  // that a split call's work is cut for: those that run at once
   int span_shift;
@@ -1089,13 +1112,14 @@ Shape shape_of(int dtype, int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t
   s.units = Hkv * ((T * (Hq / Hkv) + s.rows - 1) / s.rows + B);
   const bool narrow = s.rows == kRows;
   s.blocks = static_cast<int64_t>(current_device_shape().cus) * (narrow ? narrow_blocks(dtype, D) : 2);
+  s.tall = narrow && tall_is_faster(dtype, D, s.units, max_tokens, s.blocks);
   // spans of 128 tokens, or longer ones where the line could have 2^31 places
   s.span_shift = 7;
   while (s.units * ((max_tokens >> s.span_shift) + 1) >= (int64_t(1) << 31)) s.span_shift++;
   s.plan_bytes = (2 * (B + 1) * 4 + 255) / 256 * 256;
   // With many units the device is full without splitting; ragged lengths balance better with
   // it, which the narrow kernel's small pieces are worth up to some rounds of blocks.
-  const bool split = max_tokens > (int64_t(kMinRun) << s.span_shift) && s.units < s.blocks * (narrow ? 8 : 1);
+  const bool split = !s.tall && max_tokens > (int64_t(kMinRun) << s.span_shift) && s.units < s.blocks * (narrow ? 8 : 1);
   s.bytes = split ? s.plan_bytes + (s.units + s.blocks) * (s.rows * (D + 2)) * 4 : 0;
   return s;
 }
@@ -1111,12 +1135,17 @@ struct Launch {
   template <int D, int DT, int ROWS, bool SPLIT, int PAGE>
   void run() const {
     const size_t lds = 2 * (p.B + 1) * sizeof(int32_t);
-    if constexpr (ROWS == kRows)
-      hipLaunchKernelGGL((kv4_attention_kernel<D, DT, narrow_waves(DT, D), SPLIT, PAGE>), dim3(grid),
-                         dim3(64 * narrow_waves(DT, D)), lds, stream, p);
-    else
+    if constexpr (ROWS == kRows) {
+      if (!SPLIT && shape.tall)
+        hipLaunchKernelGGL((kv4_attention_kernel<D, DT, tall_waves(DT, D), false, PAGE>), dim3(grid),
+                           dim3(64 * tall_waves(DT, D)), lds, stream, p);
+      else
+        hipLaunchKernelGGL((kv4_attention_kernel<D, DT, narrow_waves(DT, D), SPLIT, PAGE>), dim3(grid),
+                           dim3(64 * narrow_waves(DT, D)), lds, stream, p);
+    } else {
       hipLaunchKernelGGL((kv4_attention_wide_kernel<D, DT, ROWS / 64, SPLIT, PAGE>), dim3(grid),
                          dim3(64 * kWideWaves), lds, stream, p);
+    }
     if constexpr (SPLIT) {
       const int64_t rows = p.T * p.Hq;
       // a wave per row, or where the units are cut into many pieces a block
