@@ -29,6 +29,7 @@
 // rounded to bf16 once: the error, 2^-8 of each term at most, is of the size of the output's
 // own rounding.
 #include <algorithm>
+#include <type_traits>
 
 #include "serving.h"
 #include "serving_device.h"
@@ -45,7 +46,6 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 constexpr int kRows = 16;   // query rows of an item
-constexpr int kTile = 32;   // tokens of a wave's step
 constexpr int kWideWaves = 4;  // of a block of the wide kernel
 constexpr int kJoinWaves = 4;
 constexpr int kPadV = 16;   // elements between the V rows in LDS
@@ -337,19 +337,27 @@ __device__ __forceinline__ Mult<D> mult_of(const Scales<D>& s, int h) {
   return m;
 }
 
-// Scales of 32 tokens were loaded by lanes (r, h) for token r of half h & 1: both halves' for this
-// lane's r, from the neighbouring rows of 16 lanes.
-template <int D>
-__device__ __forceinline__ void mults_of(const Scales<D>& s, int h, Mult<D> (&m)[2]) {
-  Scales<D> a, b;
+// Scales of N = 2 or 4 times 16 tokens were loaded by lanes (r, h) for token r of half h % N: each
+// half's for this lane's r, from the other rows of 16 lanes.
+template <int D, int N>
+__device__ __forceinline__ void spread_scales(const Scales<D>& s, int h, Mult<D> (&m)[N]) {
+  Scales<D> half[4];
 #pragma unroll
   for (int i = 0; i < (D == 256 ? 2 : 1); i++) {
-    const auto x = __builtin_amdgcn_permlane16_swap(s.w[i], s.w[i], false, false);
-    a.w[i] = x[0];
-    b.w[i] = x[1];
+    const auto x = __builtin_amdgcn_permlane16_swap(s.w[i], s.w[i], false, false);  // rows 0 0 2 2, 1 1 3 3
+    half[0].w[i] = x[0];
+    half[1].w[i] = x[1];
+    if constexpr (N == 4) {
+      const auto a = __builtin_amdgcn_permlane32_swap(x[0], x[0], false, false);
+      const auto b = __builtin_amdgcn_permlane32_swap(x[1], x[1], false, false);
+      half[0].w[i] = a[0];
+      half[2].w[i] = a[1];
+      half[1].w[i] = b[0];
+      half[3].w[i] = b[1];
+    }
   }
-  m[0] = mult_of<D>(a, h);
-  m[1] = mult_of<D>(b, h);
+#pragma unroll
+  for (int c = 0; c < N; c++) m[c] = mult_of<D>(half[c], h);
 }
 
 template <int D>
@@ -370,13 +378,16 @@ __device__ __forceinline__ bf16x8 widen_codes(const Codes<D>& c, const Mult<D>& 
   return bf16x8{a[0], a[1], b[0], b[1], d[0], d[1], e[0], e[1]};
 }
 
-// The 32 tokens of one step of a wave: tokens 0-15 in part 0, 16-31 in part 1.
-template <int D>
+// One step of a wave: N times 16 tokens.
+template <int D, int N>
 struct Step {
-  Codes<D> k[2], v[2];
-  Scales<D> ks, vs;  // of token r of half h & 1
-  uint32_t there;  // bit i: token i is inside the range and its page is in the cache
+  Codes<D> k[N], v[N];
+  Scales<D> ks, vs;  // of token r of half h % N
+  std::conditional_t<N == 4, uint64_t, uint32_t> there;  // bit i: token i is inside the range, its page in the cache
 };
+
+template <int N>
+constexpr std::conditional_t<N == 4, uint64_t, uint32_t> kAllThere = N == 4 ? ~0ull : (1ull << (16 * N % 64)) - 1;
 
 // How a wave looks up the pages of the tokens that it loads together: for every token; for every
 // 16 where a page holds that many; or once where a page holds all of them (the pages of the last
@@ -442,8 +453,7 @@ __device__ __forceinline__ Spots<N> locate(const Kv4AttnParams& p, const Pages<P
     const uint32_t c_sp = static_cast<uint32_t>(p.c.c_sp), c_st = static_cast<uint32_t>(p.c.c_st);
     const uint32_t s_sp = static_cast<uint32_t>(p.c.s_sp), s_st = static_cast<uint32_t>(p.c.s_st);
     const int32_t left = t_end - t;
-    constexpr uint64_t kAll = N == 4 ? ~0ull : (1ull << (16 * N % 64)) - 1;
-    a.there = left >= 16 * N ? kAll : left <= 0 ? 0 : (1ull << left) - 1;
+    a.there = left >= 16 * N ? kAllThere<N> : left <= 0 ? 0 : (1ull << left) - 1;
 #pragma unroll
     for (int i = 0; i < N; i++) {
       if (PAGE == kBy16 || i == 0) {
@@ -464,32 +474,42 @@ __device__ __forceinline__ Spots<N> locate(const Kv4AttnParams& p, const Pages<P
   return a;
 }
 
-// The scales of tokens 16 i .. 16 i + 31: lane (r, h) loads token r of half h & 1. (The choice is made
-// between values: between an array's elements it would put the array into memory.)
-template <int D, int PAGE, int N>
+// The scales of M = 2 or 4 times 16 tokens from the i-th on: lane (r, h) loads token r of half h % M.
+// (The choice is made between values: between an array's elements it would put the array into memory.)
+template <int D, int PAGE, int M, int N>
 __device__ __forceinline__ void load_scales_of(const uint8_t* scales, const Spots<N>& a, int i, int h, Scales<D>& s) {
   if constexpr (PAGE == kByStep) {
-    const uint32_t x = a.s_lane[i], y = a.s_lane[i + 1];
-    load_scales<D>(scales + a.s[0] + (h & 1 ? y : x), s);
+    const uint32_t v = a.s_lane[i], w = a.s_lane[i + 1];
+    uint32_t lane = h & 1 ? w : v;
+    if constexpr (M == 4) {
+      const uint32_t x = a.s_lane[i + 2], y = a.s_lane[i + 3], z = h & 1 ? y : x;
+      lane = h & 2 ? z : lane;
+    }
+    load_scales<D>(scales + a.s[0] + lane, s);
   } else {
-    const int64_t x = a.s[i] + a.s_lane[i], y = a.s[i + 1] + a.s_lane[i + 1];
-    load_scales<D>(scales + (h & 1 ? y : x), s);
+    const int64_t v = a.s[i] + a.s_lane[i], w = a.s[i + 1] + a.s_lane[i + 1];
+    int64_t at = h & 1 ? w : v;
+    if constexpr (M == 4) {
+      const int64_t x = a.s[i + 2] + a.s_lane[i + 2], y = a.s[i + 3] + a.s_lane[i + 3], z = h & 1 ? y : x;
+      at = h & 2 ? z : at;
+    }
+    load_scales<D>(scales + at, s);
   }
 }
 
 // Loads a step's codes and scales; k and v (with their scales) start at the unit's head.
-template <int D, int PAGE>
-__device__ __forceinline__ void load_step(const Kv4AttnParams& p, const Kv4Cache& at, const Pages<PAGE, 2>& g, int32_t t,
-                                          int32_t t_end, Step<D>& st) {
+template <int D, int PAGE, int N>
+__device__ __forceinline__ void load_step(const Kv4AttnParams& p, const Kv4Cache& at, const Pages<PAGE, N>& g, int32_t t,
+                                          int32_t t_end, Step<D, N>& st) {
   const int h = (threadIdx.x & 63) >> 4;
-  const Spots<2> a = locate<PAGE, 2>(p, g, t, t_end);
-  st.there = static_cast<uint32_t>(a.there);
-  load_codes<D>(at.k + a.c[0], a.c_lane[0], h, st.k[0]);
-  load_codes<D>(at.k + a.c[1], a.c_lane[1], h, st.k[1]);
-  load_scales_of<D, PAGE>(at.ks, a, 0, h, st.ks);
-  load_codes<D>(at.v + a.c[0], a.c_lane[0], h, st.v[0]);
-  load_codes<D>(at.v + a.c[1], a.c_lane[1], h, st.v[1]);
-  load_scales_of<D, PAGE>(at.vs, a, 0, h, st.vs);
+  const Spots<N> a = locate<PAGE, N>(p, g, t, t_end);
+  st.there = a.there;
+#pragma unroll
+  for (int c = 0; c < N; c++) load_codes<D>(at.k + a.c[c], a.c_lane[c], h, st.k[c]);
+  load_scales_of<D, PAGE, N>(at.ks, a, 0, h, st.ks);
+#pragma unroll
+  for (int c = 0; c < N; c++) load_codes<D>(at.v + a.c[c], a.c_lane[c], h, st.v[c]);
+  load_scales_of<D, PAGE, N>(at.vs, a, 0, h, st.vs);
 }
 
 // The cache from cached head `head` on.
@@ -527,13 +547,27 @@ __device__ __forceinline__ void split8(u32x4 raw, uint32_t sign, bf16x8 (&out)[P
   }
 }
 
-// Waves per SIMD that the registers are kept to (O^T and Q take D / 4 + D / 8 of them per lane).
-constexpr int waves_per_simd(int64_t D, int DT) { return D == 256 ? 2 : DT == FP8Q_DTYPE_F16 && D == 128 ? 3 : 4; }
+// V^T's operand for dims 16 d .. + 15 and the 32 tokens whose rows start at `src` (of lane (r, h): row
+// 4h + r / 4, element 4 (r % 4)).
+template <int ROW>
+__device__ __forceinline__ bf16x8 read_v(const uint16_t* src, int d) {
+  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(src + 16 * d));
+  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(src + 16 * d + 16 * ROW));
+  return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+}
 
-template <int D, int DT, int WAVES, bool SPLIT, int PAGE>
-__global__ __launch_bounds__(64 * WAVES, waves_per_simd(D, DT)) void kv4_attention_kernel(Kv4AttnParams p) {
+// Waves per SIMD that the registers are kept to (O^T and Q take D / 4 + D / 8 of them per lane, a
+// step's codes N D / 16).
+constexpr int waves_per_simd(int64_t D, int DT, int N) {
+  if (D == 256 || (D == 128 && N == 4)) return 2;
+  return N == 4 || (DT == FP8Q_DTYPE_F16 && D == 128) ? 3 : 4;
+}
+
+template <int D, int DT, int WAVES, int N, bool SPLIT, int PAGE>
+__global__ __launch_bounds__(64 * WAVES, waves_per_simd(D, DT, N)) void kv4_attention_kernel(Kv4AttnParams p) {
   constexpr int PARTS = DT == FP8Q_DTYPE_F16 ? 2 : 1;
-  constexpr int kStep = kTile * WAVES;  // tokens of the block's step
+  constexpr int kTile = 16 * N;         // tokens of a wave's step
+  constexpr int kStep = kTile * WAVES;  // and of the block's
   constexpr int kSteps = D / 32;   // contraction steps of S^T
   constexpr int kDims = D / 16;    // dim tiles of O^T
   constexpr int kRowV = D + kPadV;  // LDS row of V (bf16 elements)
@@ -559,12 +593,12 @@ __global__ __launch_bounds__(64 * WAVES, waves_per_simd(D, DT)) void kv4_attenti
     const int32_t* table = p.table + w.b * p.table_sb;
     const Kv4Cache cache = at_head(p.c, head);
     int32_t t = w.t0 + kTile * wave;
-    Step<D> st;
-    Pages<PAGE, 2> pages;
+    Step<D, N> st;
+    Pages<PAGE, N> pages;
     if (t < t_end) {
-      pages = load_pages<PAGE, 2>(p, table, t, t_end);
-      load_step<D, PAGE>(p, cache, pages, t, t_end, st);
-      pages = load_pages<PAGE, 2>(p, table, t + kStep, t_end);
+      pages = load_pages<PAGE, N>(p, table, t, t_end);
+      load_step<D, PAGE, N>(p, cache, pages, t, t_end, st);
+      pages = load_pages<PAGE, N>(p, table, t + kStep, t_end);
     }
 
     bf16x8 q[PARTS][kSteps];
@@ -588,11 +622,11 @@ __global__ __launch_bounds__(64 * WAVES, waves_per_simd(D, DT)) void kv4_attenti
     float m = kNegInf, l = 0.0f;  // l: this lane's share of the row's sum
 
     for (; t < t_end; t += kStep) {
-      f32x4 s[2];
-      Mult<D> mk[2], mv[2];
-      mults_of<D>(st.ks, h, mk);
+      f32x4 s[N];
+      Mult<D> mk[N], mv[N];
+      spread_scales<D, N>(st.ks, h, mk);
 #pragma unroll
-      for (int c = 0; c < 2; c++) {
+      for (int c = 0; c < N; c++) {
         s[c] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < kSteps; j++) {
@@ -601,12 +635,12 @@ __global__ __launch_bounds__(64 * WAVES, waves_per_simd(D, DT)) void kv4_attenti
           for (int a = 0; a < PARTS; a++) s[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, q[a][j], s[c], 0, 0, 0);
         }
       }
-      const uint32_t there = st.there;
-      const bool part = there != 0xFFFFFFFFu || t + kTile > low;  // wave-uniform
-      mults_of<D>(st.vs, h, mv);
+      const auto there = st.there;
+      const bool part = there != kAllThere<N> || t + kTile > low;  // wave-uniform
+      spread_scales<D, N>(st.vs, h, mv);
 #pragma unroll
-      for (int c = 0; c < 2; c++) {
-        if (there != 0xFFFFFFFFu && ((there >> (16 * c + r)) & 1u) == 0u) {
+      for (int c = 0; c < N; c++) {
+        if (there != kAllThere<N> && ((there >> (16 * c + r)) & 1u) == 0u) {
           zero_codes<D>(st.v[c]);
           one_mult<D>(mv[c]);
         }
@@ -616,12 +650,12 @@ __global__ __launch_bounds__(64 * WAVES, waves_per_simd(D, DT)) void kv4_attenti
       }
       // the next step's codes come in while this one's softmax and second product run (past the
       // end: rows of the last page, not used)
-      load_step<D, PAGE>(p, cache, pages, t + kStep, t_end, st);
-      pages = load_pages<PAGE, 2>(p, table, t + 2 * kStep, t_end);
+      load_step<D, PAGE, N>(p, cache, pages, t + kStep, t_end, st);
+      pages = load_pages<PAGE, N>(p, table, t + 2 * kStep, t_end);
 
       if (part) {
 #pragma unroll
-        for (int c = 0; c < 2; c++)
+        for (int c = 0; c < N; c++)
 #pragma unroll
           for (int i = 0; i < 4; i++) {
             const int n = 16 * c + 4 * h + i;
@@ -630,7 +664,7 @@ __global__ __launch_bounds__(64 * WAVES, waves_per_simd(D, DT)) void kv4_attenti
       }
       float mx = kNegInf;
 #pragma unroll
-      for (int c = 0; c < 2; c++)
+      for (int c = 0; c < N; c++)
 #pragma unroll
         for (int i = 0; i < 4; i++) mx = fmaxf(mx, s[c][i]);
       mx = quad_max(mx) * p.scale_log2;
@@ -644,29 +678,33 @@ __global__ __launch_bounds__(64 * WAVES, waves_per_simd(D, DT)) void kv4_attenti
           for (int i = 0; i < 4; i++) o[d][i] *= alpha;
       }
       const float ms = m == kNegInf ? 0.0f : m;  // nothing seen yet: every p is 0
-      bf16x8 pr[PARTS];
+      bf16x8 pr[N / 2][PARTS];
 #pragma unroll
-      for (int c = 0; c < 2; c++)
+      for (int c = 0; c < N; c++)
 #pragma unroll
         for (int i = 0; i < 4; i++) {
           const float e = exp2_fast(fmaf(s[c][i], p.scale_log2, -ms));
           l += e;
-          pr[0][4 * c + i] = static_cast<__bf16>(e);
-          if constexpr (PARTS == 2) pr[1][4 * c + i] = static_cast<__bf16>(e - static_cast<float>(pr[0][4 * c + i]));
+          const __bf16 hi = static_cast<__bf16>(e);
+          pr[c / 2][0][4 * (c % 2) + i] = hi;
+          if constexpr (PARTS == 2) pr[c / 2][1][4 * (c % 2) + i] = static_cast<__bf16>(e - static_cast<float>(hi));
         }
 
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
       __builtin_amdgcn_wave_barrier();
       __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+      // every operand is read one product ahead
+      const uint16_t* v_at = vt + (4 * h + (r >> 2)) * kRowV + 4 * (r & 3);
+      bf16x8 vf[2];
+      vf[0] = read_v<kRowV>(v_at, 0);
 #pragma unroll
-      for (int d = 0; d < kDims; d++) {
-        const uint16_t* src = vt + (4 * h + (r >> 2)) * kRowV + 16 * d + 4 * (r & 3);
-        const s16x4 a0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(src));
-        const s16x4 a1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(src + 16 * kRowV));
-        const auto av = __builtin_shufflevector(a0, a1, 0, 1, 2, 3, 4, 5, 6, 7);
+      for (int g = 0; g < N / 2 * kDims; g++) {
+        const int c = g / kDims, d = g % kDims;
+        if (g + 1 < N / 2 * kDims) vf[(g + 1) & 1] = read_v<kRowV>(v_at + 32 * ((g + 1) / kDims) * kRowV, (g + 1) % kDims);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int a = 0; a < PARTS; a++)
-          o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, av), pr[a], o[d], 0, 0, 0);
+        for (int a = 0; a < PARTS; a++) o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[g & 1], pr[c][a], o[d], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
       }
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
       __builtin_amdgcn_wave_barrier();
@@ -731,15 +769,6 @@ __global__ __launch_bounds__(64 * WAVES, waves_per_simd(D, DT)) void kv4_attenti
   }
 }
 
-// V^T's operand for dims 16 d .. + 15 and the 32 tokens whose rows start at `src` (of lane (r, h): row
-// 4h + r / 4, element 4 (r % 4)).
-template <int ROW>
-__device__ __forceinline__ bf16x8 read_v(const uint16_t* src, int d) {
-  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(src + 16 * d));
-  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(src + 16 * d + 16 * ROW));
-  return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
-}
-
 // ------------------------------------------------------------------ many query rows
 // The same products for tiles of 64 QT rows: every wave has 16 QT rows of its own and all the
 // tokens, 64 at a time. K's codes are converted in registers by every wave (they serve QT
@@ -791,7 +820,7 @@ __global__ __launch_bounds__(64 * kWideWaves, wide_waves_per_simd(D, DT, QT, SPL
       for (int c = 0; c < kHalves; c += 2) {
         load_codes<D>(cache.k + a.c[c], a.c_lane[c], h, k[c]);
         load_codes<D>(cache.k + a.c[c + 1], a.c_lane[c + 1], h, k[c + 1]);
-        load_scales_of<D, PAGE>(cache.ks, a, c, h, ks[c / 2]);
+        load_scales_of<D, PAGE, 2>(cache.ks, a, c, h, ks[c / 2]);
       }
     };
     auto load_v = [&](int32_t t) {
@@ -850,15 +879,7 @@ __global__ __launch_bounds__(64 * kWideWaves, wide_waves_per_simd(D, DT, QT, SPL
       for (int d = 0; d < kDims; d++) o[n][d] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
 
-        constexpr int kAhead = 1, kGroups = kHalves / 2 * kDims / kAhead;
-    const int v_at = (4 * h + (r >> 2)) * kRowV + 4 * (r & 3);
-    auto read_group = [&](int buf, int g, bf16x8 (&f)[kAhead]) {
-#pragma unroll
-      for (int i = 0; i < kAhead; i++) {
-        const int at = g * kAhead + i;
-        f[i] = read_v<kRowV>(&lds_v[buf][32 * (at / kDims) * kRowV + v_at], at % kDims);
-      }
-    };
+        const int v_at = (4 * h + (r >> 2)) * kRowV + 4 * (r & 3);
     if (t0 < t_end) {
       put_v(0);
       load_v(t0 + kStepW);
@@ -878,7 +899,7 @@ __global__ __launch_bounds__(64 * kWideWaves, wide_waves_per_simd(D, DT, QT, SPL
 #pragma unroll
       for (int c = 0; c < kHalves; c++) {
         Mult<D> mk[2];
-        mults_of<D>(ks[c / 2], h, mk);
+        spread_scales<D, 2>(ks[c / 2], h, mk);
 #pragma unroll
         for (int n = 0; n < QT; n++) s[n][c] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -899,8 +920,9 @@ __global__ __launch_bounds__(64 * kWideWaves, wide_waves_per_simd(D, DT, QT, SPL
       settle<PAGE, 1>(next_v);
       k_page = next_k;
       v_page = next_v;
-      bf16x8 vf[2][kAhead];
-      read_group(buf, 0, vf[0]);
+      const uint16_t* v_src = &lds_v[buf][v_at];
+      bf16x8 vf[2];
+      vf[0] = read_v<kRowV>(v_src, 0);
       {
         const bool part = there != ~0ull || t + kStepW > low;  // wave-uniform
         bf16x8 pr[QT][PARTS][kHalves / 2];
@@ -942,20 +964,18 @@ __global__ __launch_bounds__(64 * kWideWaves, wide_waves_per_simd(D, DT, QT, SPL
               if constexpr (PARTS == 2) pr[n][1][c / 2][4 * (c % 2) + i] = static_cast<__bf16>(e - static_cast<float>(hi));
             }
         }
-        // operands are read kAhead dim tiles ahead of their products
+        // every operand is read one product ahead
 #pragma unroll
-        for (int g = 0; g < kGroups; g++) {
-          if (g + 1 < kGroups) read_group(buf, g + 1, vf[(g + 1) & 1]);
+        for (int g = 0; g < kHalves / 2 * kDims; g++) {
+          const int c = g / kDims, d = g % kDims;
+          if (g + 1 < kHalves / 2 * kDims)
+            vf[(g + 1) & 1] = read_v<kRowV>(v_src + 32 * ((g + 1) / kDims) * kRowV, (g + 1) % kDims);
           __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-          for (int i = 0; i < kAhead; i++) {
-            const int at = g * kAhead + i, c = at / kDims, d = at % kDims;
+          for (int n = 0; n < QT; n++)
 #pragma unroll
-            for (int n = 0; n < QT; n++)
-#pragma unroll
-              for (int a = 0; a < PARTS; a++)
-                o[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[g & 1][i], pr[n][a][c], o[n][d], 0, 0, 0);
-          }
+            for (int a = 0; a < PARTS; a++)
+              o[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[g & 1], pr[n][a][c], o[n][d], 0, 0, 0);
           __builtin_amdgcn_sched_barrier(0);
         }
       }
@@ -1072,28 +1092,31 @@ __global__ __launch_bounds__(64 * kJoinWaves) void kv4_join_kernel(Kv4AttnParams
 constexpr int widest(int dtype, int64_t D) { return D * (dtype == FP8Q_DTYPE_F16 ? 2 : 1) <= 128 ? 128 : 64; }
 
 // Query rows of a tile. Up to two tiles of 16 rows per sequence (of mean length) and cached head
-// take the kernel whose waves share the tokens; more take the one whose waves share the rows.
+// take the kernel whose waves share the tokens; more take the one whose waves share the rows. 16
+// sequences of 4096 tokens, 8 cached heads of 128, with 16, 64 and 128 rows to a tile: 32 rows 33,
+// 41 and 53 us; 36 rows 47, 41 and 54; 64 rows 50, 45 and 58; 96 rows 76, 73 and 63.
 int tile_rows(int dtype, int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D) {
   const int64_t rows = (T * (Hq / Hkv) + B - 1) / B;
   return rows <= 2 * kRows ? kRows : rows <= 64 ? 64 : widest(dtype, D);
 }
 
-// Waves of the narrow kernel's blocks, and the blocks that a CU holds: 8 waves (fewer pieces to
-// join than with 4) where two such blocks fit its registers and LDS.
-constexpr int narrow_waves(int DT, int64_t D) { return D == 256 || waves_per_simd(D, DT) < 4 ? 4 : 8; }
-constexpr int narrow_blocks(int DT, int64_t D) { return waves_per_simd(D, DT) * 4 / narrow_waves(DT, D); }
+// The narrow kernel's split and general form: 16 N tokens per wave and step (64, but 32 where V's
+// rows in LDS and the codes' registers leave no room), in blocks of 4 waves.
+constexpr int narrow_halves(int DT, int64_t D) { return D == 256 || (D == 128 && DT == FP8Q_DTYPE_F16) ? 2 : 4; }
+constexpr int kNarrowWaves = 4;
+constexpr int narrow_blocks(int DT, int64_t D) { return waves_per_simd(D, DT, narrow_halves(DT, D)) * 4 / kNarrowWaves; }
 
 // Blocks for short caches: all the waves that a CU holds, so that a unit needs no second block and
 // no join.
-constexpr int tall_waves(int DT, int64_t D) { return waves_per_simd(D, DT) * 4; }
+constexpr int tall_waves(int DT, int64_t D) { return waves_per_simd(D, DT, 2) * 4; }
 
 // Whether every unit has a tall block of its own. That costs about 7 us and 1.6 us for each of the
 // block's steps (one sequence, 8 cached heads of 128: 500 tokens 8.7 us, 1000 10.3, 2000 13.6, 4000
 // 19.6), the split 10.1 us with its join, and as much for each of its fewer steps (11.7, 11.7,
 // 12.1 and 11.8 us; 16 sequences of 4000 tokens 24.3 us against 21.8).
 bool tall_is_faster(int dtype, int64_t D, int64_t units, int64_t max_tokens, int64_t blocks) {
-  const int64_t tall = (max_tokens + kTile * tall_waves(dtype, D) - 1) / (kTile * tall_waves(dtype, D));
-  const int64_t split = units * max_tokens / (blocks * kTile * narrow_waves(dtype, D)) + 1;
+  const int64_t tall = (max_tokens + 32 * tall_waves(dtype, D) - 1) / (32 * tall_waves(dtype, D));
+  const int64_t split = units * max_tokens / (blocks * 16 * narrow_halves(dtype, D) * kNarrowWaves) + 1;
   return units <= current_device_shape().cus && (tall <= 2 || tall <= 2 * split);
 }
 
@@ -1137,11 +1160,11 @@ struct Launch {
     const size_t lds = 2 * (p.B + 1) * sizeof(int32_t);
     if constexpr (ROWS == kRows) {
       if (!SPLIT && shape.tall)
-        hipLaunchKernelGGL((kv4_attention_kernel<D, DT, tall_waves(DT, D), false, PAGE>), dim3(grid),
+        hipLaunchKernelGGL((kv4_attention_kernel<D, DT, tall_waves(DT, D), 2, false, PAGE>), dim3(grid),
                            dim3(64 * tall_waves(DT, D)), lds, stream, p);
       else
-        hipLaunchKernelGGL((kv4_attention_kernel<D, DT, narrow_waves(DT, D), SPLIT, PAGE>), dim3(grid),
-                           dim3(64 * narrow_waves(DT, D)), lds, stream, p);
+        hipLaunchKernelGGL((kv4_attention_kernel<D, DT, kNarrowWaves, narrow_halves(DT, D), SPLIT, PAGE>), dim3(grid),
+                           dim3(64 * kNarrowWaves), lds, stream, p);
     } else {
       hipLaunchKernelGGL((kv4_attention_wide_kernel<D, DT, ROWS / 64, SPLIT, PAGE>), dim3(grid),
                          dim3(64 * kWideWaves), lds, stream, p);
@@ -1199,7 +1222,7 @@ int launch_kv4_attention(int dtype, int64_t D, Kv4AttnParams p, void* ws, int64_
   // Uniform pages where their offsets can be computed in 32 bits.
   const int64_t most = int64_t(1) << 32, most_row = most >> p.c.page_shift;
   const bool fits = p.c.c_sp < most && p.c.s_sp < most && p.c.c_st < most_row && p.c.s_st < most_row;
-  const int step = s.rows == kRows ? kTile : kStepW;
+  const int step = s.rows != kRows ? kStepW : s.tall ? 32 : static_cast<int>(16 * narrow_halves(dtype, D));
   const int page = !fits || p.c.page_shift < 4 ? kByToken : (1 << p.c.page_shift) < step ? kBy16 : kByStep;
   // unsplit: blocks walk the units in turn
   const unsigned grid = static_cast<unsigned>(split ? s.blocks : std::min<int64_t>(s.units, int64_t(1) << 20));
