@@ -250,7 +250,7 @@ int attention_entry(const void* q, int dtype, int64_t q_st, int64_t q_sh, const 
   p.l_st = l_st;
   p.table = table;
   p.table_sb = table_sb;
-  p.max_tokens = max_pages * page_size;
+  p.max_tokens = pages == 0 ? 0 : max_pages * page_size;  // an empty cache holds no sequence's tokens
   p.kv_lens = kv_lens;
   p.q_indptr = q_indptr;
   p.B = B;

@@ -360,6 +360,14 @@ __device__ __forceinline__ void spread_scales(const Scales<D>& s, int h, Mult<D>
   for (int c = 0; c < N; c++) m[c] = mult_of<D>(half[c], h);
 }
 
+// Values' scales above 2^125 count as 2^125: every value is then finite, and one that a row does not
+// see, whatever its bytes are, adds 0 times it, which is 0.
+template <int D>
+__device__ __forceinline__ void keep_finite(Mult<D>& m) {
+#pragma unroll
+  for (int i = 0; i < (D == 256 ? 2 : 1); i++) m.f[i] = __uint_as_float(min(__float_as_uint(m.f[i]), (125u + 127u) << 23));
+}
+
 template <int D>
 __device__ __forceinline__ void one_mult(Mult<D>& m) {
 #pragma unroll
@@ -523,12 +531,6 @@ __device__ __forceinline__ Kv4Cache at_head(const Kv4Cache& c, int32_t head) {
 }
 
 // ------------------------------------------------------------------ the kernel
-template <int DT>
-__device__ __forceinline__ float to_f32(uint32_t half) {
-  if constexpr (DT == FP8Q_DTYPE_BF16) return bf16_lo(half);
-  else return f16_lo(half);
-}
-
 // bf16: one part. fp16: high and low parts whose sum is the value. `sign`: 0, or 0x80008000 to
 // negate (the scale's sign: scores are then multiplied by its magnitude, after their maximum).
 template <int DT, int PARTS>
@@ -640,6 +642,7 @@ __global__ __launch_bounds__(64 * WAVES, waves_per_simd(D, DT, N)) void kv4_atte
       spread_scales<D, N>(st.vs, h, mv);
 #pragma unroll
       for (int c = 0; c < N; c++) {
+        keep_finite<D>(mv[c]);
         if (there != kAllThere<N> && ((there >> (16 * c + r)) & 1u) == 0u) {
           zero_codes<D>(st.v[c]);
           one_mult<D>(mv[c]);
@@ -756,13 +759,13 @@ __global__ __launch_bounds__(64 * WAVES, waves_per_simd(D, DT, N)) void kv4_atte
       } else {
         const int32_t i = (first + row) / p.group;
         const int64_t row_t = seq.q0 + i, hh = head * p.group + first + row - i * p.group;
-        const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
+        const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
         u32x4 bits;
 #pragma unroll
         for (int j = 0; j < 4; j++) bits[j] = pack16<DT>(v[2 * j] * inv, v[2 * j + 1] * inv);
         *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p.out) + row_t * p.o_st + hh * p.o_sh + col) = bits;
         if (p.lse && col == 0)
-          p.lse[row_t * p.l_st + hh] = ll > 0.0f ? (mm + __builtin_amdgcn_logf(ll)) * kLn2 : kNegInf;
+          p.lse[row_t * p.l_st + hh] = ll == 0.0f ? kNegInf : (mm + __builtin_amdgcn_logf(ll)) * kLn2;
       }
     }
     __syncthreads();
@@ -832,6 +835,7 @@ __global__ __launch_bounds__(64 * kWideWaves, wide_waves_per_simd(D, DT, QT, SPL
     auto pages_v = [&](int32_t t) { return load_pages<PAGE, 1>(p, table, t + 16 * wave, t_end); };
     auto put_v = [&](int buf) {
       Mult<D> mv = mult_of<D>(vs, h);
+      keep_finite<D>(mv);
       if (((v_there >> r) & 1u) == 0u) {
         zero_codes<D>(v);
         one_mult<D>(mv);
@@ -879,7 +883,7 @@ __global__ __launch_bounds__(64 * kWideWaves, wide_waves_per_simd(D, DT, QT, SPL
       for (int d = 0; d < kDims; d++) o[n][d] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
 
-        const int v_at = (4 * h + (r >> 2)) * kRowV + 4 * (r & 3);
+    const int v_at = (4 * h + (r >> 2)) * kRowV + 4 * (r & 3);
     if (t0 < t_end) {
       put_v(0);
       load_v(t0 + kStepW);
@@ -999,14 +1003,14 @@ __global__ __launch_bounds__(64 * kWideWaves, wide_waves_per_simd(D, DT, QT, SPL
       } else {
         const int32_t i = row / p.group;
         const int64_t row_t = seq.q0 + i, hh = head * p.group + row - i * p.group;
-        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
         uint16_t* dst = static_cast<uint16_t*>(p.out) + row_t * p.o_st + hh * p.o_sh + 4 * h;
 #pragma unroll
         for (int d = 0; d < kDims; d++)
           *reinterpret_cast<u32x2*>(dst + 16 * d) =
               u32x2{pack16<DT>(o[n][d][0] * inv, o[n][d][1] * inv), pack16<DT>(o[n][d][2] * inv, o[n][d][3] * inv)};
         if (p.lse && h == 0)
-          p.lse[row_t * p.l_st + hh] = sum > 0.0f ? (m[n] + __builtin_amdgcn_logf(sum)) * kLn2 : kNegInf;
+          p.lse[row_t * p.l_st + hh] = sum == 0.0f ? kNegInf : (m[n] + __builtin_amdgcn_logf(sum)) * kLn2;
       }
     }
   }
@@ -1076,7 +1080,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void kv4_join_kernel(Kv4AttnParams
       for (int i = 0; i < kPer; i++) acc[i] += lds_o[w][kPer * lane + i];
     }
   }
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   uint16_t* dst = static_cast<uint16_t*>(p.out) + t * p.o_st + qh * p.o_sh + kPer * lane;
   if constexpr (kPer == 1) {
     *dst = static_cast<uint16_t>(pack16<DT>(acc[0] * inv, 0.0f));
@@ -1084,7 +1088,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void kv4_join_kernel(Kv4AttnParams
 #pragma unroll
     for (int i = 0; i < kPer; i += 2) *reinterpret_cast<uint32_t*>(dst + i) = pack16<DT>(acc[i] * inv, acc[i + 1] * inv);
   }
-  if (p.lse && lane == 0) p.lse[t * p.l_st + qh] = l > 0.0f ? (ts + __builtin_amdgcn_logf(l)) * kLn2 : kNegInf;
+  if (p.lse && lane == 0) p.lse[t * p.l_st + qh] = l == 0.0f ? kNegInf : (ts + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
 // ------------------------------------------------------------------ launch

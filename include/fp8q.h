@@ -412,7 +412,9 @@ int fp8q_kv4_read(void* k, int64_t k_st, int64_t k_sh,
  *   lse = ln sum_j exp( sm_scale * q . k_j )   ([T][Hq] fp32 at lse + t*l_st + head; NULL: not stored)
  * A row that sees no token gets zeros, and -infinity in lse. Rows of q in no sequence are not
  * written. Cached bytes past a sequence's length, and table entries past its pages, are never
- * used. Scores, sums and the output are accumulated in fp32.
+ * used; cached bytes of tokens that a row does not see, whatever they are, do not reach its
+ * results. For that, values' scales above 2^125 (bytes above 252, which the write stores only for
+ * magnitudes above 2.5e38) count as 2^125. Scores, sums and the output are accumulated in fp32.
  *
  * fp8q_kv4_attention_workspace_size returns the bytes of workspace with which the call splits
  * long caches over more of the device (max_tokens = max_pages * page_size; 0: it needs none, or

@@ -362,6 +362,52 @@ def test_flat_softmax(D, dtype):
     check_attention([40, 3], [500, 90], 4, 1, D, 32, dtype=dtype, q_scale=0.01)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("D,page", [(64, 1), (64, 64), (128, 16), (128, 64), (256, 16)])
+@pytest.mark.parametrize("queries", [3, 12, 90])
+def test_tokens_that_a_row_does_not_see(queries, D, page, dtype):
+    """Scale bytes of NaN in the last two tokens: the queries before them give the same bits."""
+    f = fq()
+    n, Hkv, G = 200, 2, 4
+    table, pages = make_table([n], page, 1, 5)
+    c = filled_cache(pages, page, Hkv, D, "head", 6)
+    q = values(7, queries, G * Hkv, D, dtype=dtype).cuda()
+    ends = torch.tensor([0, queries], dtype=torch.int32).cuda()
+    lens = torch.tensor([n], dtype=torch.int32).cuda()
+    runs = []
+    for poison in (False, True):
+        if poison:
+            for t in (n - 2, n - 1):
+                for x in c:
+                    x[table[0, t // page], t % page] = 0xFF
+        out, lse = torch.empty_like(q), torch.empty(queries, G * Hkv, device="cuda")
+        f.fp8q_kv4_attention(q, c, table.cuda(), lens, out, D ** -0.5, True, ends, lse)
+        torch.cuda.synchronize()
+        runs.append((out[:-2], lse[:-2]))
+    assert torch.equal(runs[0][0], runs[1][0]) and torch.equal(runs[0][1], runs[1][1])
+    assert bool(torch.isfinite(runs[0][0]).all())
+
+
+@pytest.mark.parametrize("queries", [1, 5, 40])
+def test_cache_without_pages(queries):
+    """No page in the cache, whatever the lengths and the table say: nothing is seen, read or written."""
+    f = fq()
+    D, Hkv = 128, 2
+    c = f.Kv4Cache(*(torch.empty(0, 16, Hkv, w, dtype=torch.uint8, device="cuda") for w in (D // 2, D // 32) * 2))
+    q = values(1, 2 * queries, 4 * Hkv, D).cuda()
+    table = torch.arange(8, dtype=torch.int32, device="cuda").reshape(2, 4)
+    out, lse = torch.full_like(q, 77.0), torch.full(q.shape[:2], 77.0, device="cuda")
+    f.fp8q_kv4_attention(q, c, table, torch.tensor([33, 64], dtype=torch.int32, device="cuda"), out, 0.1,
+                         q_indptr=torch.tensor([0, queries, 2 * queries], dtype=torch.int32, device="cuda"), lse=lse)
+    slots = torch.tensor([0, 5, -1], dtype=torch.int32, device="cuda")
+    rows = values(2, 3, Hkv, D).cuda()
+    f.fp8q_kv4_write(rows, rows, slots, c)
+    k, v = f.kv4_read(c, slots)
+    torch.cuda.synchronize()
+    assert bool((out == 0).all()) and bool((lse == -math.inf).all())
+    assert bool((k == 0).all()) and bool((v == 0).all())
+
+
 def test_no_queries_or_sequences():
     f = fq()
     c = f.alloc_kv4_cache(4, 16, 2, 64)
