@@ -1114,14 +1114,25 @@ constexpr int narrow_blocks(int DT, int64_t D) { return waves_per_simd(D, DT, na
 // no join.
 constexpr int tall_waves(int DT, int64_t D) { return waves_per_simd(D, DT, 2) * 4; }
 
-// Whether every unit has a tall block of its own. That costs about 7 us and 1.6 us for each of the
-// block's steps (one sequence, 8 cached heads of 128: 500 tokens 8.7 us, 1000 10.3, 2000 13.6, 4000
-// 19.6), the split 10.1 us with its join, and as much for each of its fewer steps (11.7, 11.7,
-// 12.1 and 11.8 us; 16 sequences of 4000 tokens 24.3 us against 21.8).
-bool tall_is_faster(int dtype, int64_t D, int64_t units, int64_t max_tokens, int64_t blocks) {
-  const int64_t tall = (max_tokens + 32 * tall_waves(dtype, D) - 1) / (32 * tall_waves(dtype, D));
-  const int64_t split = units * max_tokens / (blocks * 16 * narrow_halves(dtype, D) * kNarrowWaves) + 1;
-  return units <= current_device_shape().cus && (tall <= 2 || tall <= 2 * split);
+// How the narrow kernel's calls are cut: every unit whole, in a block of 4 waves or a tall one, or the
+// line split. The split has a plan, pieces in the workspace and a second launch, which cost about 6 us
+// more than the others' 5 us, but its time does not depend on how even the lengths are; the others
+// take as long as their longest unit, 1.3 us for each of a block's steps (tall: 1.65). So whole units
+// have a bounded number of steps (the longest unit then takes about twice the split's fixed time), and
+// those of tall blocks, up to one per CU, not more than three times the steps of the split's blocks. us
+// for whole, tall and split of B sequences and at most L tokens, 8 cached heads of 128:
+//   1 x  500  7.1  8.0 10.4    16 x  700  9.0  9.1 17.0    64 x  300 10.5 15.9 19.6
+//   1 x 2000 15   13.6 12.1    16 x 1500 15   12.4 19.2    64 x 1500 20.3 25.3 31.9
+//   2 x 4000 25   19.1 11.5    32 x 5000      33   39.6    64 x 3000 38.9 41.7 47
+enum class Cut { kWhole, kTall, kSplit };
+constexpr int kMostSteps = 16, kMostTallSteps = 12;
+
+Cut narrow_cut(int dtype, int64_t D, int64_t units, int64_t max_tokens, int64_t blocks) {
+  const int64_t step = 16 * narrow_halves(dtype, D) * kNarrowWaves, tall_step = 32 * tall_waves(dtype, D);
+  const int64_t whole = (max_tokens + step - 1) / step, tall = (max_tokens + tall_step - 1) / tall_step;
+  if (whole <= 2 || units >= 8 * blocks) return Cut::kWhole;
+  if (units > current_device_shape().cus) return whole <= kMostSteps ? Cut::kWhole : Cut::kSplit;
+  return tall <= kMostTallSteps && tall <= 3 * (units * max_tokens / (blocks * step) + 1) ? Cut::kTall : Cut::kSplit;
 }
 
 struct Shape {
@@ -1138,15 +1149,16 @@ Shape shape_of(int dtype, int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t
   s.rows = tile_rows(dtype, B, T, Hq, Hkv, D);
   s.units = Hkv * ((T * (Hq / Hkv) + s.rows - 1) / s.rows + B);
   const bool narrow = s.rows == kRows;
+  const int64_t rows_each = (T * (Hq / Hkv) + B - 1) / B;  // of a sequence and cached head, in the mean
   s.blocks = static_cast<int64_t>(current_device_shape().cus) * (narrow ? narrow_blocks(dtype, D) : 2);
-  s.tall = narrow && tall_is_faster(dtype, D, s.units, max_tokens, s.blocks);
+  const Cut cut = narrow ? narrow_cut(dtype, D, Hkv * B * ((rows_each + kRows - 1) / kRows), max_tokens, s.blocks)
+                  : s.units < s.blocks ? Cut::kSplit : Cut::kWhole;
+  s.tall = cut == Cut::kTall;
   // spans of 128 tokens, or longer ones where the line could have 2^31 places
   s.span_shift = 7;
   while (s.units * ((max_tokens >> s.span_shift) + 1) >= (int64_t(1) << 31)) s.span_shift++;
   s.plan_bytes = (2 * (B + 1) * 4 + 255) / 256 * 256;
-  // With many units the device is full without splitting; ragged lengths balance better with
-  // it, which the narrow kernel's small pieces are worth up to some rounds of blocks.
-  const bool split = !s.tall && max_tokens > (int64_t(kMinRun) << s.span_shift) && s.units < s.blocks * (narrow ? 8 : 1);
+  const bool split = cut == Cut::kSplit && max_tokens > (int64_t(kMinRun) << s.span_shift);
   s.bytes = split ? s.plan_bytes + (s.units + s.blocks) * (s.rows * (D + 2)) * 4 : 0;
   return s;
 }
@@ -1163,6 +1175,8 @@ struct Launch {
   void run() const {
     const size_t lds = 2 * (p.B + 1) * sizeof(int32_t);
     if constexpr (ROWS == kRows) {
+      // the plan of a tall call: at most one sequence per CU
+      static_assert(tall_waves(DT, D) * (32 * (D + kPadV) * 2 + 2 * kRows * 4 + 16) + 8 * 1024 <= 160 * 1024, "LDS of a CU");
       if (!SPLIT && shape.tall)
         hipLaunchKernelGGL((kv4_attention_kernel<D, DT, tall_waves(DT, D), 2, false, PAGE>), dim3(grid),
                            dim3(64 * tall_waves(DT, D)), lds, stream, p);

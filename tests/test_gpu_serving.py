@@ -363,6 +363,14 @@ def test_flat_softmax(D, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 64), (256, 8)])
+@pytest.mark.parametrize("most", [450, 1700, 9000])
+def test_ragged_queries_over_longer_caches(most, D, page, dtype):
+    """Few queries per sequence, the longest cache of one block's steps, of several, or split."""
+    check_attention([1, 3, 0, 6, 2], [most, 40, 300, most * 2 // 3, 1], 8, 2, D, page, dtype=dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("D,page", [(64, 1), (64, 64), (128, 16), (128, 64), (256, 16)])
 @pytest.mark.parametrize("queries", [3, 12, 90])
 def test_tokens_that_a_row_does_not_see(queries, D, page, dtype):
