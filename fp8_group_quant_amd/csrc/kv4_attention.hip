@@ -1135,6 +1135,20 @@ Cut narrow_cut(int dtype, int64_t D, int64_t units, int64_t max_tokens, int64_t 
   return tall <= kMostTallSteps && tall <= 3 * (units * max_tokens / (blocks * step) + 1) ? Cut::kTall : Cut::kSplit;
 }
 
+// The wide kernel's calls, by the same weighing: a step of a whole unit takes 1.4 us while its CU has one
+// block, the split about 9 steps more than its blocks' own, two of which share a CU. us whole and split,
+// 8 cached heads of 128, 4 query heads to each; sequences x queries of tokens:
+//   1 x 128 of 512  19.8 24.6    4 x 128 of 300   16.3 35.3    16 x 64 of  512  24.0 48.5
+//   1 x 128 of 1000 31.4 27.1    4 x 128 of 1000  33.4 38.4    16 x 64 of 2000  60.3 75.4
+//   8 x  17 of 1000 31.0 22.9    4 x 128 of 2000  56.7 46.9    16 x 64 of 8000 194  191
+constexpr int kMostWideSteps = 32;
+
+Cut wide_cut(int64_t units, int64_t max_tokens, int64_t blocks) {
+  const int64_t steps = (max_tokens + kStepW - 1) / kStepW;
+  if (units >= blocks) return Cut::kWhole;
+  return steps <= kMostWideSteps && steps <= 9 + 2 * units * steps / blocks ? Cut::kWhole : Cut::kSplit;
+}
+
 struct Shape {
   int rows;        // of a tile
   bool tall;
@@ -1149,10 +1163,10 @@ Shape shape_of(int dtype, int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t
   s.rows = tile_rows(dtype, B, T, Hq, Hkv, D);
   s.units = Hkv * ((T * (Hq / Hkv) + s.rows - 1) / s.rows + B);
   const bool narrow = s.rows == kRows;
-  const int64_t rows_each = (T * (Hq / Hkv) + B - 1) / B;  // of a sequence and cached head, in the mean
   s.blocks = static_cast<int64_t>(current_device_shape().cus) * (narrow ? narrow_blocks(dtype, D) : 2);
-  const Cut cut = narrow ? narrow_cut(dtype, D, Hkv * B * ((rows_each + kRows - 1) / kRows), max_tokens, s.blocks)
-                  : s.units < s.blocks ? Cut::kSplit : Cut::kWhole;
+  // units of sequences of mean length
+  const int64_t rows_each = (T * (Hq / Hkv) + B - 1) / B, units = Hkv * B * ((rows_each + s.rows - 1) / s.rows);
+  const Cut cut = narrow ? narrow_cut(dtype, D, units, max_tokens, s.blocks) : wide_cut(units, max_tokens, s.blocks);
   s.tall = cut == Cut::kTall;
   // spans of 128 tokens, or longer ones where the line could have 2^31 places
   s.span_shift = 7;

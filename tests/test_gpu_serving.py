@@ -371,6 +371,14 @@ def test_ragged_queries_over_longer_caches(most, D, page, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 64), (256, 32)])
+def test_many_queries_over_longer_caches(D, page, dtype):
+    """Many queries per sequence over a split cache: pieces of units that are cut between blocks."""
+    check_attention([40, 0, 25, 33], [2500, 10, 1500, 33], 4, 2, D, page, dtype=dtype)
+    check_attention([70, 21], [2200, 700], 8, 2, D, page, dtype=dtype, causal=False, q_scale=0.02)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("D,page", [(64, 1), (64, 64), (128, 16), (128, 64), (256, 16)])
 @pytest.mark.parametrize("queries", [3, 12, 90])
 def test_tokens_that_a_row_does_not_see(queries, D, page, dtype):
