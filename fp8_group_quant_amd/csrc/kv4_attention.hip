@@ -1095,13 +1095,20 @@ __global__ __launch_bounds__(64 * kJoinWaves) void kv4_join_kernel(Kv4AttnParams
 // Rows of the widest tile whose queries and outputs the registers hold.
 constexpr int widest(int dtype, int64_t D) { return D * (dtype == FP8Q_DTYPE_F16 ? 2 : 1) <= 128 ? 128 : 64; }
 
+constexpr int kMostWideSteps = 32;  // of a unit that the wide kernel does not split
+
 // Query rows of a tile. Up to two tiles of 16 rows per sequence (of mean length) and cached head
 // take the kernel whose waves share the tokens; more take the one whose waves share the rows. 16
 // sequences of 4096 tokens, 8 cached heads of 128, with 16, 64 and 128 rows to a tile: 32 rows 33,
-// 41 and 53 us; 36 rows 47, 41 and 54; 64 rows 50, 45 and 58; 96 rows 76, 73 and 63.
-int tile_rows(int dtype, int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D) {
-  const int64_t rows = (T * (Hq / Hkv) + B - 1) / B;
-  return rows <= 2 * kRows ? kRows : rows <= 64 ? 64 : widest(dtype, D);
+// 41 and 53 us; 36 rows 47, 41 and 54; 64 rows 50, 45 and 58; 96 rows 76, 73 and 63. The widest
+// tile shares each conversion of K and V among the most rows; where caches are short and there is no second
+// block for a CU anyway, 64 rows use more CUs and have the shorter steps (512 queries, 4 heads
+// to each of 8 cached: over 512 tokens 16.1 us, 20.6 with 128 rows, over 2000 43.2 and 46.3,
+// over 4000, split, 74 and 64).
+int tile_rows(int dtype, int64_t B, int64_t rows_each, int64_t Hkv, int64_t D, int64_t max_tokens) {
+  if (rows_each <= 2 * kRows) return kRows;
+  const bool one_each = Hkv * B * ((rows_each + 63) / 64) <= current_device_shape().cus;
+  return rows_each <= 64 || (one_each && max_tokens <= kMostWideSteps * kStepW) ? 64 : widest(dtype, D);
 }
 
 // The narrow kernel's split and general form: 16 N tokens per wave and step (64, but 32 where V's
@@ -1141,8 +1148,6 @@ Cut narrow_cut(int dtype, int64_t D, int64_t units, int64_t max_tokens, int64_t 
 //   1 x 128 of 512  19.8 24.6    4 x 128 of 300   16.3 35.3    16 x 64 of  512  24.0 48.5
 //   1 x 128 of 1000 31.4 27.1    4 x 128 of 1000  33.4 38.4    16 x 64 of 2000  60.3 75.4
 //   8 x  17 of 1000 31.0 22.9    4 x 128 of 2000  56.7 46.9    16 x 64 of 8000 194  191
-constexpr int kMostWideSteps = 32;
-
 Cut wide_cut(int64_t units, int64_t max_tokens, int64_t blocks) {
   const int64_t steps = (max_tokens + kStepW - 1) / kStepW;
   if (units >= blocks) return Cut::kWhole;
@@ -1160,12 +1165,13 @@ struct Shape {
 
 Shape shape_of(int dtype, int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_tokens) {
   Shape s;
-  s.rows = tile_rows(dtype, B, T, Hq, Hkv, D);
+  // rows and units of sequences of mean length
+  const int64_t rows_each = (T * (Hq / Hkv) + B - 1) / B;
+  s.rows = tile_rows(dtype, B, rows_each, Hkv, D, max_tokens);
+  const int64_t units = Hkv * B * ((rows_each + s.rows - 1) / s.rows);
   s.units = Hkv * ((T * (Hq / Hkv) + s.rows - 1) / s.rows + B);
   const bool narrow = s.rows == kRows;
   s.blocks = static_cast<int64_t>(current_device_shape().cus) * (narrow ? narrow_blocks(dtype, D) : 2);
-  // units of sequences of mean length
-  const int64_t rows_each = (T * (Hq / Hkv) + B - 1) / B, units = Hkv * B * ((rows_each + s.rows - 1) / s.rows);
   const Cut cut = narrow ? narrow_cut(dtype, D, units, max_tokens, s.blocks) : wide_cut(units, max_tokens, s.blocks);
   s.tall = cut == Cut::kTall;
   // spans of 128 tokens, or longer ones where the line could have 2^31 places

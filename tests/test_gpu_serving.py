@@ -379,6 +379,14 @@ def test_many_queries_over_longer_caches(D, page, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("D,page", [(64, 2), (64, 64), (128, 16), (128, 64), (256, 64)])
+def test_more_units_than_compute_units(D, page, dtype):
+    """So many query rows that the widest tiles are taken, and blocks take one unit after another."""
+    check_attention([150, 140, 90, 160], [300, 140, 200, 230], 32, 8, D, page, dtype=dtype)
+    check_attention([300, 140, 290, 160, 1], [300, 440, 200, 230, 0], 32, 8, D, page, dtype=dtype, causal=False, q_scale=0.05)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("D,page", [(64, 1), (64, 64), (128, 16), (128, 64), (256, 16)])
 @pytest.mark.parametrize("queries", [3, 12, 90])
 def test_tokens_that_a_row_does_not_see(queries, D, page, dtype):
