@@ -7,9 +7,11 @@
 // A row stays in registers between the sum of squares and the encode, so every input is read
 // once and every output written once: 7 bytes per bf16 element with a residual (x, residual
 // and its sum 2 each, the code 1). That traffic is what bounds it: 4096 x 7168 with a residual,
-// 206 MB, takes 40.2 us = 5.1 TB/s, the rate of a plain copy. The arithmetic, about 10 fp32
-// operations per element, shows in short rows without a residual (30011 x 576, fp16, 53 MB: 12.8
-// us = 4.2 TB/s). The row's sum of squares is fp32: four sums per lane by fma, then a tree.
+// 206 MB, takes 41.4 us = 5.0 TB/s, the rate of a plain copy. The arithmetic, about 10 fp32
+// operations per element, shows in short rows without a residual (30011 x 576, fp16, 53 MB: 14.3
+// us = 3.7 TB/s). The row's sum of squares is fp32: four sums per lane by fma, then a tree. The
+// factors are carried with their rounding errors, so that y has one rounding to fp32: of the codes
+// that a plain fp32 evaluation rounds to a neighbour's side of a tie, half are then right.
 #include <algorithm>
 
 #include "quant_device.h"
@@ -52,8 +54,12 @@ __device__ __forceinline__ u32x4 encode16_below448(const float (&v)[16], float i
 
 // LANES lanes of each of WPR waves share a row (64, or 16 of one wave), each lane holding CH times
 // 16 elements: lane and wave i take the elements [16 i, 16 i + 16) of every 16 * LANES * WPR.
+// Waves per SIMD that the registers are kept to: one register more than four waves have would cost a
+// quarter of the loads in flight (30011 x 576, fp16: 16.7 us).
+constexpr int norm_waves(int DT, int CH) { return CH == 3 && DT != FP8Q_DTYPE_F32 ? 4 : 1; }
+
 template <int DT, int LANES, int WPR, int CH>
-__global__ __launch_bounds__(WPR < 4 ? 256 : 64 * WPR) void rms_norm_quant_kernel(NormParams p) {
+__global__ __launch_bounds__(WPR < 4 ? 256 : 64 * WPR, norm_waves(DT, CH)) void rms_norm_quant_kernel(NormParams p) {
   static_assert(LANES == 64 || WPR == 1, "a row of 16 lanes is one wave's");
   constexpr int kWaves = WPR < 4 ? 4 : WPR;
   constexpr int kRows = kWaves / WPR * (64 / LANES);  // of a block
@@ -101,11 +107,19 @@ __global__ __launch_bounds__(WPR < 4 ? 256 : 64 * WPR) void rms_norm_quant_kerne
     if constexpr (WPR > 1) {
       if (lane == 0) part[par][0][wr][wi] = ss;
       __syncthreads();
-      ss = 0.0f;
+      float s[WPR];
 #pragma unroll
-      for (int i = 0; i < WPR; i++) ss += part[par][0][wr][i];
+      for (int i = 0; i < WPR; i++) s[i] = part[par][0][wr][i];
+#pragma unroll
+      for (int n = WPR / 2; n > 0; n /= 2)
+#pragma unroll
+        for (int i = 0; i < n; i++) s[i] += s[i + n];
+      ss = s[0];
     }
-    const float r = 1.0f / sqrtf(ss / p.k + p.eps);
+    // r + r_lo = 1 / sqrt(v) but for r_lo's own rounding (Newton's step, its residual by fma)
+    const float v = ss / p.k + p.eps, r = 1.0f / sqrtf(v), vr = v * r;
+    const float left = fmaf(-vr, r, 1.0f) - fmaf(v, r, -vr) * r;
+    const float r_lo = fabsf(left) < 1.0f ? 0.5f * r * left : 0.0f;  // v of 0 or infinity: no residual
     float amax[CH], row_max = 0.0f;
 #pragma unroll
     for (int i = 0; i < CH; i++) {
@@ -114,7 +128,8 @@ __global__ __launch_bounds__(WPR < 4 ? 256 : 64 * WPR) void rms_norm_quant_kerne
       amax[i] = 0.0f;
 #pragma unroll
       for (int j = 0; j < 16; j++) {
-        h[i][j] = (h[i][j] * r) * g[j];
+        const float hr = h[i][j] * r, hr_lo = fmaf(h[i][j], r_lo, fmaf(h[i][j], r, -hr));
+        h[i][j] = fmaf(hr, g[j], hr_lo * g[j]);
         amax[i] = fmaxf(amax[i], fabsf(h[i][j]));
       }
       if (p.group != 0) {
