@@ -7,7 +7,7 @@
 // A row stays in registers between the sum of squares and the encode, so every input is read
 // once and every output written once: 7 bytes per bf16 element with a residual (x, residual
 // and its sum 2 each, the code 1). That traffic is what bounds it: 4096 x 7168 with a residual,
-// 206 MB, takes 41.4 us = 5.0 TB/s, the rate of a plain copy. The arithmetic, about 10 fp32
+// 206 MB, takes 41.4 us = 5.0 TB/s, the rate of a plain copy. The arithmetic, about 13 fp32
 // operations per element, shows in short rows without a residual (30011 x 576, fp16, 53 MB: 14.3
 // us = 3.7 TB/s). The row's sum of squares is fp32: four sums per lane by fma, then a tree. The
 // factors are carried with their rounding errors, so that y has one rounding to fp32: of the codes
