@@ -6,20 +6,21 @@
 // One pass over the cache with a running maximum and sum per query row (fp32, base 2). Query
 // heads that share a cached head are rows of one tile, so the cache is read once for all.
 //
-// Tiles. A unit is 16, 64 or 128 query rows (tokens x heads of the group) of one cached head against
-// the sequence's cached tokens. With 16 rows the waves of a block share the tokens, 64 (or 32) of
-// a step each, with a running softmax of their own; their results meet in LDS at the end. With
-// more they share the rows (below). Short units are one block's. Long ones are cut: the units lie in a row, in spans of 128
-// tokens, and the row is cut into equal runs, one per block, wherever the cuts fall, so that every
-// block has the same work however ragged the lengths are. A unit that is cut leaves a piece per
-// block in the workspace, which a second kernel joins.
+// Tiles. A unit is 16, 64 or 128 query rows (tokens x heads of the group) of one cached head
+// against the sequence's cached tokens. With 16 rows the waves of a block share the tokens, 64 (or
+// 32) of a step each, with a running softmax of their own; their results meet in LDS at the end.
+// With more they share the rows (below). Short units are one block's. Long ones are cut: the units
+// lie in a row, in spans of 128 tokens, and the row is cut into equal runs, one per block, wherever
+// the cuts fall, so that every block has the same work however ragged the lengths are. A unit that
+// is cut leaves a piece per block in the workspace, which a second kernel joins.
 //
-// Bounds. Few rows: the cache's bytes. 64 sequences of 3300 to 8192 tokens, 64 heads on 8 cached ones
-// of 128: 408 MB in 86.6 us = 4.7 TB/s, and 5.9 us for the join. The loads decide it: with 32 tokens
-// to a step the whole took 102 us and its loads without any arithmetic 92 (a plain read of 4 KB
-// pieces in random order: 69). One sequence of 262144 tokens: 285 MB in 58.7 us = 4.9 TB/s. Many rows: the matrix pipe together with the vector pipe, which converts
-// K for every wave and exponentiates. 2 x 2048 queries of 32 heads over 8192 tokens, 386 GFLOP: 430 us =
-// 0.90 PFLOP/s, 0.76 of a large bf16 library product's rate.
+// Bounds. Few rows: the cache's bytes. 64 sequences of 3300 to 8192 tokens, 64 heads on 8 cached
+// ones of 128: 408 MB in 86.6 us = 4.7 TB/s, and 5.9 us for the join. The loads decide it: with 32
+// tokens to a step the whole took 102 us and its loads without any arithmetic 92 (a plain read of
+// 4 KB pieces in random order: 69). One sequence of 262144 tokens: 285 MB in 58.7 us = 4.9 TB/s.
+// Many rows: the matrix pipe together with the vector pipe, which converts K for every wave and
+// exponentiates. 2 x 2048 queries of 32 heads over 8192 tokens, 386 GFLOP: 430 us = 0.90 PFLOP/s,
+// 0.76 of a large bf16 library product's rate.
 //
 // Layouts (v_mfma_f32_16x16x32_bf16; lane l, r = l % 16, h = l / 16):
 //   S^T = K Q^T: lane (r, h) loads dims [D/4 h, D/4 (h + 1)) of token r, one or two scale blocks

@@ -56,10 +56,10 @@ __device__ __forceinline__ u32x4 encode16_below448(const float (&v)[16], float i
 // 16 elements: lane and wave i take the elements [16 i, 16 i + 16) of every 16 * LANES * WPR.
 // Waves per SIMD that the registers are kept to: one register more than four waves have would cost a
 // quarter of the loads in flight (30011 x 576, fp16: 16.7 us).
-constexpr int norm_waves(int DT, int CH) { return CH == 3 && DT != FP8Q_DTYPE_F32 ? 4 : 1; }
+constexpr int norm_waves(int CH) { return CH == 3 ? 4 : 1; }
 
 template <int DT, int LANES, int WPR, int CH>
-__global__ __launch_bounds__(WPR < 4 ? 256 : 64 * WPR, norm_waves(DT, CH)) void rms_norm_quant_kernel(NormParams p) {
+__global__ __launch_bounds__(WPR < 4 ? 256 : 64 * WPR, norm_waves(CH)) void rms_norm_quant_kernel(NormParams p) {
   static_assert(LANES == 64 || WPR == 1, "a row of 16 lanes is one wave's");
   constexpr int kWaves = WPR < 4 ? 4 : WPR;
   constexpr int kRows = kWaves / WPR * (64 / LANES);  // of a block
@@ -181,17 +181,19 @@ void launch_one(const NormParams& p, hipStream_t stream) {
 }
 
 // Lanes per row by its length: short rows share a wave, four to one (each lane's fixed work, about
-// 60 instructions for sums and scales, then serves up to 48 elements: 60000 x 256 takes 21.8 us,
+// 60 instructions for sums and scales, then serves up to 48 elements: 60000 x 256 takes 22.0 us,
 // 38 us with a wave per row); longer ones have 16 elements per lane and as many waves as that
 // takes, which is the most loads in flight (4096 x 7168: 8 waves 41.8 us, 4 waves of 32 elements
-// 42.7; one row of 7168: 3.2 and 3.7 us). Between 512 and 768 elements the registers decide: three
-// passes with a residual leave 4 waves per SIMD (30000 x 768: 35.7 us against 33.1 with a wave per
-// row; without a residual 15.0 against 15.7).
+// 42.7; one row of 7168: 3.3 and 3.7 us). Between 512 and 768 elements the registers decide: three
+// passes fit where there is no residual and 16-bit rows (30000 x 768: 16.9 us, 19.7 with a wave per
+// row; fp32 28.6 and 25.2; with a residual 35.7 and 33.1).
 template <int DT>
 void launch_dt(const NormParams& p, hipStream_t s) {
+  if constexpr (DT != FP8Q_DTYPE_F32) {
+    if (p.K > 512 && p.K <= 768 && !p.res) return launch_one<DT, 16, 1, 3>(p, s);
+  }
   if (p.K <= 256) launch_one<DT, 16, 1, 1>(p, s);
   else if (p.K <= 512) launch_one<DT, 16, 1, 2>(p, s);
-  else if (p.K <= 768 && !p.res) launch_one<DT, 16, 1, 3>(p, s);
   else if (p.K <= 1024) launch_one<DT, 64, 1, 1>(p, s);
   else if (p.K <= 2048) launch_one<DT, 64, 2, 1>(p, s);
   else if (p.K <= 4096) launch_one<DT, 64, 4, 1>(p, s);
