@@ -40,6 +40,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "kv4_attention_shape.h"
 #include "serving.h"
 #include "serving_device.h"
 
@@ -54,11 +55,9 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
-constexpr int kRows = 16;   // query rows of an item
 constexpr int kWideWaves = 4;  // of a block of the wide kernel
 constexpr int kJoinWaves = 4;
 constexpr int kPadV = 16;   // elements between the V rows in LDS
-constexpr int kMinRun = 2;  // spans of a block's run at least
 constexpr float kLn2 = 0.6931471805599453f;
 // Outputs are rescaled only when a row's maximum has grown by more than 2^8 since it last was:
 // probabilities then reach 2^8, which costs fp32 sums and bf16 factors no precision.
@@ -117,8 +116,9 @@ __device__ __forceinline__ int32_t spans_of(const Kv4AttnParams& p, const Seq& s
 // ------------------------------------------------------------------ units and runs
 // Prefixes over the sequences: first[b] the query tiles, line[b] the (tile, span) pairs before
 // sequence b. Unit (b, tile, head) is number (first[b] + tile) * Hkv + head and has the places
-// [line[b] * Hkv + (tile * Hkv + head) * spans, + spans) of the line of all spans. The host
-// chooses the span so that the line has fewer than 2^31 places.
+// [line[b] * Hkv + (tile * Hkv + head) * spans, + spans) of the line of all spans. For a
+// split call, which alone uses the line, the host chooses a span with which it has fewer than 2^31
+// places.
 struct Plan {
   int32_t* line;   // [B + 1]
   int32_t* first;  // [B + 1]
@@ -567,13 +567,6 @@ __device__ __forceinline__ bf16x8 read_v(const uint16_t* src, int d) {
   return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-// Waves per SIMD that the registers are kept to (O^T and Q take D / 4 + D / 8 of them per lane, a
-// step's codes N D / 16).
-constexpr int waves_per_simd(int64_t D, int DT, int N) {
-  if (D == 256 || (D == 128 && N == 4)) return 2;
-  return N == 4 || (DT == FP8Q_DTYPE_F16 && D == 128) ? 3 : 4;
-}
-
 template <int D, int DT, int WAVES, int N, bool SPLIT, int PAGE>
 __global__ __launch_bounds__(64 * WAVES, waves_per_simd(D, DT, N)) void kv4_attention_kernel(Kv4AttnParams p) {
   constexpr int PARTS = DT == FP8Q_DTYPE_F16 ? 2 : 1;
@@ -788,8 +781,6 @@ __global__ __launch_bounds__(64 * WAVES, waves_per_simd(D, DT, N)) void kv4_atte
 // step ahead of its use (two buffers, one barrier per step). Each of V's operands is read one product
 // ahead of its use (529 us for 2 x 2048 queries over 8192 tokens when the compiler placed the reads,
 // 484 so), and a step's 64 tokens take one page lookup where a page holds them (435).
-constexpr int kStepW = 64;
-
 // Waves per SIMD that the registers are kept to (fp16, D = 128, 64 rows: 451 us at 3, 468 at 2, for 2 x
 // 1024 queries of 32 heads over 8192 tokens; bf16, D = 64, 128 rows: 350 and 388 for 2 x 2048).
 constexpr int wide_waves_per_simd(int D, int DT, int QT, bool split) {
@@ -1103,102 +1094,11 @@ __global__ __launch_bounds__(64 * kJoinWaves) void kv4_join_kernel(Kv4AttnParams
 }
 
 // ------------------------------------------------------------------ launch
-// Rows of the widest tile whose queries and outputs the registers hold.
-constexpr int widest(int dtype, int64_t D) { return D * (dtype == FP8Q_DTYPE_F16 ? 2 : 1) <= 128 ? 128 : 64; }
-
-constexpr int kMostWideSteps = 32;  // of a unit that the wide kernel does not split
-
-// Query rows of a tile. Up to two tiles of 16 rows per sequence (of mean length) and cached head
-// take the kernel whose waves share the tokens; more take the one whose waves share the rows. 16
-// sequences of 4096 tokens, 8 cached heads of 128, with 16, 64 and 128 rows to a tile: 32 rows 33,
-// 41 and 53 us; 36 rows 47, 41 and 54; 64 rows 50, 45 and 58; 96 rows 76, 73 and 63. The widest
-// tile shares each conversion of K and V among the most rows; where caches are short and there is no second
-// block for a CU anyway, 64 rows use more CUs and have the shorter steps (512 queries, 4 heads
-// to each of 8 cached: over 512 tokens 16.1 us, 20.6 with 128 rows, over 2000 43.2 and 46.3,
-// over 4000, split, 74 and 64).
-int tile_rows(int dtype, int64_t B, int64_t rows_each, int64_t Hkv, int64_t D, int64_t max_tokens) {
-  if (rows_each <= 2 * kRows) return kRows;
-  const bool one_each = Hkv * B * ((rows_each + 63) / 64) <= current_device_shape().cus;
-  return rows_each <= 64 || (one_each && max_tokens <= kMostWideSteps * kStepW) ? 64 : widest(dtype, D);
-}
-
-// The narrow kernel's split and general form: 16 N tokens per wave and step (64, but 32 where V's
-// rows in LDS and the codes' registers leave no room), in blocks of 4 waves.
-constexpr int narrow_halves(int DT, int64_t D) { return D == 256 || (D == 128 && DT == FP8Q_DTYPE_F16) ? 2 : 4; }
-constexpr int kNarrowWaves = 4;
-constexpr int narrow_blocks(int DT, int64_t D) { return waves_per_simd(D, DT, narrow_halves(DT, D)) * 4 / kNarrowWaves; }
-
-// Blocks for short caches: all the waves that a CU holds, so that a unit needs no second block and
-// no join.
-constexpr int tall_waves(int DT, int64_t D) { return waves_per_simd(D, DT, 2) * 4; }
-
-// How the narrow kernel's calls are cut: every unit whole, in a block of 4 waves or a tall one, or the
-// line split. The split has a plan, pieces in the workspace and a second launch, which cost about 6 us
-// more than the others' 5 us, but its time does not depend on how even the lengths are; the others
-// take as long as their longest unit, 1.3 us for each of a block's steps (tall: 1.65). So whole units
-// have a bounded number of steps (the longest unit then takes about twice the split's fixed time), and
-// those of tall blocks, up to one per CU, not more than three times the steps of the split's blocks. us
-// for whole, tall and split of B sequences and at most L tokens, 8 cached heads of 128:
-//   1 x  500  7.1  8.0 10.4    16 x  700  9.0  9.1 17.0    64 x  300 10.5 15.9 19.6
-//   1 x 2000 15   13.6 12.1    16 x 1500 15   12.4 19.2    64 x 1500 20.3 25.3 31.9
-//   2 x 4000 25   19.1 11.5    32 x 5000      33   39.6    64 x 3000 38.9 41.7 47
-enum class Cut { kWhole, kTall, kSplit };
-constexpr int kMostSteps = 16, kMostTallSteps = 12;
-
-Cut narrow_cut(int dtype, int64_t D, int64_t units, int64_t max_tokens, int64_t blocks) {
-  const int64_t step = 16 * narrow_halves(dtype, D) * kNarrowWaves, tall_step = 32 * tall_waves(dtype, D);
-  const int64_t whole = (max_tokens + step - 1) / step, tall = (max_tokens + tall_step - 1) / tall_step;
-  if (whole <= 2 || units >= 8 * blocks) return Cut::kWhole;
-  if (units > current_device_shape().cus) return whole <= kMostSteps ? Cut::kWhole : Cut::kSplit;
-  return tall <= kMostTallSteps && tall <= 3 * (units * max_tokens / (blocks * step) + 1) ? Cut::kTall : Cut::kSplit;
-}
-
-// The wide kernel's calls, by the same weighing: a step of a whole unit takes 1.4 us while its CU has one
-// block, the split about 9 steps more than its blocks' own, two of which share a CU. us whole and split,
-// 8 cached heads of 128, 4 query heads to each; sequences x queries of tokens:
-//   1 x 128 of 512  19.8 24.6    4 x 128 of 300   16.3 35.3    16 x 64 of  512  24.0 48.5
-//   1 x 128 of 1000 31.4 27.1    4 x 128 of 1000  33.4 38.4    16 x 64 of 2000  60.3 75.4
-//   8 x  17 of 1000 31.0 22.9    4 x 128 of 2000  56.7 46.9    16 x 64 of 8000 194  191
-Cut wide_cut(int64_t units, int64_t max_tokens, int64_t blocks) {
-  const int64_t steps = (max_tokens + kStepW - 1) / kStepW;
-  if (units >= blocks) return Cut::kWhole;
-  return steps <= kMostWideSteps && steps <= 9 + 2 * units * steps / blocks ? Cut::kWhole : Cut::kSplit;
-}
-
-struct Shape {
-  int rows;        // of a tile
-  bool tall;
-  int64_t units;   // at most
-  int64_t blocks;  // that a split call's work is cut for: those that run at once
-  int span_shift;
-  int64_t plan_bytes, bytes;  // workspace; 0: no split
-};
-
-Shape shape_of(int dtype, int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_tokens) {
-  Shape s;
-  // rows and units of sequences of mean length
-  const int64_t rows_each = (T * (Hq / Hkv) + B - 1) / B;
-  s.rows = tile_rows(dtype, B, rows_each, Hkv, D, max_tokens);
-  const int64_t units = Hkv * B * ((rows_each + s.rows - 1) / s.rows);
-  s.units = Hkv * ((T * (Hq / Hkv) + s.rows - 1) / s.rows + B);
-  const bool narrow = s.rows == kRows;
-  s.blocks = static_cast<int64_t>(current_device_shape().cus) * (narrow ? narrow_blocks(dtype, D) : 2);
-  const Cut cut = narrow ? narrow_cut(dtype, D, units, max_tokens, s.blocks) : wide_cut(units, max_tokens, s.blocks);
-  s.tall = cut == Cut::kTall;
-  // spans of 128 tokens, or longer ones where the line could have 2^31 places
-  s.span_shift = 7;
-  while (s.units * ((max_tokens >> s.span_shift) + 1) >= (int64_t(1) << 31)) s.span_shift++;
-  s.plan_bytes = (2 * (B + 1) * 4 + 255) / 256 * 256;
-  const bool split = cut == Cut::kSplit && max_tokens > (int64_t(kMinRun) << s.span_shift);
-  s.bytes = split ? s.plan_bytes + (s.units + s.blocks) * (s.rows * (D + 2)) * 4 : 0;
-  return s;
-}
-
 struct Launch {
   const Kv4AttnParams& p;
   bool split;
   int page;  // kByToken, kBy16, kByStep
-  const Shape& shape;
+  const AttnShape& shape;
   unsigned grid;
   hipStream_t stream;
 
@@ -1255,11 +1155,11 @@ struct Launch {
 }  // namespace
 
 int64_t kv4_attention_workspace(int dtype, int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_tokens) {
-  return shape_of(dtype, B, T, Hq, Hkv, D, max_tokens).bytes;
+  return attention_shape(current_device_shape().cus, dtype, B, T, Hq, Hkv, D, max_tokens).bytes;
 }
 
 int launch_kv4_attention(int dtype, int64_t D, Kv4AttnParams p, void* ws, int64_t ws_bytes, hipStream_t stream) {
-  const Shape s = shape_of(dtype, p.B, p.T, p.Hq, p.Hkv, D, p.max_tokens);
+  const AttnShape s = attention_shape(current_device_shape().cus, dtype, p.B, p.T, p.Hq, p.Hkv, D, p.max_tokens);
   const bool split = s.bytes > 0 && ws && ws_bytes >= s.bytes;
   p.max_units = s.units;
   p.span_shift = s.span_shift;
