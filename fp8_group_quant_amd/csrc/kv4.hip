@@ -110,18 +110,43 @@ __device__ __forceinline__ uint32_t encode8(const Raw8<DT>& r, float scale) {
   return c;
 }
 
-// The values of 8 codes. Exact in bf16 and fp32; fp16 is rounded from the exact value.
+// Whether 6, the largest code, at this scale byte passes the type's largest finite value. (255 is no
+// scale: its values are NaN, and stay so.)
 template <int DT>
-__device__ __forceinline__ Raw8<DT> decode8(uint32_t c, float scale) {
+__device__ __forceinline__ bool may_overflow(uint32_t byte) {
+  constexpr uint32_t kFirst = DT == FP8Q_DTYPE_F16 ? 127 + 14 : 127 + 126;
+  return byte - kFirst < 255u - kFirst;
+}
+
+// The values of 8 codes, those past the type's largest finite value as that value. Else exact in bf16
+// and fp32; fp16 is rounded from the exact value.
+template <int DT>
+__device__ __forceinline__ Raw8<DT> decode8(uint32_t c, uint32_t byte) {
+  const float scale = __uint_as_float(byte << 23);
   Raw8<DT> r;
   if constexpr (DT == FP8Q_DTYPE_BF16) {
     r.w[0][0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 0));
     r.w[0][1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 1));
     r.w[0][2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 2));
     r.w[0][3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 3));
+    if (may_overflow<DT>(byte)) {
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const u16x2 mag = __builtin_elementwise_min(pair<u16x2>(r.w[0][i] & 0x7FFF7FFFu), u16x2{0x7F7F, 0x7F7F});
+        r.w[0][i] = (r.w[0][i] & 0x80008000u) | __builtin_bit_cast(uint32_t, mag);
+      }
+    }
   } else {
-    const f32x2 v[4] = {__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, scale, 0), __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, scale, 1),
-                        __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, scale, 2), __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, scale, 3)};
+    f32x2 v[4] = {__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, scale, 0), __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, scale, 1),
+                  __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, scale, 2), __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, scale, 3)};
+    if (may_overflow<DT>(byte)) {
+      constexpr float kMost = DT == FP8Q_DTYPE_F16 ? 65504.0f : __FLT_MAX__;
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        v[i].x = fminf(fmaxf(v[i].x, -kMost), kMost);
+        v[i].y = fminf(fmaxf(v[i].y, -kMost), kMost);
+      }
+    }
 #pragma unroll
     for (int i = 0; i < 4; i++) {
       if constexpr (DT == FP8Q_DTYPE_F16) {
@@ -220,7 +245,7 @@ __global__ __launch_bounds__(kThreads) void kv4_read_kernel(Kv4RowsParams p, Gri
 #pragma unroll
   for (int i = 0; i < kTok; i++) {
     if (at.t + i >= p.T) break;
-    const Raw8<DT> r = decode8<DT>(c[i], __uint_as_float(byte[i] << 23));
+    const Raw8<DT> r = decode8<DT>(c[i], byte[i]);
 #pragma unroll
     for (int j = 0; j < kEsz / 2; j++) reinterpret_cast<u32x4*>(x + i * p.x_st[which] * kEsz)[j] = r.w[j];
   }

@@ -385,8 +385,10 @@ int fp8q_kv4_write(const void* k, int64_t k_st, int64_t k_sh,
  * fp8q_kv4_read — reads T slots of the cache back as rows of out_dtype
  *
  * The arguments of fp8q_kv4_write with k and v as outputs: row t gets the values that slot
- * slots[t] holds, rounded to out_dtype (exact in BF16 and F32); a slot outside the cache gives
- * zeros. Output rows must not overlap [EINVAL].
+ * slots[t] holds, rounded to out_dtype (exact in BF16 and F32); a value past the type's largest
+ * finite one becomes that one. (Codes round up: 57344 and more written in F16 are held as 65536,
+ * 2.98e38 and more in BF16 or F32 as 2^128, and are read back as the largest finite value.) A
+ * slot outside the cache gives zeros. Output rows must not overlap [EINVAL].
  */
 int fp8q_kv4_read(void* k, int64_t k_st, int64_t k_sh,
                   void* v, int64_t v_st, int64_t v_sh,

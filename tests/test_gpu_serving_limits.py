@@ -17,6 +17,49 @@ def gen(seed):
     return torch.Generator().manual_seed(seed)
 
 
+def saturated(v, dtype):
+    """float64 values rounded to dtype, those past its largest finite value as that value."""
+    most = torch.finfo(dtype).max
+    return v.clamp(-most, most).to(dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+def test_largest_finite_values_read_back_finite(dtype):
+    """Codes round up to 4 / 3.5 of a value: the largest finite inputs are held as more than their type
+    has, and come back as its largest finite value."""
+    f = fq()
+    most = torch.finfo(dtype).max
+    steps = torch.cat([torch.linspace(0.80, 1.0, 63, dtype=torch.float64), torch.tensor([57344 / 65504], dtype=torch.float64)])
+    x = (most * steps).to(dtype).reshape(64, 1, 1) * torch.tensor([1.0, -1.0] * 32, dtype=dtype)
+    assert bool(torch.isfinite(x).all())
+    n = x.shape[0]
+    c = f.alloc_kv4_cache(n, 1, 1, 128)
+    x = torch.cat([x, x / 3], -1).cuda()
+    slots = torch.arange(n, dtype=torch.int32).cuda()
+    f.fp8q_kv4_write(x, -x, slots, c)
+    k, v = f.kv4_read(c, slots, dtype)
+    torch.cuda.synchronize()
+    exp = saturated(ref.dequantize(*ref.quantize(x.cpu())), dtype)
+    assert bool(torch.isfinite(k).all()) and bool((k.abs() == most).any())
+    assert torch.equal(k.cpu(), exp) and torch.equal(v.cpu(), -exp)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+def test_every_scale_byte_reads_back(dtype):
+    """Every code at every scale byte that is a number."""
+    f = fq()
+    c = f.alloc_kv4_cache(255, 1, 1, 64)
+    codes = torch.arange(16).repeat(4)
+    packed = (codes[0::2] | (codes[1::2] << 4)).to(torch.uint8)
+    for t in (c.k, c.v):
+        t.copy_(packed.cuda().expand(t.shape))
+    for t in (c.k_scales, c.v_scales):
+        t.copy_(torch.arange(255, dtype=torch.uint8).cuda().reshape(-1, 1, 1, 1).expand(t.shape))
+    k, v = f.kv4_read(c, torch.arange(255, dtype=torch.int32).cuda(), dtype)
+    exp = saturated(ref.dequantize(c.k.cpu(), c.k_scales.cpu())[:, 0], dtype)
+    assert torch.equal(k.cpu(), exp) and torch.equal(v.cpu(), exp)
+
+
 def test_many_heads_and_sequences():
     """One query of 2^19 heads in one of 4096 sequences: more (sequence, head) pairs than 2^31. A
     cache of one token makes the softmax 1, so the outputs are its values."""
