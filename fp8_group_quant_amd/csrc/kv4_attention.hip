@@ -558,6 +558,18 @@ __device__ __forceinline__ void split8(u32x4 raw, uint32_t sign, bf16x8 (&out)[P
   }
 }
 
+// Two outputs rounded to their type. The cache holds up to 98304 of fp16's 65504 (codes round up): an
+// average past the largest finite value becomes that value. bf16 has every value's range.
+template <int DT>
+__device__ __forceinline__ uint32_t pack_out(float a, float b) {
+  if constexpr (DT == FP8Q_DTYPE_F16) {
+    constexpr float kMost = 65504.0f;
+    a = fabsf(a) > kMost ? copysignf(kMost, a) : a;  // (NaN stays)
+    b = fabsf(b) > kMost ? copysignf(kMost, b) : b;
+  }
+  return pack16<DT>(a, b);
+}
+
 // V^T's operand for dims 16 d .. + 15 and the 32 tokens whose rows start at `src` (of lane (r, h): row
 // 4h + r / 4, element 4 (r % 4)).
 template <int ROW>
@@ -764,7 +776,7 @@ __global__ __launch_bounds__(64 * WAVES, waves_per_simd(D, DT, N)) void kv4_atte
         const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
         u32x4 bits;
 #pragma unroll
-        for (int j = 0; j < 4; j++) bits[j] = pack16<DT>(v[2 * j] * inv, v[2 * j + 1] * inv);
+        for (int j = 0; j < 4; j++) bits[j] = pack_out<DT>(v[2 * j] * inv, v[2 * j + 1] * inv);
         *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p.out) + row_t * p.o_st + hh * p.o_sh + col) = bits;
         if (p.lse && col == 0)
           p.lse[row_t * p.l_st + hh] = ll == 0.0f ? kNegInf : (mm + __builtin_amdgcn_logf(ll)) * kLn2;
@@ -1010,7 +1022,7 @@ __global__ __launch_bounds__(64 * kWideWaves, wide_waves_per_simd(D, DT, QT, SPL
 #pragma unroll
         for (int d = 0; d < kDims; d++)
           *reinterpret_cast<u32x2*>(dst + 16 * d) =
-              u32x2{pack16<DT>(o[n][d][0] * inv, o[n][d][1] * inv), pack16<DT>(o[n][d][2] * inv, o[n][d][3] * inv)};
+              u32x2{pack_out<DT>(o[n][d][0] * inv, o[n][d][1] * inv), pack_out<DT>(o[n][d][2] * inv, o[n][d][3] * inv)};
         if (p.lse && h == 0)
           p.lse[row_t * p.l_st + hh] = sum == 0.0f ? kNegInf : (m[n] + __builtin_amdgcn_logf(sum)) * kLn2;
       }
@@ -1085,10 +1097,10 @@ __global__ __launch_bounds__(64 * kJoinWaves) void kv4_join_kernel(Kv4AttnParams
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   uint16_t* dst = static_cast<uint16_t*>(p.out) + t * p.o_st + qh * p.o_sh + kPer * lane;
   if constexpr (kPer == 1) {
-    *dst = static_cast<uint16_t>(pack16<DT>(acc[0] * inv, 0.0f));
+    *dst = static_cast<uint16_t>(pack_out<DT>(acc[0] * inv, 0.0f));
   } else {
 #pragma unroll
-    for (int i = 0; i < kPer; i += 2) *reinterpret_cast<uint32_t*>(dst + i) = pack16<DT>(acc[i] * inv, acc[i + 1] * inv);
+    for (int i = 0; i < kPer; i += 2) *reinterpret_cast<uint32_t*>(dst + i) = pack_out<DT>(acc[i] * inv, acc[i + 1] * inv);
   }
   if (p.lse && lane == 0) p.lse[t * p.l_st + qh] = l == 0.0f ? kNegInf : (ts + __builtin_amdgcn_logf(l)) * kLn2;
 }

@@ -416,7 +416,8 @@ int fp8q_kv4_read(void* k, int64_t k_st, int64_t k_sh,
  * written. Cached bytes past a sequence's length, and table entries past its pages, are never
  * used; cached bytes of tokens that a row does not see, whatever they are, do not reach its
  * results. For that, values' scales above 2^125 (bytes above 252, which the write stores only for
- * magnitudes above 2.5e38) count as 2^125. Scores, sums and the output are accumulated in fp32.
+ * magnitudes above 2.5e38) count as 2^125. Scores, sums and the output are accumulated in fp32;
+ * outputs past the type's largest finite value become that value.
  *
  * fp8q_kv4_attention_workspace_size returns the bytes of workspace with which the call splits
  * long caches over more of the device (max_tokens = max_pages * page_size; 0: it needs none, or

@@ -60,6 +60,25 @@ def test_every_scale_byte_reads_back(dtype):
     assert torch.equal(k.cpu(), exp) and torch.equal(v.cpu(), exp)
 
 
+@pytest.mark.parametrize("queries,tokens", [(1, 1), (1, 70), (3, 3000), (40, 100), (40, 2500)])
+def test_fp16_outputs_stay_finite(queries, tokens):
+    """Values at the top of fp16, all held as 65536 (and half of them negative): averages of one sign are
+    the largest finite value, whole units and joined pieces alike."""
+    f = fq()
+    D, page = 64, 16
+    pages = -(-tokens // page)
+    c = f.alloc_kv4_cache(pages, page, 1, D)
+    sign = torch.tensor([1.0, -1.0] * 32)
+    v = (torch.linspace(57344, 65504, tokens)[:, None, None] * sign).to(torch.float16).cuda()
+    k = torch.randn(tokens, 1, D, generator=gen(3)).to(torch.float16).cuda()
+    f.fp8q_kv4_write(k, v, torch.arange(tokens, dtype=torch.int32).cuda(), c)
+    q = torch.randn(queries, 2, D, generator=gen(4)).to(torch.float16).cuda()
+    args = (q, c, torch.arange(pages, dtype=torch.int32).cuda()[None], torch.tensor([tokens], dtype=torch.int32).cuda())
+    out = f.kv4_attention(*args, 0.125, causal=False, q_indptr=torch.tensor([0, queries], dtype=torch.int32).cuda())
+    torch.cuda.synchronize()
+    assert torch.equal(out.cpu(), (65504 * sign).to(torch.float16).expand(out.shape))
+
+
 def test_many_heads_and_sequences():
     """One query of 2^19 heads in one of 4096 sequences: more (sequence, head) pairs than 2^31. A
     cache of one token makes the softmax 1, so the outputs are its values."""
