@@ -242,12 +242,21 @@ __global__ __launch_bounds__(kThreads) void kv4_read_kernel(Kv4RowsParams p, Gri
     }
   }
   uint8_t* x = static_cast<uint8_t*>(p.x[which]) + (at.t * p.x_st[which] + at.head * p.x_sh[which] + at.d) * kEsz;
+  // Tokens decoded together before their stores, by the type: the check for infinities between the stores
+  // costs more than its instructions. us for 1, 2 and 4: 131072 tokens of 8 x 128 in bf16 134, 131 and
+  // 136 (128 without the check), 65536 in fp16 67, 68 and 72 (67), in fp32 142, - and 117 (125).
+  constexpr int kAhead = DT == FP8Q_DTYPE_F32 ? 4 : 2;
 #pragma unroll
-  for (int i = 0; i < kTok; i++) {
-    if (at.t + i >= p.T) break;
-    const Raw8<DT> r = decode8<DT>(c[i], byte[i]);
+  for (int i = 0; i < kTok; i += kAhead) {
+    Raw8<DT> r[kAhead];
 #pragma unroll
-    for (int j = 0; j < kEsz / 2; j++) reinterpret_cast<u32x4*>(x + i * p.x_st[which] * kEsz)[j] = r.w[j];
+    for (int a = 0; a < kAhead; a++) r[a] = decode8<DT>(c[i + a], byte[i + a]);
+#pragma unroll
+    for (int a = 0; a < kAhead; a++) {
+      if (at.t + i + a >= p.T) return;
+#pragma unroll
+      for (int j = 0; j < kEsz / 2; j++) reinterpret_cast<u32x4*>(x + (i + a) * p.x_st[which] * kEsz)[j] = r[a].w[j];
+    }
   }
 }
 
