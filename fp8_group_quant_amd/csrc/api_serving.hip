@@ -259,7 +259,7 @@ int attention_entry(const void* q, int dtype, int64_t q_st, int64_t q_sh, const 
   p.Hkv = static_cast<int32_t>(Hkv);
   p.group = static_cast<int32_t>(Hq / Hkv);
   // a scale of zero stays above the smallest numbers, so that a masked score times it is -infinity
-  p.scale_log2 = std::max(std::fabs(sm_scale) * 1.4426950408889634f, 1e-30f);
+  p.scale_log2 = std::max(std::fabs(sm_scale) * 5.770780163555854f, 1e-30f);
   p.q_sign = sm_scale < 0.0f ? 0x80008000u : 0u;
   p.causal = causal != 0;
   return launch_kv4_attention(dtype, D, p, workspace, workspace_bytes, static_cast<hipStream_t>(stream));

@@ -369,12 +369,24 @@ __device__ __forceinline__ void spread_scales(const Scales<D>& s, int h, Mult<D>
   for (int c = 0; c < N; c++) m[c] = mult_of<D>(half[c], h);
 }
 
-// Values' scales above 2^125 count as 2^125: every value is then finite, and one that a row does not
-// see, whatever its bytes are, adds 0 times it, which is 0.
+// Keys and values are converted as a quarter of themselves, which bf16 holds whatever the scale is: up to
+// 6 * 2^127 cached (codes round up, so finite rows of the model's type are held as up to 2^128), of which
+// a quarter is finite. Scores are then multiplied by four times the scale, outputs by four times
+// the sum's reciprocal: all exact. (Scale bytes 0 and 1, which the write never stores, count as 2.)
+__device__ __forceinline__ float quarter(float pow2) {
+  return __uint_as_float(__builtin_elementwise_sub_sat(__float_as_uint(pow2), 2u << 23));
+}
 template <int D>
-__device__ __forceinline__ void keep_finite(Mult<D>& m) {
+__device__ __forceinline__ void quarter_keys(Mult<D>& m) {
 #pragma unroll
-  for (int i = 0; i < (D == 256 ? 2 : 1); i++) m.f[i] = __uint_as_float(min(__float_as_uint(m.f[i]), (125u + 127u) << 23));
+  for (int i = 0; i < (D == 256 ? 2 : 1); i++) m.f[i] = quarter(m.f[i]);
+}
+// Values also where a scale byte is 255, which is no number: a value that a row does not see, whatever
+// its bytes are, adds 0 times a finite number, which is 0.
+template <int D>
+__device__ __forceinline__ void quarter_values(Mult<D>& m) {
+#pragma unroll
+  for (int i = 0; i < (D == 256 ? 2 : 1); i++) m.f[i] = quarter(__uint_as_float(min(__float_as_uint(m.f[i]), 254u << 23)));
 }
 
 template <int D>
@@ -558,15 +570,13 @@ __device__ __forceinline__ void split8(u32x4 raw, uint32_t sign, bf16x8 (&out)[P
   }
 }
 
-// Two outputs rounded to their type. The cache holds up to 98304 of fp16's 65504 (codes round up): an
-// average past the largest finite value becomes that value. bf16 has every value's range.
+// Two outputs rounded to their type, an average past its largest finite value as that value: the cache
+// holds up to 98304 of fp16's 65504 and 2^128 of bf16's (codes round up). (NaN stays.)
 template <int DT>
 __device__ __forceinline__ uint32_t pack_out(float a, float b) {
-  if constexpr (DT == FP8Q_DTYPE_F16) {
-    constexpr float kMost = 65504.0f;
-    a = fabsf(a) > kMost ? copysignf(kMost, a) : a;  // (NaN stays)
-    b = fabsf(b) > kMost ? copysignf(kMost, b) : b;
-  }
+  constexpr float kMost = DT == FP8Q_DTYPE_F16 ? 65504.0f : 0x1.FEp127f;
+  a = fabsf(a) > kMost ? copysignf(kMost, a) : a;
+  b = fabsf(b) > kMost ? copysignf(kMost, b) : b;
   return pack16<DT>(a, b);
 }
 
@@ -644,6 +654,7 @@ __global__ __launch_bounds__(64 * WAVES, waves_per_simd(D, DT, N)) void kv4_atte
 #pragma unroll
       for (int c = 0; c < N; c++) {
         s[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+        quarter_keys<D>(mk[c]);
 #pragma unroll
         for (int j = 0; j < kSteps; j++) {
           const bf16x8 k = widen_codes<D>(st.k[c], mk[c], j);
@@ -656,7 +667,7 @@ __global__ __launch_bounds__(64 * WAVES, waves_per_simd(D, DT, N)) void kv4_atte
       spread_scales<D, N>(st.vs, h, mv);
 #pragma unroll
       for (int c = 0; c < N; c++) {
-        keep_finite<D>(mv[c]);
+        quarter_values<D>(mv[c]);
         if (there != kAllThere<N> && ((there >> (16 * c + r)) & 1u) == 0u) {
           zero_codes<D>(st.v[c]);
           one_mult<D>(mv[c]);
@@ -773,7 +784,7 @@ __global__ __launch_bounds__(64 * WAVES, waves_per_simd(D, DT, N)) void kv4_atte
       } else {
         const int32_t i = (first + row) / p.group;
         const int64_t row_t = seq.q0 + i, hh = head * p.group + first + row - i * p.group;
-        const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
+        const float inv = ll == 0.0f ? 0.0f : 4.0f / ll;
         u32x4 bits;
 #pragma unroll
         for (int j = 0; j < 4; j++) bits[j] = pack_out<DT>(v[2 * j] * inv, v[2 * j + 1] * inv);
@@ -849,7 +860,7 @@ __global__ __launch_bounds__(64 * kWideWaves, wide_waves_per_simd(D, DT, QT, SPL
     auto pages_v = [&](int32_t t) { return load_pages<PAGE, 1>(p, table, t + 16 * wave, t_end); };
     auto put_v = [&](int buf) {
       Mult<D> mv = mult_of<D>(vs, h);
-      keep_finite<D>(mv);
+      quarter_values<D>(mv);
       if (((v_there >> r) & 1u) == 0u) {
         zero_codes<D>(v);
         one_mult<D>(mv);
@@ -918,6 +929,7 @@ __global__ __launch_bounds__(64 * kWideWaves, wide_waves_per_simd(D, DT, QT, SPL
       for (int c = 0; c < kHalves; c++) {
         Mult<D> mk[2];
         spread_scales<D, 2>(ks[c / 2], h, mk);
+        quarter_keys<D>(mk[c % 2]);
 #pragma unroll
         for (int n = 0; n < QT; n++) s[n][c] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -1017,7 +1029,7 @@ __global__ __launch_bounds__(64 * kWideWaves, wide_waves_per_simd(D, DT, QT, SPL
       } else {
         const int32_t i = row / p.group;
         const int64_t row_t = seq.q0 + i, hh = head * p.group + row - i * p.group;
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        const float inv = sum == 0.0f ? 0.0f : 4.0f / sum;
         uint16_t* dst = static_cast<uint16_t*>(p.out) + row_t * p.o_st + hh * p.o_sh + 4 * h;
 #pragma unroll
         for (int d = 0; d < kDims; d++)
@@ -1094,7 +1106,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void kv4_join_kernel(Kv4AttnParams
       for (int i = 0; i < kPer; i++) acc[i] += lds_o[w][kPer * lane + i];
     }
   }
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  const float inv = l == 0.0f ? 0.0f : 4.0f / l;
   uint16_t* dst = static_cast<uint16_t*>(p.out) + t * p.o_st + qh * p.o_sh + kPer * lane;
   if constexpr (kPer == 1) {
     *dst = static_cast<uint16_t>(pack_out<DT>(acc[0] * inv, 0.0f));

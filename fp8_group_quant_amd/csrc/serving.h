@@ -70,7 +70,7 @@ struct Kv4AttnParams {
   const int32_t* q_indptr;   // [B + 1], or nullptr: sequence b is row b
   int64_t B, T;
   int32_t Hq, Hkv, group;    // group = Hq / Hkv
-  float scale_log2;          // magnitude of the softmax scale times log2(e)
+  float scale_log2;          // magnitude of the softmax scale times 4 log2(e)
   uint32_t q_sign;           // 0x80008000 where the scale is negative
   int32_t causal;
   int32_t span_shift;        // log2 of the tokens of a span

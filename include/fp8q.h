@@ -415,9 +415,10 @@ int fp8q_kv4_read(void* k, int64_t k_st, int64_t k_sh,
  * A row that sees no token gets zeros, and -infinity in lse. Rows of q in no sequence are not
  * written. Cached bytes past a sequence's length, and table entries past its pages, are never
  * used; cached bytes of tokens that a row does not see, whatever they are, do not reach its
- * results. For that, values' scales above 2^125 (bytes above 252, which the write stores only for
- * magnitudes above 2.5e38) count as 2^125. Scores, sums and the output are accumulated in fp32;
- * outputs past the type's largest finite value become that value.
+ * results. Scale bytes 0 and 1, which the write never stores, count as 2; 255 is no scale. Scores,
+ * sums and the output are accumulated in fp32, and must stay inside it: sum_d |q_d k_d| and
+ * sm_scale times it below 2^127, the cached values that a sequence sees below 2^122 / kv_lens[b].
+ * Outputs past the type's largest finite value become that value.
  *
  * fp8q_kv4_attention_workspace_size returns the bytes of workspace with which the call splits
  * long caches over more of the device (max_tokens = max_pages * page_size; 0: it needs none, or

@@ -79,6 +79,57 @@ def test_fp16_outputs_stay_finite(queries, tokens):
     assert torch.equal(out.cpu(), (65504 * sign).to(torch.float16).expand(out.shape))
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("queries", [1, 40])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_values_at_every_scale(D, queries, dtype):
+    """Caches of one token, whose softmax is 1 up to the roundings of its exponent, of 1 / sum and of their
+    product (2^-22 together, which decides fp16's ties below its normal numbers): the outputs are its
+    values, those past the type's largest finite value that value."""
+    f = fq()
+    first, last = 8, 254
+    B = last - first + 1
+    c = f.alloc_kv4_cache(B, 1, 1, D)
+    c.k.copy_(torch.randint(0, 256, c.k.shape, generator=gen(5), dtype=torch.uint8))
+    c.k_scales.fill_(125)
+    c.v.copy_(torch.randint(0, 256, c.v.shape, generator=gen(6), dtype=torch.uint8))
+    byte = torch.randint(first, last + 1, c.v_scales.shape, generator=gen(7), dtype=torch.uint8)
+    byte[..., 0] = torch.arange(first, last + 1, dtype=torch.uint8)[:, None, None]
+    c.v_scales.copy_(byte)
+    q = torch.randn(B * queries, 2, D, generator=gen(8)).to(dtype).cuda()
+    out = f.kv4_attention(q, c, torch.arange(B, dtype=torch.int32).cuda()[:, None], torch.ones(B, dtype=torch.int32).cuda(),
+                          0.125, causal=False, q_indptr=torch.arange(0, (B + 1) * queries, queries, dtype=torch.int32).cuda())
+    torch.cuda.synchronize()
+    exact, got = ref.dequantize(c.v.cpu(), byte), out.cpu().view(B, queries, 2, D)  # [B, 1, 1, D]
+    assert bool(((got == saturated(exact * (1 - 2.0 ** -22), dtype)) | (got == saturated(exact * (1 + 2.0 ** -22), dtype))).all())
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("queries,tokens", [(1, 200), (1, 5000), (40, 200), (40, 2500)])
+def test_keys_at_the_top(queries, tokens, D):
+    """Keys up to bf16's largest value, held as up to 2^128, with queries small enough for ordinary scores."""
+    f = fq()
+    page, big = 16, 2.0 ** 126
+    pages = -(-tokens // page)
+    c = f.alloc_kv4_cache(pages, page, 1, D)
+    most = torch.finfo(torch.bfloat16).max
+    k = (torch.randn(tokens, 1, D, generator=gen(9), dtype=torch.float64) * big).clamp(-most, most).to(torch.bfloat16)
+    v = torch.randn(tokens, 1, D, generator=gen(10)).to(torch.bfloat16)
+    f.fp8q_kv4_write(k.cuda(), v.cuda(), torch.arange(tokens, dtype=torch.int32).cuda(), c)
+    assert int(c.k_scales.max()) == 253
+    q = (torch.randn(queries, 2, D, generator=gen(11)) * 2.0 ** -110).to(torch.bfloat16)
+    table, scale = torch.arange(pages, dtype=torch.int32)[None], 2.0 ** -16 / D ** 0.5
+    out, lse = torch.empty_like(q, device="cuda"), torch.empty(queries, 2, device="cuda")
+    f.fp8q_kv4_attention(q.cuda(), c, table.cuda(), torch.tensor([tokens], dtype=torch.int32).cuda(), out, scale, True,
+                         torch.tensor([0, queries], dtype=torch.int32).cuda(), lse)
+    torch.cuda.synchronize()
+    k64, v64 = ref.dequantize(c.k.cpu(), c.k_scales.cpu()), ref.dequantize(c.v.cpu(), c.v_scales.cpu())
+    o, l, mass, slack = ref.attention(q, k64, v64, table, [tokens], [queries], page, pages, scale, True)
+    ob, lb = ref.attention_bounds(o, l, mass, slack, D, tokens, torch.bfloat16)
+    assert float(k64.abs().max()) >= 2.0 ** 128 and float(l.min()) < 20
+    assert bool(((out.cpu().double() - o).abs() <= ob).all()) and bool(((lse.cpu().double() - l).abs() <= lb).all())
+
+
 def test_many_heads_and_sequences():
     """One query of 2^19 heads in one of 4096 sequences: more (sequence, head) pairs than 2^31. A
     cache of one token makes the softmax 1, so the outputs are its values."""
