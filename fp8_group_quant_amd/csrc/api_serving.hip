@@ -3,6 +3,7 @@
 // include/fp8q.h.
 #include <algorithm>
 #include <cmath>
+#include <limits>
 
 #include "serving.h"
 
@@ -258,8 +259,10 @@ int attention_entry(const void* q, int dtype, int64_t q_st, int64_t q_sh, const 
   p.Hq = static_cast<int32_t>(Hq);
   p.Hkv = static_cast<int32_t>(Hkv);
   p.group = static_cast<int32_t>(Hq / Hkv);
-  // a scale of zero stays above the smallest numbers, so that a masked score times it is -infinity
-  p.scale_log2 = std::max(std::fabs(sm_scale) * 5.770780163555854f, 1e-30f);
+  // A scale of zero becomes the smallest number instead, so that a masked score times it is still
+  // -infinity; a score below 2^127 times that is below 2^-22. (fp32 denormals are on in the kernels.)
+  p.scale_log2 = std::min(std::max(std::fabs(sm_scale) * 5.770780163555854f, std::numeric_limits<float>::denorm_min()),
+                          std::numeric_limits<float>::max());
   p.q_sign = sm_scale < 0.0f ? 0x80008000u : 0u;
   p.causal = causal != 0;
   return launch_kv4_attention(dtype, D, p, workspace, workspace_bytes, static_cast<hipStream_t>(stream));

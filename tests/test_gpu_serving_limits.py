@@ -130,6 +130,33 @@ def test_keys_at_the_top(queries, tokens, D):
     assert bool(((out.cpu().double() - o).abs() <= ob).all()) and bool(((lse.cpu().double() - l).abs() <= lb).all())
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("scale", [0.0, 1e-36, 2.0 ** -104, -(2.0 ** -104)])
+@pytest.mark.parametrize("queries,tokens", [(3, 200), (3, 3000), (40, 200), (40, 2500)])
+def test_small_scales_of_large_scores(queries, tokens, scale, dtype):
+    """Products of 2^100 and more, scaled to ordinary scores, to almost nothing or to zero, with tokens
+    that are masked and a sequence that sees none."""
+    f = fq()
+    D, page = 128, 16
+    pages = -(-tokens // page)
+    c = f.alloc_kv4_cache(pages, page, 1, D)
+    k = torch.randn(tokens, 1, D, generator=gen(12)) * 2.0 ** 100
+    v = torch.randn(tokens, 1, D, generator=gen(13))
+    f.fp8q_kv4_write(k.cuda(), v.cuda(), torch.arange(tokens, dtype=torch.int32).cuda(), c)
+    q = torch.randn(2 * queries, 2, D, generator=gen(14)).to(dtype)
+    table = torch.arange(pages, dtype=torch.int32).expand(2, -1)
+    out, lse = torch.empty_like(q, device="cuda"), torch.empty(2 * queries, 2, device="cuda")
+    f.fp8q_kv4_attention(q.cuda(), c, table.contiguous().cuda(), torch.tensor([tokens, 0], dtype=torch.int32).cuda(), out, scale,
+                         True, torch.tensor([0, queries, 2 * queries], dtype=torch.int32).cuda(), lse)
+    torch.cuda.synchronize()
+    k64, v64 = ref.dequantize(c.k.cpu(), c.k_scales.cpu()), ref.dequantize(c.v.cpu(), c.v_scales.cpu())
+    o, l, mass, slack = ref.attention(q, k64, v64, table, [tokens, 0], [queries, queries], page, pages, scale, True)
+    ob, lb = ref.attention_bounds(o, l, mass, slack, D, tokens, dtype)
+    got, sums = out.cpu().double(), lse.cpu().double()
+    assert bool((got[queries:] == 0).all()) and bool(torch.isinf(sums[queries:]).all())
+    assert bool(((got - o).abs() <= ob).all()) and bool(((sums - l).abs() <= lb)[:queries].all())
+
+
 def test_many_heads_and_sequences():
     """One query of 2^19 heads in one of 4096 sequences: more (sequence, head) pairs than 2^31. A
     cache of one token makes the softmax 1, so the outputs are its values."""
