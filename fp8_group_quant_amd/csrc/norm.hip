@@ -61,6 +61,11 @@ constexpr int norm_waves(int CH) { return CH == 3 ? 4 : 1; }
 template <int DT, int LANES, int WPR, int CH>
 __global__ __launch_bounds__(WPR < 4 ? 256 : 64 * WPR, norm_waves(CH)) void rms_norm_quant_kernel(NormParams p) {
   static_assert(LANES == 64 || WPR == 1, "a row of 16 lanes is one wave's");
+  // 64 values of h leave no registers for the other inputs of all passes: x and the residual come in for
+  // two passes at a time, and the weight after the sum. (All at once, 36 to 116 registers went to
+  // scratch: 1024 x 65536 with a residual took 149 us in bf16 and 344 in fp32, now 107 and 195.)
+  constexpr bool kLong = CH == 4;
+  constexpr int kAhead = 2;
   constexpr int kWaves = WPR < 4 ? 4 : WPR;
   constexpr int kRows = kWaves / WPR * (64 / LANES);  // of a block
   constexpr int kPass = LANES * WPR * kPerLane;       // elements of a row that its lanes hold at a time
@@ -75,22 +80,32 @@ __global__ __launch_bounds__(WPR < 4 ? 256 : 64 * WPR, norm_waves(CH)) void rms_
     const int64_t m = row0 + (LANES == 64 ? wr : wave * 4 + (lane >> 4));
     const bool live = m < p.M;
     Raw16<DT> xr[CH], rr[CH], gr[CH];
-#pragma unroll
-    for (int i = 0; i < CH; i++) {
+    auto load = [&](int i, bool with_weight) {
       zero_raw<DT>(xr[i]);
       zero_raw<DT>(rr[i]);
-      zero_raw<DT>(gr[i]);
+      if (with_weight) zero_raw<DT>(gr[i]);
       const int32_t k = at + kPass * i;
       if (live && k < p.K) {
         load_raw<DT>(p.x, m * p.x_sm + k, xr[i]);
         if (p.res) load_raw<DT>(p.res, m * p.r_sm + k, rr[i]);
-        load_raw<DT>(p.w, k, gr[i]);
+        if (with_weight) load_raw<DT>(p.w, k, gr[i]);
       }
+    };
+    if constexpr (!kLong) {
+#pragma unroll
+      for (int i = 0; i < CH; i++) load(i, true);
     }
     float h[CH][16];
     float sq[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < CH; i++) {
+      if constexpr (kLong) {
+        if (i % kAhead == 0) {
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int a = 0; a < kAhead; a++) load(i + a, false);
+        }
+      }
       widen<DT>(xr[i], h[i]);
       if (p.res) {
         float r[16];
@@ -124,6 +139,11 @@ __global__ __launch_bounds__(WPR < 4 ? 256 : 64 * WPR, norm_waves(CH)) void rms_
 #pragma unroll
     for (int i = 0; i < CH; i++) {
       float g[16];
+      if constexpr (kLong) {
+        __builtin_amdgcn_sched_barrier(0);
+        zero_raw<DT>(gr[i]);
+        if (live && at + kPass * i < p.K) load_raw<DT>(p.w, at + kPass * i, gr[i]);
+      }
       widen<DT>(gr[i], g);
       amax[i] = 0.0f;
 #pragma unroll
@@ -153,7 +173,11 @@ __global__ __launch_bounds__(WPR < 4 ? 256 : 64 * WPR, norm_waves(CH)) void rms_
     }
 #pragma unroll
     for (int i = 0; i < CH; i++) {
-      const int32_t k = at + kPass * i;
+      int32_t k = at + kPass * i;
+      if constexpr (kLong) {
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("" : "+v"(k));  // the passes' scale addresses are not worth registers across the rows
+      }
       uint32_t sbits;
       float inv;
       if (p.ue8m0) inv = group_multiplier<FP8Q_SCALE_UE8M0, false>(fmaxf(amax[i], kEps), sbits);
@@ -184,7 +208,8 @@ void launch_one(const NormParams& p, hipStream_t stream) {
 // 60 instructions for sums and scales, then serves up to 48 elements: 60000 x 256 takes 22.0 us,
 // 38 us with a wave per row); longer ones have 16 elements per lane and as many waves as that
 // takes, which is the most loads in flight (4096 x 7168: 8 waves 41.8 us, 4 waves of 32 elements
-// 42.7; one row of 7168: 3.3 and 3.7 us). Between 512 and 768 elements the registers decide: three
+// 42.7; one row of 7168: 3.3 and 3.7 us), up to a block's 16, and then two or four passes of them (2048 x
+// 24576 in bf16: 83 us with two, 162 with four, which held them all). Between 512 and 768 elements the registers decide: three
 // passes fit where there is no residual and 16-bit rows (30000 x 768: 16.9 us, 19.7 with a wave per
 // row; fp32 28.6 and 25.2; with a residual 35.7 and 33.1).
 template <int DT>
@@ -199,6 +224,7 @@ void launch_dt(const NormParams& p, hipStream_t s) {
   else if (p.K <= 4096) launch_one<DT, 64, 4, 1>(p, s);
   else if (p.K <= 8192) launch_one<DT, 64, 8, 1>(p, s);
   else if (p.K <= 16384) launch_one<DT, 64, 16, 1>(p, s);
+  else if (p.K <= 32768) launch_one<DT, 64, 16, 2>(p, s);
   else launch_one<DT, 64, 16, 4>(p, s);
 }
 

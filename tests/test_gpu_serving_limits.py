@@ -17,6 +17,27 @@ def gen(seed):
     return torch.Generator().manual_seed(seed)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("K,group,fmt", [(16400, 16400, "f32"), (16512, 128, "ue8m0"), (32768, 128, "ue8m0_packed"), (32800, 32, "f32"),
+                                         (49152, 49152, "ue8m0"), (65520, 65520, "f32"), (65536, 64, "ue8m0")])
+def test_long_norm_rows(K, group, fmt, dtype):
+    """Rows of two and four passes, with and without a residual, and updated in place."""
+    from test_gpu_serving import DT, check_norm, run_norm, values
+    x, res = values(K, 3, K, dtype=dtype), values(K + 1, 3, K, dtype=dtype, spread=0.5)
+    w = (1 + 0.2 * torch.randn(K, generator=gen(K))).to(DT[dtype])
+    check_norm(x, w, res, group, fmt, "row")
+    check_norm(x, w, None, group, fmt, "col")
+    f = fq()
+    q0, s0, h0 = run_norm(x, w, res, group, fmt, "row")
+    for into in (0, 1):
+        xr = [x.cuda(), res.cuda()]
+        q = torch.empty(3, K, dtype=torch.uint8, device="cuda")
+        s = f.alloc_scales(None, 3, K // group, fmt, "row", "cuda")
+        f.fp8q_rms_norm_group_quant(xr[0], w.cuda(), q, s, group, residual=xr[1], residual_out=xr[into])
+        torch.cuda.synchronize()
+        assert torch.equal(q.cpu().view(torch.float8_e4m3fn).double(), q0) and torch.equal(xr[into].cpu(), h0)
+
+
 def saturated(v, dtype):
     """float64 values rounded to dtype, those past its largest finite value as that value."""
     most = torch.finfo(dtype).max
