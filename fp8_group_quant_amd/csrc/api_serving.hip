@@ -90,7 +90,7 @@ int norm_entry(const void* x, int in_dtype, int64_t M, int64_t K, int64_t x_sm, 
   p.s_sm = s_sm;
   p.s_sg = s_sg;
   p.eps = eps;
-  p.k = static_cast<float>(K);
+  p.inv_k = 1.0 / static_cast<double>(K);
   p.group = grouped ? group_size : 0;
   p.group_shift = group_size == 32 ? 5 : group_size == 64 ? 6 : group_size == 128 ? 7 : 30;
   p.ue8m0 = scale_fmt != FP8Q_SCALE_F32;

@@ -7,11 +7,16 @@
 // A row stays in registers between the sum of squares and the encode, so every input is read
 // once and every output written once: 7 bytes per bf16 element with a residual (x, residual
 // and its sum 2 each, the code 1). That traffic is what bounds it: 4096 x 7168 with a residual,
-// 206 MB, takes 41.4 us = 5.0 TB/s, the rate of a plain copy. The arithmetic, about 13 fp32
-// operations per element, shows in short rows without a residual (30011 x 576, fp16, 53 MB: 14.3
-// us = 3.7 TB/s). The row's sum of squares is fp32: four sums per lane by fma, then a tree. The
-// factors are carried with their rounding errors, so that y has one rounding to fp32: of the codes
-// that a plain fp32 evaluation rounds to a neighbour's side of a tie, half are then right.
+// 206 MB, takes 41.6 us = 4.9 TB/s, the rate of a plain copy. The arithmetic, about 13 fp32
+// operations per element, shows in short rows without a residual (30011 x 576, fp16, 53 MB: 14.7
+// us = 3.6 TB/s; there two of the five operations per element between h and y are for the root's and
+// the products' rounding errors).
+//
+// h is rounded to fp32. The sum of its squares is fp32 in each lane (four sums by fma) and over the first
+// lanes, and 64-bit in its last additions; the mean is 64-bit, and the factors are carried with their
+// rounding errors, so that y is the exact value's own rounding but for what the sum's 32-bit parts
+// leave (0.2 units). Against 64 bits 11 of 1.8e8 codes are off with UE8M0 scales (4096 x 7168; a plain fp32
+// evaluation 80); with fp32 scales, whose reciprocal and its product round again, 1317 and 1508.
 #include <algorithm>
 
 #include "quant_device.h"
@@ -23,23 +28,42 @@
 namespace fp8q {
 namespace {
 
-// Reductions over the LANES (16 or 64) lanes that share a row, or a wave's part of one: the steps
-// of group_max within 16 lanes, then the wave's four rows of lanes through readlane.
-template <int LANES, typename F>
-__device__ __forceinline__ float row_reduce(float v, F f) {
-  v = f(v, dpp<0xB1>(v));
-  v = f(v, dpp<0x4E>(v));
-  v = f(v, dpp<0x141>(v));
-  v = f(v, dpp<0x140>(v));
-  if constexpr (LANES == 16) return v;
-  const float r0 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 0));
-  const float r1 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 16));
-  const float r2 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 32));
-  const float r3 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 48));
-  return f(f(r0, r1), f(r2, r3));
+// Reductions over the LANES (16 or 64) lanes that share a row, or a wave's part of one: the steps of
+// group_max within 16 lanes, then the wave's four rows of lanes through readlane.
+template <int LANE>
+__device__ __forceinline__ float lane_of(float v) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), LANE));
 }
-__device__ __forceinline__ float add(float a, float b) { return a + b; }
-__device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
+template <int LANES>
+__device__ __forceinline__ float row_max_of(float v) {
+  v = group_max<8>(v);
+  v = fmaxf(v, dpp<0x140>(v));
+  if constexpr (LANES == 16) return v;
+  return fmaxf(fmaxf(lane_of<0>(v), lane_of<16>(v)), fmaxf(lane_of<32>(v), lane_of<48>(v)));
+}
+
+template <int CTRL>
+__device__ __forceinline__ double dpp64(double v) {
+  const int2 w = __builtin_bit_cast(int2, v);
+  return __builtin_bit_cast(double, int2{__builtin_amdgcn_update_dpp(w.x, w.x, CTRL, 0xF, 0xF, false),
+                                         __builtin_amdgcn_update_dpp(w.y, w.y, CTRL, 0xF, 0xF, false)});
+}
+// The last additions of a sum decide its error (that of those before averages out over the parts), so
+// they are done in 64 bits: of 16 lanes the sums of four, of a wave the sums of 16.
+template <int LANES>
+__device__ __forceinline__ double row_sum_of(float v) {
+  v += dpp<0xB1>(v);
+  v += dpp<0x4E>(v);
+  if constexpr (LANES == 16) {
+    double s = v;
+    s += dpp64<0x141>(s);
+    return s + dpp64<0x140>(s);
+  } else {
+    v += dpp<0x141>(v);
+    v += dpp<0x140>(v);
+    return (static_cast<double>(lane_of<0>(v)) + lane_of<16>(v)) + (static_cast<double>(lane_of<32>(v)) + lane_of<48>(v));
+  }
+}
 
 // 16 values times their groups' multiplier as e4m3 codes. Nothing is clamped: the scale is amax / 448
 // or more up to its rounding and the multiplier's, so a product stays below 448 * (1 + 2^-21),
@@ -62,14 +86,15 @@ template <int DT, int LANES, int WPR, int CH>
 __global__ __launch_bounds__(WPR < 4 ? 256 : 64 * WPR, norm_waves(CH)) void rms_norm_quant_kernel(NormParams p) {
   static_assert(LANES == 64 || WPR == 1, "a row of 16 lanes is one wave's");
   // 64 values of h leave no registers for the other inputs of all passes: x and the residual come in for
-  // two passes at a time, and the weight after the sum. (All at once, 36 to 116 registers went to
-  // scratch: 1024 x 65536 with a residual took 149 us in bf16 and 344 in fp32, now 107 and 195.)
+  // two passes at a time (fp32: one), and the weight after the sum. (All at once, 36 to 116 registers
+  // went to memory: 1024 x 65536 with a residual took 149 us in bf16 and 344 in fp32, now 106 and 193.)
   constexpr bool kLong = CH == 4;
-  constexpr int kAhead = 2;
+  constexpr int kAhead = DT == FP8Q_DTYPE_F32 ? 1 : 2;
   constexpr int kWaves = WPR < 4 ? 4 : WPR;
   constexpr int kRows = kWaves / WPR * (64 / LANES);  // of a block
   constexpr int kPass = LANES * WPR * kPerLane;       // elements of a row that its lanes hold at a time
-  __shared__ float part[2][2][kWaves / WPR][WPR];  // by iteration parity: sums of squares, maxima
+  __shared__ double sums[2][kWaves / WPR][WPR];  // of squares, by iteration parity
+  __shared__ float maxima[2][kWaves / WPR][WPR];
   const int lane = threadIdx.x & 63;
   const int wave = wave_index();
   const int wr = wave / WPR, wi = wave % WPR;
@@ -118,22 +143,20 @@ __global__ __launch_bounds__(WPR < 4 ? 256 : 64 * WPR, norm_waves(CH)) void rms_
       const int32_t k = at + kPass * i;
       if (p.res_out && live && k < p.K) store16<DT>(p.res_out, m * p.ro_sm + k, h[i]);
     }
-    float ss = row_reduce<LANES>((sq[0] + sq[1]) + (sq[2] + sq[3]), add);
+    double ss = row_sum_of<LANES>((sq[0] + sq[1]) + (sq[2] + sq[3]));
     if constexpr (WPR > 1) {
-      if (lane == 0) part[par][0][wr][wi] = ss;
+      if (lane == 0) sums[par][wr][wi] = ss;
       __syncthreads();
-      float s[WPR];
-#pragma unroll
-      for (int i = 0; i < WPR; i++) s[i] = part[par][0][wr][i];
-#pragma unroll
-      for (int n = WPR / 2; n > 0; n /= 2)
-#pragma unroll
-        for (int i = 0; i < n; i++) s[i] += s[i + n];
-      ss = s[0];
+      ss = sums[par][wr][lane & (WPR - 1)];  // every lane one wave's, then over WPR neighbours
+      ss += dpp64<0xB1>(ss);
+      if constexpr (WPR >= 4) ss += dpp64<0x4E>(ss);
+      if constexpr (WPR >= 8) ss += dpp64<0x141>(ss);
+      if constexpr (WPR >= 16) ss += dpp64<0x140>(ss);
     }
-    // r + r_lo = 1 / sqrt(v) but for r_lo's own rounding (Newton's step, its residual by fma)
-    const float v = ss / p.k + p.eps, r = 1.0f / sqrtf(v), vr = v * r;
-    const float left = fmaf(-vr, r, 1.0f) - fmaf(v, r, -vr) * r;
+    // r + r_lo = 1 / sqrt(v) but for r_lo's own rounding: Newton's step from the instruction's estimate
+    const double v = fma(ss, p.inv_k, static_cast<double>(p.eps));
+    const float r = static_cast<float>(__builtin_amdgcn_rsq(v));
+    const float left = static_cast<float>(fma(-v * r, static_cast<double>(r), 1.0));
     const float r_lo = fabsf(left) < 1.0f ? 0.5f * r * left : 0.0f;  // v of 0 or infinity: no residual
     float amax[CH], row_max = 0.0f;
 #pragma unroll
@@ -161,12 +184,12 @@ __global__ __launch_bounds__(WPR < 4 ? 256 : 64 * WPR, norm_waves(CH)) void rms_
       }
     }
     if (p.group == 0) {  // one group per row
-      row_max = row_reduce<LANES>(row_max, larger);
+      row_max = row_max_of<LANES>(row_max);
       if constexpr (WPR > 1) {
-        if (lane == 0) part[par][1][wr][wi] = row_max;
+        if (lane == 0) maxima[par][wr][wi] = row_max;
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < WPR; i++) row_max = fmaxf(row_max, part[par][1][wr][i]);
+        for (int i = 0; i < WPR; i++) row_max = fmaxf(row_max, maxima[par][wr][i]);
       }
 #pragma unroll
       for (int i = 0; i < CH; i++) amax[i] = row_max;
@@ -209,9 +232,9 @@ void launch_one(const NormParams& p, hipStream_t stream) {
 // 38 us with a wave per row); longer ones have 16 elements per lane and as many waves as that
 // takes, which is the most loads in flight (4096 x 7168: 8 waves 41.8 us, 4 waves of 32 elements
 // 42.7; one row of 7168: 3.3 and 3.7 us), up to a block's 16, and then two or four passes of them (2048 x
-// 24576 in bf16: 83 us with two, 162 with four, which held them all). Between 512 and 768 elements the registers decide: three
-// passes fit where there is no residual and 16-bit rows (30000 x 768: 16.9 us, 19.7 with a wave per
-// row; fp32 28.6 and 25.2; with a residual 35.7 and 33.1).
+// 24576 in bf16: 82 us with two, 162 with four). Between 512 and 768 elements the registers decide:
+// three passes fit, but for two to four registers, 16-bit rows without a residual (30000 x 768: bf16 15.6 us,
+// 17.4 with a wave per row, fp16 16.0 and 18.0; fp32 28.6 and 25.2; with a residual 35.7 and 33.1).
 template <int DT>
 void launch_dt(const NormParams& p, hipStream_t s) {
   if constexpr (DT != FP8Q_DTYPE_F32) {

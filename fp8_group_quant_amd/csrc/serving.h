@@ -18,7 +18,8 @@ struct NormParams {
   int64_t x_sm, r_sm, ro_sm;   // elements
   int64_t q_sm;                // bytes
   int64_t s_sm, s_sg;          // scale elements (packed UE8M0: words of 4 groups)
-  float eps, k;                // k = K
+  float eps;
+  double inv_k;                // 1 / K
   int32_t group;               // 32, 64, 128, or 0 (one group per row)
   int32_t group_shift;         // log2 of it (one group per row: any shift past the row)
   int32_t ue8m0, packed;

@@ -324,9 +324,10 @@ int fp8q_grouped_gemm_contiguous(const uint8_t* a, int64_t lda,
  * fp8q_rms_norm_group_quant — root-mean-square norm of each row, with the residual's addition
  * before it and group quantization to e4m3 after it
  *
- * x is [M][K] of in_dtype (row m at x + m*x_sm); weight is [K] of in_dtype. In fp32:
- *   h = x (+ residual, [M][K] of in_dtype, row m at residual + m*r_sm)
- *   y = (h * r) * weight, r = 1 / sqrt( sum_k h^2 / K + eps )
+ * x is [M][K] of in_dtype (row m at x + m*x_sm); weight is [K] of in_dtype:
+ *   h = x (+ residual, [M][K] of in_dtype, row m at residual + m*r_sm), rounded to fp32
+ *   y = h * r * weight, r = 1 / sqrt( sum_k h^2 / K + eps ), rounded to fp32 once, but for an error of the
+ *       sum, which is fp32 up to its last additions
  * y, not rounded to a narrower type, is quantized as by fp8q_group_quant (same scale formats,
  * layouts and group sizes, group_size == K included) into q and s (row m of q at q + m*q_sm;
  * scale of group g at s + m*s_sm + g*s_sg). h rounded to in_dtype is stored at residual_out

@@ -194,3 +194,28 @@ def test_many_heads_and_sequences():
                           torch.ones(B, dtype=torch.int32, device="cuda"), 0.125, q_indptr=indptr.cuda())
     torch.cuda.synchronize()
     assert torch.equal(out.cpu()[0], ref.dequantize(c.v.cpu(), c.v_scales.cpu())[0, 0].to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("dtype,M,K,residual", [("bf16", 8192, 7168, True), ("f16", 30011, 576, False), ("bf16", 20000, 1024, True),
+                                                ("bf16", 20000, 256, False), ("f32", 8192, 2048, True)])
+def test_norm_is_rounded_once(dtype, M, K, residual):
+    """A row's fp32 scale is its largest |y| / 448, each rounded to fp32, so it shows whether y is the exact value's
+    own rounding. That y is another number takes an error before its rounding that reaches the nearest
+    boundary, of probability E|error| / unit. Sums of squares whose last additions are in 64 bits are of
+    at least four 32-bit parts, each at most 0.58 sqrt(2) = 0.82 units rms off (the unit 2^-24, halves of
+    it per addition, their weights halving from the last one on): 0.41 together, of which the root
+    takes half; mean, root and products add nothing of that size. E|error| is then 0.8 x 0.2 units: 0.17
+    of the scales at most. (A mean or a root rounded to 32 bits alone would be 0.2 and more.)"""
+    f = fq()
+    g = torch.Generator(device="cuda").manual_seed(K)
+    dt = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}[dtype]
+    x = torch.randn(M, K, device="cuda", generator=g).to(dt)
+    r = torch.randn(M, K, device="cuda", generator=g).to(dt) if residual else None
+    w = (1 + 0.1 * torch.randn(K, device="cuda", generator=g)).to(dt)
+    s = f.rms_norm_group_quant(x, w, K, "f32", "row", 1e-6, residual=r)[1].double()
+    h = x.float() + r.float() if residual else x.float()  # rounded to fp32, as the formula says
+    y = h.double() / torch.sqrt(h.double().square().mean(-1, keepdim=True) + float(torch.tensor(1e-6))) * w.double()
+    own = y.abs().amax(-1, keepdim=True).float() / torch.tensor(448.0, device="cuda")
+    off = float((s.float() != own).double().mean())
+    print(f"{dtype} {M} x {K}: {off:.3f}")
+    assert off <= 0.17
