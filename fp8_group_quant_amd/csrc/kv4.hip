@@ -11,8 +11,8 @@
 // tokens in a row: 16 bytes per lane and access on the model's side, next to the neighbour's,
 // and the index arithmetic is done once for the four. Blocks of the write take keys and values in
 // turn: they are often views of one projection's output, whose rows are then read whole (65536
-// tokens of 8 x 128, 350 MB: 70 us, 82 us with all keys before all values). The read's outputs
-// are two tensors, written one after the other (131072 tokens, 680 MB: 139.4 us, in turn 140.1).
+// tokens of 8 x 128, 340 MB: 70 us, 82 us with all keys before all values; fp32 124 either way). The
+// read's outputs are two tensors, written one after the other (131072 tokens, 680 MB: 131 us, in turn too).
 #include <algorithm>
 
 #include "quant_device.h"

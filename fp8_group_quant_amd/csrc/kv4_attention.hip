@@ -15,18 +15,18 @@
 // is cut leaves a piece per block in the workspace, which a second kernel joins.
 //
 // Bounds. Few rows: the cache's bytes. 64 sequences of 3300 to 8192 tokens, 64 heads on 8 cached
-// ones of 128: 408 MB in 86.6 us = 4.7 TB/s, and 5.9 us for the join. The loads decide it: with 32
+// ones of 128: 408 MB in 86 us = 4.7 TB/s, and 6 us for the join. The loads decide it: with 32
 // tokens to a step the whole took 102 us and its loads without any arithmetic 92 (a plain read of
-// 4 KB pieces in random order: 69). One sequence of 262144 tokens: 285 MB in 58.7 us = 4.9 TB/s.
+// 4 KB pieces in random order: 69). One sequence of 262144 tokens: 285 MB in 56 us = 5.1 TB/s.
 // Many rows: the matrix pipe together with the vector pipe, which converts K for every wave and
-// exponentiates. 2 x 2048 queries of 32 heads over 8192 tokens, 386 GFLOP: 430 us = 0.90 PFLOP/s,
-// 0.76 of a large bf16 library product's rate.
+// exponentiates. 2 x 1434 and 2048 queries of 32 heads over 8192 tokens, 386 GFLOP: 431 us = 0.90
+// PFLOP/s, 0.65 of a large bf16 library product's rate.
 //
 // Layouts (v_mfma_f32_16x16x32_bf16; lane l, r = l % 16, h = l / 16):
 //   S^T = K Q^T: lane (r, h) loads dims [D/4 h, D/4 (h + 1)) of token r, one or two scale blocks
 //     of which all elements share one scale, and converts them in registers. The contraction
 //     index is free, so step j takes dims D/4 h + 8j .. + 7 from lane group h of both operands.
-//     e2m1 times a power of two is exact in bf16: no error is added.
+//     e2m1 times a power of two is exact in bf16 (a quarter of it, below): no error is added.
 //   S^T leaves lane (r, h) with tokens 4h .. 4h + 3 of query row r: as the operand of O^T = V^T P^T
 //     that is a permutation of the contraction index, which V^T's reads follow, so P never
 //     leaves its registers.
@@ -804,8 +804,10 @@ __global__ __launch_bounds__(64 * WAVES, waves_per_simd(D, DT, N)) void kv4_atte
 // step ahead of its use (two buffers, one barrier per step). Each of V's operands is read one product
 // ahead of its use (529 us for 2 x 2048 queries over 8192 tokens when the compiler placed the reads,
 // 484 so), and a step's 64 tokens take one page lookup where a page holds them (435).
-// Waves per SIMD that the registers are kept to (fp16, D = 128, 64 rows: 451 us at 3, 468 at 2, for 2 x
-// 1024 queries of 32 heads over 8192 tokens; bf16, D = 64, 128 rows: 350 and 388 for 2 x 2048).
+// Waves per SIMD that the registers are kept to (fp16, D = 128, 64 rows: 452 us at 3, 468 at 2, for 2 x
+// 1024 queries of 32 heads over 8192 tokens; bf16, D = 64, 128 rows: 353 and 388 for 2 x 2048). Up to 17
+// registers then go through memory: in fp16 at D = 128 and 256 with one page lookup per step or per token, in bf16
+// with one per token.
 constexpr int wide_waves_per_simd(int D, int DT, int QT, bool split) {
   const int parts = DT == FP8Q_DTYPE_F16 ? 2 : 1;
   if (D * QT * parts <= 64) return 4;

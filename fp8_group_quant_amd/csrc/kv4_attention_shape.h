@@ -23,7 +23,8 @@ constexpr int waves_per_simd(int64_t D, int DT, int N) {
   return N == 4 || (DT == FP8Q_DTYPE_F16 && D == 128) ? 3 : 4;
 }
 
-// Rows of the widest tile whose queries and outputs the registers hold.
+// Rows of the widest tile whose queries and outputs the registers hold (in fp16, as two parts, all but up
+// to 17 of them).
 constexpr int widest(int dtype, int64_t D) { return D * (dtype == FP8Q_DTYPE_F16 ? 2 : 1) <= 128 ? 128 : 64; }
 
 constexpr int kMostWideSteps = 32;  // of a unit that the wide kernel does not split
