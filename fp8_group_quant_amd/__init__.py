@@ -1,14 +1,15 @@
 """Python binding of libfp8q.so: per-token-group FP8 quantization, block-scaled FP8 GEMMs,
-and the operators between them in a serving layer (quantizing norm, 4-bit key/value cache,
-attention over it) for AMD Instinct MI355X (gfx950).
+their 4-bit (MXFP4) counterparts, and the operators between them in a serving layer (quantizing
+norm, 4-bit key/value cache with its page plan, attention over it) for AMD Instinct MI355X (gfx950).
 
 This module only marshals torch tensors (device memory, strides, the current HIP
 stream) into the C ABI declared in include/fp8q.h; every step of the computation runs
 in the library's HIP kernels. The functions named fp8q_* mirror the C entry points one
 to one and write into caller-allocated tensors; group_quant() additionally allocates
 its outputs (the role of _allocate_outputs in the sglang PR #30924 design, prhub
-report section "实现拆解" item 2), as do rms_norm_group_quant(), kv4_read() and
-kv4_attention(); alloc_kv4_cache() allocates a cache.
+report section "实现拆解" item 2), as do rms_norm_group_quant(), mxfp4_quant(), mxfp4_dequant(),
+kv4_read(), kv4_attention(), kv4_window_attention(), kv4_tree_attention() and kv4_plan();
+alloc_kv4_cache() allocates a cache.
 
 There is no fallback: if libfp8q.so is missing or the device is not a gfx950, calls
 raise.
@@ -69,6 +70,20 @@ _SIGNATURES = {
                            _P, _I64, _I64, _P, _P, _P, _I64, _I64, _P, _I64, _I64, _I64, _I64, _I64, _I64, _F32,
                            _INT, _P, _I64, _P],
     "fp8q_kv4_attention_workspace_size": [_INT, _I64, _I64, _I64, _I64, _I64, _I64],
+    "fp8q_kv4_window_attention": [_P, _INT, _I64, _I64, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _I64, _I64, _I64,
+                                  _P, _I64, _I64, _P, _P, _P, _I64, _I64, _P, _I64, _I64, _I64, _I64, _I64, _I64, _F32,
+                                  _I64, _I64, _P, _I64, _P],
+    "fp8q_kv4_window_attention_workspace_size": [_INT, _I64, _I64, _I64, _I64, _I64, _I64, _I64, _I64],
+    "fp8q_kv4_tree_attention": [_P, _INT, _I64, _I64, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _I64, _I64, _I64,
+                                _P, _I64, _I64, _P, _P, _P, _I64, _I64, _P, _I64, _I64, _I64, _I64, _I64, _I64, _F32,
+                                _P, _I64, _I64, _P, _I64, _P],
+    "fp8q_kv4_plan": [_P, _P, _I64, _P, _I64, _P, _I64, _I64, _I64, _I64, _P, _P, _P, _P, _I64, _P, _P],
+    "fp8q_mxfp4_quant": [_P, _INT, _I64, _I64, _I64, _P, _I64, _P, _INT, _I64, _I64, _P],
+    "fp8q_silu_mul_mxfp4_quant": [_P, _INT, _I64, _I64, _I64, _P, _I64, _P, _INT, _I64, _I64, _P],
+    "fp8q_mxfp4_dequant": [_P, _I64, _P, _INT, _I64, _I64, _P, _INT, _I64, _I64, _I64, _P],
+    "fp8q_gemm_mxfp4": [_P, _I64, _P, _INT, _I64, _I64, _P, _I64, _P, _INT, _I64, _I64, _P, _I64, _I64, _I64, _I64,
+                        _P, _I64, _P],
+    "fp8q_gemm_mxfp4_workspace_size": [_I64, _I64, _I64],
     "fp8q_status_string": [_INT],
     "fp8q_last_error": [],
     "fp8q_device_check": [_INT],
@@ -119,6 +134,18 @@ def _stream(stream) -> int:
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
+
+
+def _stream_on(stream, device: int) -> int:
+    """The stream's handle, for a call whose tensors are on GPU `device`: kernels run on the current one."""
+    if stream is None:
+        current = torch._C._cuda_getDevice()
+        if current != device:
+            raise ValueError("the tensors must be on the current GPU")
+        return torch._C._cuda_getCurrentRawStream(current)
+    if torch.cuda.is_initialized() and torch._C._cuda_getDevice() != device:
+        raise ValueError("the tensors must be on the current GPU")
+    return _stream(stream)
 
 
 def _ptr(t: torch.Tensor | None) -> int | None:
@@ -395,6 +422,115 @@ def fp8q_grouped_gemm_contiguous(a: torch.Tensor, sa: torch.Tensor, b: torch.Ten
 _ELSEWHERE = "every tensor must be on one GPU"
 
 
+# ------------------------------------------------------------------------------ MXFP4
+def _mxfp4_rows(entry: str, x, q, s, width, stream) -> None:
+    """The rows' checks and call of the quantizer (x of `width` elements per row, gate | up twice as many) and,
+    with its own argument order, of the way back."""
+    dt = _DTYPES.get(x.dtype)
+    if dt is None or x.dim() != 2 or q.dim() != 2 or s.dim() != 2:
+        raise ValueError("x (bf16, fp16 or fp32), q and s must be 2-D tensors")
+    M = x.shape[0]
+    K = 2 * q.shape[1]
+    if q.element_size() != 1 or q.shape[0] != M or width != K:
+        raise ValueError(f"q has shape {tuple(q.shape)} of {q.dtype}, expected bytes of {(M, width // 2)}")
+    x_sm, x_in = x.stride()
+    q_sm, q_in = q.stride()
+    if (x_in != 1 and x.shape[1] > 1) or (q_in != 1 and K > 2):
+        raise ValueError("innermost dimensions must be contiguous")
+    fmt = _scale_fmt_of(s)
+    if s.shape != (M, K // 128 if fmt == SCALE_UE8M0_PACKED else K // 32):
+        raise ValueError(f"s has shape {tuple(s.shape)} of {s.dtype}, expected a scale per 32 of {(M, K)} elements")
+    if not 0 <= x.get_device() == q.get_device() == s.get_device():
+        raise ValueError(_ELSEWHERE)
+    s_sm, s_sg = s.stride()
+    if entry == "fp8q_mxfp4_dequant":
+        _check(load_library().fp8q_mxfp4_dequant(q.data_ptr(), q_sm, s.data_ptr(), fmt, s_sm, s_sg, x.data_ptr(), dt, M, K,
+                                                 x_sm, _stream_on(stream, x.get_device())))
+    else:
+        _check(getattr(load_library(), entry)(x.data_ptr(), dt, M, K, x_sm, q.data_ptr(), q_sm, s.data_ptr(), fmt, s_sm, s_sg,
+                                              _stream_on(stream, x.get_device())))
+
+
+def fp8q_mxfp4_quant(x: torch.Tensor, q: torch.Tensor, s: torch.Tensor, stream=None) -> None:
+    """x [M, K] (bf16, fp16 or fp32) as e2m1 codes q (uint8 [M, K/2], element 2i in the low half of byte i) with one
+    UE8M0 scale per 32 elements: s uint8 [M, K/32], or int32 words of four [M, K/128]; its strides choose the
+    row- or column-major layout."""
+    _mxfp4_rows("fp8q_mxfp4_quant", x, q, s, x.shape[-1], stream)
+
+
+def fp8q_silu_mul_mxfp4_quant(x: torch.Tensor, q: torch.Tensor, s: torch.Tensor, stream=None) -> None:
+    """As fp8q_mxfp4_quant, with x [M, 2K] = gate | up and silu(gate) * up quantized."""
+    if x.shape[-1] % 2:
+        raise ValueError("x must hold gate | up, two halves of one width")
+    _mxfp4_rows("fp8q_silu_mul_mxfp4_quant", x, q, s, x.shape[-1] // 2, stream)
+
+
+def fp8q_mxfp4_dequant(q: torch.Tensor, s: torch.Tensor, x: torch.Tensor, stream=None) -> None:
+    """The rows x [M, K] (bf16, fp16 or fp32) that codes q and scales s stand for."""
+    _mxfp4_rows("fp8q_mxfp4_dequant", x, q, s, x.shape[-1], stream)
+
+
+def mxfp4_quant(x: torch.Tensor, scale_fmt: str = "ue8m0_packed", layout: str = "col", silu: bool = False,
+                stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """Allocating form: (q uint8 [M, K/2], scales viewed as [M, K/32], or [M, K/128] words with "ue8m0_packed")."""
+    M, W = x.shape
+    K = W // 2 if silu else W
+    if scale_fmt not in ("ue8m0", "ue8m0_packed"):
+        raise ValueError("scale_fmt must be 'ue8m0' or 'ue8m0_packed'")
+    with _allocating_on(stream, x.device):
+        q = torch.empty(M, K // 2, dtype=torch.uint8, device=x.device)
+        s = alloc_scales(None, M, K // 32, scale_fmt, layout, x.device)
+    (fp8q_silu_mul_mxfp4_quant if silu else fp8q_mxfp4_quant)(x, q, s, stream)
+    return q, s
+
+
+def mxfp4_dequant(q: torch.Tensor, s: torch.Tensor, dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+    """Allocating form of fp8q_mxfp4_dequant: [M, K] of dtype."""
+    with _allocating_on(stream, q.device):
+        x = torch.empty(q.shape[0], 2 * q.shape[1], dtype=dtype, device=q.device)
+    fp8q_mxfp4_dequant(q, s, x, stream)
+    return x
+
+
+def fp8q_gemm_mxfp4_workspace_size(M: int, N: int, K: int) -> int:
+    """Bytes of workspace with which fp8q_gemm_mxfp4 splits K over more of the current device (0: it does not)."""
+    return int(load_library().fp8q_gemm_mxfp4_workspace_size(M, N, K))
+
+
+def fp8q_gemm_mxfp4(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torch.Tensor, y: torch.Tensor, stream=None,
+                    workspace: torch.Tensor | None = None) -> None:
+    """y [M, N] (bf16) = a b^T of MXFP4 operands: codes a [M, K/2], b [N, K/2] (uint8) with scales sa, sb as the
+    quantizer gives them: int32 words [rows, K/128] of any strides (column-major ones are read fastest), or
+    row-major uint8 [rows, K/32].
+    When the shape can use a workspace and none is given, one is taken from torch's allocator."""
+    M, kb = a.shape
+    N, kb2 = b.shape
+    K = 2 * kb
+    if kb != kb2 or y.shape != (M, N) or y.dtype != torch.bfloat16 or a.element_size() != 1 or b.element_size() != 1:
+        raise ValueError("shape mismatch: a [M, K/2] and b [N, K/2] of bytes, y [M, N] of bf16")
+    lda, a_in = a.stride()
+    ldb, b_in = b.stride()
+    ldy, y_in = y.stride()
+    if ((a_in != 1 or b_in != 1) and kb > 1) or (y_in != 1 and N > 1):
+        raise ValueError("innermost dimensions must be contiguous")
+    fa, fb = _scale_fmt_of(sa), _scale_fmt_of(sb)
+    if sa.shape != (M, K // 128 if fa == SCALE_UE8M0_PACKED else K // 32) or \
+            sb.shape != (N, K // 128 if fb == SCALE_UE8M0_PACKED else K // 32):
+        raise ValueError("scales must be [rows, K/32] bytes or [rows, K/128] words")
+    if not 0 <= a.get_device() == b.get_device() == y.get_device() == sa.get_device() == sb.get_device() \
+            or (workspace is not None and workspace.get_device() != a.get_device()):
+        raise ValueError(_ELSEWHERE)
+    handle = _stream_on(stream, a.get_device())
+    lib = load_library()
+    if workspace is None:
+        workspace = _alloc_workspace(lib.fp8q_gemm_mxfp4_workspace_size(M, N, K), a.device, stream)
+    sa_sm, sa_sk = sa.stride()
+    sb_sn, sb_sk = sb.stride()
+    _check(lib.fp8q_gemm_mxfp4(a.data_ptr(), lda, sa.data_ptr(), fa, sa_sm, sa_sk, b.data_ptr(), ldb, sb.data_ptr(), fb, sb_sn,
+                               sb_sk, y.data_ptr(), ldy, M, N, K, None if workspace is None else workspace.data_ptr(),
+                               0 if workspace is None else workspace.numel() * workspace.element_size(), handle))
+
+
 # ------------------------------------------------------------------------------ norm
 def fp8q_rms_norm_group_quant(x: torch.Tensor, weight: torch.Tensor, q: torch.Tensor, s: torch.Tensor,
                               group_size: int = 128, eps: float = 1e-6, residual: torch.Tensor | None = None,
@@ -548,16 +684,10 @@ def fp8q_kv4_attention_workspace_size(dtype: torch.dtype, seqs: int, tokens: int
                                                                 head_dim, max_kv_tokens))
 
 
-def fp8q_kv4_attention(q: torch.Tensor, cache: Kv4Cache, block_table: torch.Tensor, kv_lens: torch.Tensor,
-                       out: torch.Tensor, sm_scale: float, causal: bool = True,
-                       q_indptr: torch.Tensor | None = None, lse: torch.Tensor | None = None, stream=None,
-                       workspace: torch.Tensor | None = None) -> None:
-    """out[t, h] = softmax(sm_scale * q[t, h] k^T) v over the cached tokens that the query sees.
-    q, out [T, heads, D] (bf16 or fp16); block_table int32 [B, max_pages]; kv_lens int32 [B];
-    q_indptr int32 [B + 1]: sequence b's queries are rows q_indptr[b] .. q_indptr[b + 1] - 1 (None: row
-    b, T == B). causal: the last query of a sequence sees all its cached tokens, the one before it
-    one less, ... lse [T, heads] fp32 receives the logarithm of each row's softmax sum.
-    When the shape can use a workspace and none is given, one is taken from torch's allocator."""
+def _kv4_attend(entry: str, sizes: tuple, extra: tuple, q, cache, block_table, kv_lens, out, sm_scale, q_indptr, lse,
+                stream, workspace) -> None:
+    """Checks and call of the attention entries: `extra` are the C arguments after sm_scale, `sizes` what the size of
+    the workspace depends on besides the shape."""
     shape, dt = q.shape, _DTYPES.get(q.dtype, DTYPE_F32)
     if len(shape) != 3 or dt == DTYPE_F32:
         raise ValueError("q must be a [T, heads, D] bf16 or fp16 tensor")
@@ -592,15 +722,30 @@ def fp8q_kv4_attention(q: torch.Tensor, cache: Kv4Cache, block_table: torch.Tens
             or (lse is not None and lse.get_device() != q.get_device()) \
             or (workspace is not None and workspace.get_device() != q.get_device()):
         raise ValueError(_ELSEWHERE)
+    handle = _stream_on(stream, q.get_device())
     lib = load_library()
     if workspace is None:
-        workspace = _alloc_workspace(
-            lib.fp8q_kv4_attention_workspace_size(dt, B, T, H, kv_heads, D, max_pages * page), q.device, stream)
-    _check(lib.fp8q_kv4_attention(
+        size = lib.fp8q_kv4_window_attention_workspace_size if sizes else lib.fp8q_kv4_attention_workspace_size
+        workspace = _alloc_workspace(size(dt, B, T, H, kv_heads, D, max_pages * page, *sizes), q.device, stream)
+    _check(getattr(lib, entry)(
         q.data_ptr(), dt, q_st, q_sh, *args, block_table.data_ptr(), table_sb, max_pages, kv_lens.data_ptr(), ip_ptr,
-        out.data_ptr(), o_st, o_sh, lse_ptr, l_st, B, T, H, kv_heads, D, sm_scale, causal,
+        out.data_ptr(), o_st, o_sh, lse_ptr, l_st, B, T, H, kv_heads, D, sm_scale, *extra,
         None if workspace is None else workspace.data_ptr(),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)))
+        0 if workspace is None else workspace.numel() * workspace.element_size(), handle))
+
+
+def fp8q_kv4_attention(q: torch.Tensor, cache: Kv4Cache, block_table: torch.Tensor, kv_lens: torch.Tensor,
+                       out: torch.Tensor, sm_scale: float, causal: bool = True,
+                       q_indptr: torch.Tensor | None = None, lse: torch.Tensor | None = None, stream=None,
+                       workspace: torch.Tensor | None = None) -> None:
+    """out[t, h] = softmax(sm_scale * q[t, h] k^T) v over the cached tokens that the query sees.
+    q, out [T, heads, D] (bf16 or fp16); block_table int32 [B, max_pages]; kv_lens int32 [B];
+    q_indptr int32 [B + 1]: sequence b's queries are rows q_indptr[b] .. q_indptr[b + 1] - 1 (None: row
+    b, T == B). causal: the last query of a sequence sees all its cached tokens, the one before it
+    one less, ... lse [T, heads] fp32 receives the logarithm of each row's softmax sum.
+    When the shape can use a workspace and none is given, one is taken from torch's allocator."""
+    _kv4_attend("fp8q_kv4_attention", (), (causal,), q, cache, block_table, kv_lens, out, sm_scale, q_indptr, lse, stream,
+                workspace)
 
 
 def kv4_attention(q: torch.Tensor, cache: Kv4Cache, block_table: torch.Tensor, kv_lens: torch.Tensor,
@@ -611,6 +756,119 @@ def kv4_attention(q: torch.Tensor, cache: Kv4Cache, block_table: torch.Tensor, k
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     fp8q_kv4_attention(q, cache, block_table, kv_lens, out, sm_scale, causal, q_indptr, None, stream)
     return out
+
+
+def fp8q_kv4_window_attention_workspace_size(dtype: torch.dtype, seqs: int, tokens: int, heads: int, kv_heads: int,
+                                             head_dim: int, max_kv_tokens: int, window: int, sinks: int = 0) -> int:
+    """Bytes of workspace with which fp8q_kv4_window_attention splits long windows over more of the current device
+    (0: it needs none)."""
+    return int(load_library().fp8q_kv4_window_attention_workspace_size(_DTYPES[dtype], seqs, tokens, heads, kv_heads,
+                                                                       head_dim, max_kv_tokens, window, sinks))
+
+
+def fp8q_kv4_window_attention(q: torch.Tensor, cache: Kv4Cache, block_table: torch.Tensor, kv_lens: torch.Tensor,
+                              out: torch.Tensor, sm_scale: float, window: int, sinks: int = 0,
+                              q_indptr: torch.Tensor | None = None, lse: torch.Tensor | None = None, stream=None,
+                              workspace: torch.Tensor | None = None) -> None:
+    """fp8q_kv4_attention (causal) in which a query sees the last `window` tokens up to and with its own, and the
+    first `sinks` of its sequence."""
+    _kv4_attend("fp8q_kv4_window_attention", (window, sinks), (window, sinks), q, cache, block_table, kv_lens, out, sm_scale,
+                q_indptr, lse, stream, workspace)
+
+
+def kv4_window_attention(q: torch.Tensor, cache: Kv4Cache, block_table: torch.Tensor, kv_lens: torch.Tensor,
+                         sm_scale: float, window: int, sinks: int = 0, q_indptr: torch.Tensor | None = None,
+                         stream=None) -> torch.Tensor:
+    """Allocating form of fp8q_kv4_window_attention (rows of q in no sequence are left unset)."""
+    with _allocating_on(stream, q.device):
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    fp8q_kv4_window_attention(q, cache, block_table, kv_lens, out, sm_scale, window, sinks, q_indptr, None, stream)
+    return out
+
+
+def fp8q_kv4_tree_attention(q: torch.Tensor, cache: Kv4Cache, block_table: torch.Tensor, kv_lens: torch.Tensor,
+                            out: torch.Tensor, sm_scale: float, tree_mask: torch.Tensor,
+                            q_indptr: torch.Tensor | None = None, lse: torch.Tensor | None = None, stream=None,
+                            workspace: torch.Tensor | None = None) -> None:
+    """fp8q_kv4_attention for drafted tokens that form a tree: a sequence's n rows of q are held at its last n cached
+    places; each sees every token before them, and drafted token j if bit j % 32 of word j // 32 of its row of
+    tree_mask (int32 [T, words]) is set."""
+    if tree_mask.dtype != torch.int32 or tree_mask.dim() != 2 or tree_mask.shape[0] != q.shape[0] \
+            or (tree_mask.shape[1] > 1 and tree_mask.stride(1) != 1):
+        raise ValueError("tree_mask must be an int32 [T, words] tensor with contiguous rows")
+    if tree_mask.get_device() != q.get_device():
+        raise ValueError(_ELSEWHERE)
+    _kv4_attend("fp8q_kv4_tree_attention", (), (tree_mask.data_ptr(), tree_mask.stride(0), tree_mask.shape[1]), q, cache,
+                block_table, kv_lens, out, sm_scale, q_indptr, lse, stream, workspace)
+
+
+def kv4_tree_attention(q: torch.Tensor, cache: Kv4Cache, block_table: torch.Tensor, kv_lens: torch.Tensor,
+                       sm_scale: float, tree_mask: torch.Tensor, q_indptr: torch.Tensor | None = None,
+                       stream=None) -> torch.Tensor:
+    """Allocating form of fp8q_kv4_tree_attention (rows of q in no sequence are left unset)."""
+    with _allocating_on(stream, q.device):
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    fp8q_kv4_tree_attention(q, cache, block_table, kv_lens, out, sm_scale, tree_mask, q_indptr, None, stream)
+    return out
+
+
+def fp8q_kv4_plan(kv_lens: torch.Tensor, q_lens: torch.Tensor, free_pages: torch.Tensor, block_table: torch.Tensor,
+                  pages: int, page_size: int, new_lens: torch.Tensor, q_indptr: torch.Tensor, slots: torch.Tensor,
+                  pages_taken: torch.Tensor, positions: torch.Tensor | None = None, stream=None) -> None:
+    """One serving step's page bookkeeping for a cache of `pages` pages: sequence b holds kv_lens[b] tokens and gets
+    q_lens[b] new ones. Writes the entries of block_table [B, max_pages] for the pages that are new, taken in order from
+    free_pages; new_lens [B]; q_indptr [B + 1]; the slot (and position) of every new token [T], -1 past the last
+    one; and pages_taken [1], how many pages were needed (more than free_pages holds: the missing ones are
+    -1). All int32 on one GPU; no written tensor may share memory with another."""
+    # written for few interpreter steps: at a decode step the checks are most of the call's time
+    i32 = torch.int32
+    if not (kv_lens.dtype == q_lens.dtype == free_pages.dtype == block_table.dtype == new_lens.dtype == q_indptr.dtype
+            == slots.dtype == pages_taken.dtype == i32) or (positions is not None and positions.dtype != i32):
+        raise ValueError("every tensor must be int32")
+    dev = kv_lens.get_device()
+    if not 0 <= dev == q_lens.get_device() == free_pages.get_device() == block_table.get_device() == new_lens.get_device() \
+            == q_indptr.get_device() == slots.get_device() == pages_taken.get_device() \
+            or (positions is not None and positions.get_device() != dev):
+        raise ValueError(_ELSEWHERE)
+    shape = kv_lens.shape
+    if len(shape) != 1 or block_table.dim() != 2 or slots.dim() != 1 or free_pages.dim() != 1:
+        raise ValueError("kv_lens, slots and free_pages must be 1-D, block_table 2-D")
+    B, T, F = shape[0], slots.shape[0], free_pages.shape[0]
+    rows, max_pages = block_table.shape
+    if q_lens.shape != shape or new_lens.shape != shape or rows != B or q_indptr.shape != (B + 1,) \
+            or pages_taken.numel() != 1 or (positions is not None and positions.shape != slots.shape):
+        raise ValueError("expected q_lens and new_lens [B], block_table [B, max_pages], q_indptr [B + 1], positions [T] "
+                         "and pages_taken [1]")
+    table_sb, table_in = block_table.stride()
+    if (table_in != 1 and max_pages > 1) or (B > 1 and not 1 == kv_lens.stride(0) == q_lens.stride(0) == new_lens.stride(0)) \
+            or (B > 0 and q_indptr.stride(0) != 1) or (T > 1 and slots.stride(0) != 1) \
+            or (F > 1 and free_pages.stride(0) != 1) or (positions is not None and T > 1 and positions.stride(0) != 1):
+        raise ValueError("every tensor must be contiguous (block_table: its rows)")
+    _check(load_library().fp8q_kv4_plan(
+        kv_lens.data_ptr(), q_lens.data_ptr(), B, free_pages.data_ptr(), F, block_table.data_ptr(), table_sb, max_pages, pages,
+        page_size, new_lens.data_ptr(), q_indptr.data_ptr(), slots.data_ptr(),
+        None if positions is None else positions.data_ptr(), T, pages_taken.data_ptr(), _stream_on(stream, dev)))
+
+
+class Kv4Plan(NamedTuple):
+    """What fp8q_kv4_plan writes besides the block table."""
+    kv_lens: torch.Tensor
+    q_indptr: torch.Tensor
+    slots: torch.Tensor
+    positions: torch.Tensor
+    pages_taken: torch.Tensor
+
+
+def kv4_plan(cache: Kv4Cache, kv_lens: torch.Tensor, q_lens: torch.Tensor, free_pages: torch.Tensor,
+             block_table: torch.Tensor, tokens: int, stream=None) -> Kv4Plan:
+    """Allocating form of fp8q_kv4_plan for a cache and at most `tokens` new tokens."""
+    B = kv_lens.numel()
+    with _allocating_on(stream, kv_lens.device):
+        new, ends, slots, positions, taken = (torch.empty(n, dtype=torch.int32, device=kv_lens.device)
+                                              for n in (B, B + 1, tokens, tokens, 1))
+    fp8q_kv4_plan(kv_lens, q_lens, free_pages, block_table, cache.k.shape[0], cache.k.shape[1], new, ends, slots, taken,
+                  positions, stream)
+    return Kv4Plan(new, ends, slots, positions, taken)
 
 
 def fp8q_device_check(device: int = 0) -> int:

@@ -1,10 +1,11 @@
-// api_serving.hip — C ABI of the quantizing norm and the 4-bit cache: argument validation
+// api_serving.hip — C ABI of the quantizing norm, the 4-bit cache, its page plan and attention: argument validation
 // (host only, before any device call), the device check, then the launch. Semantics:
 // include/fp8q.h.
 #include <algorithm>
 #include <cmath>
 #include <limits>
 
+#include "kv4_attention_shape.h"
 #include "serving.h"
 
 namespace fp8q {
@@ -190,8 +191,6 @@ int rows_entry(bool write, const void* k, int64_t k_st, int64_t k_sh, const void
 }
 
 // ------------------------------------------------------------------ attention
-constexpr int64_t kMaxSequences = 4096;
-
 // Sizes alone; FP8Q_OK also for empty problems.
 int check_attention_sizes(const std::string& pre, int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
                           int64_t max_tokens) {
@@ -206,14 +205,32 @@ int check_attention_sizes(const std::string& pre, int64_t B, int64_t T, int64_t 
   return FP8Q_OK;
 }
 
-int attention_entry(const void* q, int dtype, int64_t q_st, int64_t q_sh, const uint8_t* kc, const uint8_t* ks,
+// What tells the three attention calls apart.
+enum AttnKind { kAttnAll, kAttnWindow, kAttnTree };
+struct AttnMask {
+  AttnKind kind;
+  int causal;                // kAttnAll
+  int64_t window, sinks;     // kAttnWindow
+  const int32_t* tree;       // kAttnTree
+  int64_t tree_st, tree_words;
+};
+
+int check_window(const std::string& pre, int64_t window, int64_t sinks) {
+  if (window < 1) return fail(FP8Q_EINVAL, pre + "window must be at least 1");
+  if (sinks < 0) return fail(FP8Q_EINVAL, pre + "sinks must be >= 0");
+  return FP8Q_OK;
+}
+
+// A window, and sinks, past every possible length are as that length.
+int64_t at_most_tokens(int64_t v) { return std::min(v, int64_t(1) << 30); }
+
+int attention_entry(const std::string& pre, const AttnMask& mask, const void* q, int dtype, int64_t q_st, int64_t q_sh, const uint8_t* kc, const uint8_t* ks,
                     const uint8_t* vc, const uint8_t* vs, int64_t pages, int64_t page_size, int64_t c_sp, int64_t c_st,
                     int64_t c_sh, int64_t s_sp, int64_t s_st, int64_t s_sh, const int32_t* table, int64_t table_sb,
                     int64_t max_pages, const int32_t* kv_lens, const int32_t* q_indptr, void* out, int64_t o_st,
                     int64_t o_sh, float* lse, int64_t l_st, int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
-                    float sm_scale, int causal, void* workspace, int64_t workspace_bytes, void* stream) {
+                    float sm_scale, void* workspace, int64_t workspace_bytes, void* stream) {
   set_error("");
-  const std::string pre = "fp8q_kv4_attention: ";
   if (dtype != FP8Q_DTYPE_BF16 && dtype != FP8Q_DTYPE_F16)
     return fail(FP8Q_EUNSUPPORTED, pre + "dtype must be BF16 or F16");
   int rc = check_cache(pre, kc, ks, vc, vs, pages, page_size, Hkv, D, c_sp, c_st, c_sh, s_sp, s_st, s_sh, false);
@@ -224,18 +241,25 @@ int attention_entry(const void* q, int dtype, int64_t q_st, int64_t q_sh, const 
   if (q_st < 0 || q_sh < 0 || o_st < 0 || o_sh < 0 || l_st < 0 || table_sb < 0)
     return fail(FP8Q_EINVAL, pre + "negative stride");
   if (!std::isfinite(sm_scale)) return fail(FP8Q_EINVAL, pre + "sm_scale must be finite");
+  if (mask.kind == kAttnWindow && (rc = check_window(pre, mask.window, mask.sinks)) != FP8Q_OK) return rc;
+  if (mask.kind == kAttnTree && (mask.tree_words < 0 || mask.tree_st < 0))
+    return fail(FP8Q_EINVAL, pre + "negative size or stride of the tree mask");
   if (workspace_bytes < 0) return fail(FP8Q_EINVAL, pre + "workspace_bytes must be >= 0");
   if (B == 0 || T == 0 || Hq == 0) return FP8Q_OK;
   if (!q || !out || !kv_lens || (!table && max_pages > 0)) return fail(FP8Q_EINVAL, pre + "null tensor pointer");
   if (!q_indptr && T != B) return fail(FP8Q_EINVAL, pre + "without q_indptr every sequence has one query (T == B)");
+  if (mask.kind == kAttnTree && mask.tree_words > 0 && !mask.tree) return fail(FP8Q_EINVAL, pre + "null tree mask");
+  if (mask.kind == kAttnTree && mask.tree_words > (int64_t(1) << 26))
+    return fail(FP8Q_EUNSUPPORTED, pre + "at most 2^26 words of the tree mask for a query");
   if (!disjoint(D, {T, o_st}, {Hq, o_sh})) return fail(FP8Q_EINVAL, pre + "output rows overlap");
   if (lse && T > 1 && l_st < Hq) return fail(FP8Q_EINVAL, pre + "lse rows overlap (l_st < Hq)");
   if (!aligned(q, 16) || q_st % 8 != 0 || q_sh % 8 != 0)
     return fail(FP8Q_EALIGN, pre + "q and its strides must be 16-byte aligned");
   if (!aligned(out, 16) || o_st % 8 != 0 || o_sh % 8 != 0)
     return fail(FP8Q_EALIGN, pre + "out and its strides must be 16-byte aligned");
-  if (!aligned(table, 4) || !aligned(kv_lens, 4) || !aligned(q_indptr, 4) || !aligned(lse, 4))
-    return fail(FP8Q_EALIGN, pre + "page table, lengths, q_indptr and lse must be 4-byte aligned");
+  if (!aligned(table, 4) || !aligned(kv_lens, 4) || !aligned(q_indptr, 4) || !aligned(lse, 4) ||
+      !aligned(mask.tree, 4))
+    return fail(FP8Q_EALIGN, pre + "page table, lengths, q_indptr, tree mask and lse must be 4-byte aligned");
   if (!aligned(workspace, 16)) return fail(FP8Q_EALIGN, pre + "workspace must be 16-byte aligned");
   const int dev = check_current_device();
   if (dev != FP8Q_OK) return dev;
@@ -264,8 +288,96 @@ int attention_entry(const void* q, int dtype, int64_t q_st, int64_t q_sh, const 
   p.scale_log2 = std::min(std::max(std::fabs(sm_scale) * 5.770780163555854f, std::numeric_limits<float>::denorm_min()),
                           std::numeric_limits<float>::max());
   p.q_sign = sm_scale < 0.0f ? 0x80008000u : 0u;
-  p.causal = causal != 0;
-  return launch_kv4_attention(dtype, D, p, workspace, workspace_bytes, static_cast<hipStream_t>(stream));
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  if (mask.kind == kAttnWindow) {
+    p.window = static_cast<int32_t>(at_most_tokens(mask.window));
+    p.sinks = static_cast<int32_t>(at_most_tokens(mask.sinks));
+    p.sink_end = static_cast<int32_t>(sink_stretch(p.sinks));
+    return launch_kv4_window_attention(dtype, D, p, workspace, workspace_bytes, st);
+  }
+  if (mask.kind == kAttnTree) {
+    p.tree = mask.tree;
+    p.tree_st = mask.tree_st;
+    p.tree_words = static_cast<int32_t>(mask.tree_words);
+    return launch_kv4_tree_attention(dtype, D, p, workspace, workspace_bytes, st);
+  }
+  p.causal = mask.causal != 0;
+  return launch_kv4_attention(dtype, D, p, workspace, workspace_bytes, st);
+}
+
+int64_t attention_workspace(const char* pre, int dtype, int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                            int64_t max_tokens, const AttnMask& mask) {
+  set_error("");
+  if (check_attention_sizes(pre, B, T, Hq, Hkv, D, max_tokens) != FP8Q_OK ||
+      (dtype != FP8Q_DTYPE_BF16 && dtype != FP8Q_DTYPE_F16) || B == 0 || T == 0 || Hq == 0 ||
+      (mask.kind == kAttnWindow && check_window(pre, mask.window, mask.sinks) != FP8Q_OK) ||
+      check_current_device() != FP8Q_OK)
+    return 0;
+  if (mask.kind == kAttnWindow)
+    max_tokens = window_tokens(max_tokens, at_most_tokens(mask.window), at_most_tokens(mask.sinks));
+  return kv4_attention_workspace(dtype, B, T, Hq, Hkv, D, max_tokens);
+}
+
+// ------------------------------------------------------------------ page plan
+struct Bytes {
+  const void* at;
+  int64_t n;
+};
+bool overlap(const Bytes& a, const Bytes& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+  return a.n > 0 && b.n > 0 && a.at && b.at && x < y + b.n && y < x + a.n;
+}
+
+int plan_entry(const int32_t* kv_lens, const int32_t* q_lens, int64_t B, const int32_t* free_pages, int64_t F, int32_t* table,
+               int64_t table_sb, int64_t max_pages, int64_t pages, int64_t page_size, int32_t* new_lens, int32_t* q_indptr,
+               int32_t* slots, int32_t* positions, int64_t T, int32_t* pages_taken, void* stream) {
+  set_error("");
+  static const std::string pre = "fp8q_kv4_plan: ";
+  if (B < 0 || F < 0 || T < 0 || pages < 0 || max_pages < 0) return fail(FP8Q_EINVAL, pre + "negative size");
+  if (table_sb < 0) return fail(FP8Q_EINVAL, pre + "negative stride");
+  if (B > kMaxSequences) return fail(FP8Q_EUNSUPPORTED, pre + "at most 4096 sequences");
+  if (log2_exact(page_size) < 0) return fail(FP8Q_EUNSUPPORTED, pre + "page_size must be a power of two below 2^31");
+  if (pages >= (int64_t(1) << 31) || pages * page_size >= (int64_t(1) << 31))
+    return fail(FP8Q_EUNSUPPORTED, pre + "the cache must have fewer than 2^31 slots");
+  if (T >= (int64_t(1) << 30)) return fail(FP8Q_EUNSUPPORTED, pre + "fewer than 2^30 new tokens");
+  if (max_pages > (int64_t(1) << 30) || max_pages * page_size > (int64_t(1) << 30))
+    return fail(FP8Q_EUNSUPPORTED, pre + "at most 2^30 tokens in a sequence's pages");
+  if (F >= (int64_t(1) << 31)) return fail(FP8Q_EUNSUPPORTED, pre + "fewer than 2^31 free pages");
+  if (table_sb > (int64_t(1) << 40)) return fail(FP8Q_EUNSUPPORTED, pre + "a block table stride of at most 2^40");
+  if (!q_indptr || !pages_taken || (B > 0 && (!kv_lens || !q_lens || !new_lens)) || (F > 0 && !free_pages) ||
+      (T > 0 && !slots) || (B > 0 && max_pages > 0 && !table))
+    return fail(FP8Q_EINVAL, pre + "null tensor pointer");
+  if (B > 1 && table_sb < max_pages) return fail(FP8Q_EINVAL, pre + "rows of the block table overlap");
+  if (!aligned(kv_lens, 4) || !aligned(q_lens, 4) || !aligned(free_pages, 4) || !aligned(table, 4) || !aligned(new_lens, 4) ||
+      !aligned(q_indptr, 4) || !aligned(slots, 4) || !aligned(positions, 4) || !aligned(pages_taken, 4))
+    return fail(FP8Q_EALIGN, pre + "every tensor must be 4-byte aligned");
+  // Blocks read the inputs while others write: no output may share memory with anything else.
+  const Bytes all[9] = {{new_lens, 4 * B}, {q_indptr, 4 * (B + 1)}, {slots, 4 * T}, {positions, 4 * T}, {pages_taken, 4},
+                        {table, B > 0 ? 4 * ((B - 1) * table_sb + max_pages) : 0},
+                        {kv_lens, 4 * B}, {q_lens, 4 * B}, {free_pages, 4 * F}};
+  for (int i = 0; i < 6; i++)
+    for (int j = i + 1; j < 9; j++)
+      if (overlap(all[i], all[j])) return fail(FP8Q_EINVAL, pre + "an output overlaps another tensor");
+  const int dev = check_current_device();
+  if (dev != FP8Q_OK) return dev;
+  Kv4PlanParams p{};
+  p.kv_lens = kv_lens;
+  p.q_lens = q_lens;
+  p.free_pages = free_pages;
+  p.table = table;
+  p.table_sb = table_sb;
+  p.max_tokens = max_pages * page_size;
+  p.B = B;
+  p.T = T;
+  p.F = F;
+  p.pages = pages;
+  p.page_shift = log2_exact(page_size);
+  p.new_lens = new_lens;
+  p.q_indptr = q_indptr;
+  p.slots = slots;
+  p.positions = positions;
+  p.pages_taken = pages_taken;
+  return launch_kv4_plan(p, static_cast<hipStream_t>(stream));
 }
 
 }  // namespace
@@ -299,23 +411,60 @@ int fp8q_kv4_read(void* k, int64_t k_st, int64_t k_sh, void* v, int64_t v_st, in
 
 int64_t fp8q_kv4_attention_workspace_size(int dtype, int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
                                           int64_t max_tokens) {
-  if (fp8q::check_attention_sizes("fp8q_kv4_attention_workspace_size: ", B, T, Hq, Hkv, D, max_tokens) != FP8Q_OK ||
-      (dtype != FP8Q_DTYPE_BF16 && dtype != FP8Q_DTYPE_F16) || B == 0 || T == 0 || Hq == 0 ||
-      fp8q::check_current_device() != FP8Q_OK)
-    return 0;
-  return fp8q::kv4_attention_workspace(dtype, B, T, Hq, Hkv, D, max_tokens);
+  return fp8q::attention_workspace("fp8q_kv4_attention_workspace_size: ", dtype, B, T, Hq, Hkv, D, max_tokens,
+                                   {fp8q::kAttnAll, 1, 0, 0, nullptr, 0, 0});
 }
 
-int fp8q_kv4_attention(const void* q, int dtype, int64_t q_st, int64_t q_sh, const uint8_t* kc, const uint8_t* ks,
-                       const uint8_t* vc, const uint8_t* vs, int64_t pages, int64_t page_size, int64_t c_sp,
-                       int64_t c_st, int64_t c_sh, int64_t s_sp, int64_t s_st, int64_t s_sh, const int32_t* table,
-                       int64_t table_sb, int64_t max_pages, const int32_t* kv_lens, const int32_t* q_indptr, void* out,
-                       int64_t o_st, int64_t o_sh, float* lse, int64_t l_st, int64_t B, int64_t T, int64_t Hq,
-                       int64_t Hkv, int64_t D, float sm_scale, int causal, void* workspace, int64_t workspace_bytes,
-                       void* stream) {
-  return fp8q::attention_entry(q, dtype, q_st, q_sh, kc, ks, vc, vs, pages, page_size, c_sp, c_st, c_sh, s_sp, s_st,
-                               s_sh, table, table_sb, max_pages, kv_lens, q_indptr, out, o_st, o_sh, lse, l_st, B, T,
-                               Hq, Hkv, D, sm_scale, causal, workspace, workspace_bytes, stream);
+int fp8q_kv4_attention(
+    const void* q, int dtype, int64_t q_st, int64_t q_sh, const uint8_t* kc, const uint8_t* ks,
+    const uint8_t* vc, const uint8_t* vs, int64_t pages, int64_t page_size, int64_t c_sp, int64_t c_st, int64_t c_sh,
+    int64_t s_sp, int64_t s_st, int64_t s_sh, const int32_t* table, int64_t table_sb, int64_t max_pages,
+    const int32_t* kv_lens, const int32_t* q_indptr, void* out, int64_t o_st, int64_t o_sh, float* lse, int64_t l_st,
+    int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, float sm_scale, int causal, void* workspace,
+    int64_t workspace_bytes, void* stream) {
+  return fp8q::attention_entry("fp8q_kv4_attention: ", {fp8q::kAttnAll, causal, 0, 0, nullptr, 0, 0}, q, dtype, q_st, q_sh, kc, ks, vc, vs,
+                               pages, page_size, c_sp, c_st, c_sh, s_sp, s_st, s_sh, table, table_sb, max_pages, kv_lens,
+                               q_indptr, out, o_st, o_sh, lse, l_st, B, T, Hq, Hkv, D, sm_scale, workspace,
+                               workspace_bytes, stream);
+}
+
+int64_t fp8q_kv4_window_attention_workspace_size(int dtype, int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                                                 int64_t max_tokens, int64_t window, int64_t sinks) {
+  return fp8q::attention_workspace("fp8q_kv4_window_attention_workspace_size: ", dtype, B, T, Hq, Hkv, D, max_tokens,
+                                   {fp8q::kAttnWindow, 1, window, sinks, nullptr, 0, 0});
+}
+
+int fp8q_kv4_window_attention(
+    const void* q, int dtype, int64_t q_st, int64_t q_sh, const uint8_t* kc, const uint8_t* ks,
+    const uint8_t* vc, const uint8_t* vs, int64_t pages, int64_t page_size, int64_t c_sp, int64_t c_st, int64_t c_sh,
+    int64_t s_sp, int64_t s_st, int64_t s_sh, const int32_t* table, int64_t table_sb, int64_t max_pages,
+    const int32_t* kv_lens, const int32_t* q_indptr, void* out, int64_t o_st, int64_t o_sh, float* lse, int64_t l_st,
+    int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, float sm_scale, int64_t window, int64_t sinks,
+    void* workspace, int64_t workspace_bytes, void* stream) {
+  return fp8q::attention_entry("fp8q_kv4_window_attention: ", {fp8q::kAttnWindow, 1, window, sinks, nullptr, 0, 0}, q, dtype, q_st, q_sh, kc, ks, vc, vs,
+                               pages, page_size, c_sp, c_st, c_sh, s_sp, s_st, s_sh, table, table_sb, max_pages, kv_lens,
+                               q_indptr, out, o_st, o_sh, lse, l_st, B, T, Hq, Hkv, D, sm_scale, workspace,
+                               workspace_bytes, stream);
+}
+
+int fp8q_kv4_tree_attention(
+    const void* q, int dtype, int64_t q_st, int64_t q_sh, const uint8_t* kc, const uint8_t* ks,
+    const uint8_t* vc, const uint8_t* vs, int64_t pages, int64_t page_size, int64_t c_sp, int64_t c_st, int64_t c_sh,
+    int64_t s_sp, int64_t s_st, int64_t s_sh, const int32_t* table, int64_t table_sb, int64_t max_pages,
+    const int32_t* kv_lens, const int32_t* q_indptr, void* out, int64_t o_st, int64_t o_sh, float* lse, int64_t l_st,
+    int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, float sm_scale, const int32_t* tree_mask,
+    int64_t tree_st, int64_t tree_words, void* workspace, int64_t workspace_bytes, void* stream) {
+  return fp8q::attention_entry("fp8q_kv4_tree_attention: ", {fp8q::kAttnTree, 0, 0, 0, tree_mask, tree_st, tree_words}, q, dtype, q_st, q_sh, kc, ks, vc, vs,
+                               pages, page_size, c_sp, c_st, c_sh, s_sp, s_st, s_sh, table, table_sb, max_pages, kv_lens,
+                               q_indptr, out, o_st, o_sh, lse, l_st, B, T, Hq, Hkv, D, sm_scale, workspace,
+                               workspace_bytes, stream);
+}
+
+int fp8q_kv4_plan(const int32_t* kv_lens, const int32_t* q_lens, int64_t B, const int32_t* free_pages, int64_t F,
+                  int32_t* table, int64_t table_sb, int64_t max_pages, int64_t pages, int64_t page_size, int32_t* new_lens,
+                  int32_t* q_indptr, int32_t* slots, int32_t* positions, int64_t T, int32_t* pages_taken, void* stream) {
+  return fp8q::plan_entry(kv_lens, q_lens, B, free_pages, F, table, table_sb, max_pages, pages, page_size, new_lens,
+                          q_indptr, slots, positions, T, pages_taken, stream);
 }
 
 }  // extern "C"

@@ -86,6 +86,15 @@ inline Cut wide_cut(int64_t units, int64_t max_tokens, int64_t blocks) {
   return steps <= kMostWideSteps && steps <= 9 + 2 * units * steps / blocks ? Cut::kWhole : Cut::kSplit;
 }
 
+// The sinks' stretch of a window call: steps of 64 tokens (the longest step of any kernel).
+inline int64_t sink_stretch(int64_t sinks) { return (sinks + 63) / 64 * 64; }
+
+// The most tokens that a unit of a window call reads: both stretches, the windows of its queries (at most 128)
+// reaching one token further for each after the first, and their start rounded down to a step.
+inline int64_t window_tokens(int64_t max_tokens, int64_t window, int64_t sinks) {
+  return std::min(max_tokens, sink_stretch(sinks) + window + 128 - 1 + 64 - 1);
+}
+
 struct AttnShape {
   int rows;        // of a tile
   bool tall;

@@ -79,11 +79,38 @@ struct Kv4AttnParams {
   int32_t blocks;            // split only, as the next two: blocks that share the line of spans
   int32_t* plan;             // [2][B + 1] spans and query tiles before each sequence
   float* parts;              // partial outputs, maxima and sums by piece
+  int32_t window, sinks, sink_end;  // window calls: sink_end is sinks rounded up to a step
+  const int32_t* tree;       // tree calls: [T][tree_words] words of drafted tokens that a query sees
+  int64_t tree_st;
+  int32_t tree_words;
 };
 
 // Bytes of workspace with which attention of this shape splits the cache axis on the current
 // device (0: it never does).
 int64_t kv4_attention_workspace(int dtype, int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_tokens);
-int launch_kv4_attention(int dtype, int64_t D, Kv4AttnParams p, void* ws, int64_t ws_bytes, hipStream_t stream);
+int launch_kv4_attention(int dtype, int64_t D, const Kv4AttnParams& p, void* ws, int64_t ws_bytes, hipStream_t stream);
+int launch_kv4_window_attention(int dtype, int64_t D, const Kv4AttnParams& p, void* ws, int64_t ws_bytes, hipStream_t stream);
+int launch_kv4_tree_attention(int dtype, int64_t D, const Kv4AttnParams& p, void* ws, int64_t ws_bytes, hipStream_t stream);
+
+// ------------------------------------------------------------------ page plan
+constexpr int64_t kMaxSequences = 4096;  // of one call
+
+struct Kv4PlanParams {
+  const int32_t* kv_lens;     // [B]
+  const int32_t* q_lens;      // [B]
+  const int32_t* free_pages;  // [F]
+  int32_t* table;             // [B][max_pages]
+  int64_t table_sb;
+  int64_t max_tokens;         // max_pages << page_shift
+  int64_t B, T, F, pages;
+  int32_t page_shift;
+  int32_t* new_lens;          // [B]
+  int32_t* q_indptr;          // [B + 1]
+  int32_t* slots;             // [T]
+  int32_t* positions;         // [T], or nullptr
+  int32_t* pages_taken;       // [1]
+};
+
+int launch_kv4_plan(const Kv4PlanParams& p, hipStream_t stream);
 
 }  // namespace fp8q

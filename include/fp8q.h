@@ -1,7 +1,8 @@
 /*
  * fp8q.h — C ABI of libfp8q.so: per-token-group FP8 quantization of activations, the
- * block-scaled FP8 GEMMs that consume it, and the operators between them in a serving layer
- * (quantizing norm, 4-bit key/value cache, attention over it), for AMD Instinct MI355X (gfx950).
+ * block-scaled FP8 GEMMs that consume it, their 4-bit (MXFP4) counterparts, and the operators
+ * between them in a serving layer (quantizing norm, 4-bit key/value cache with its page plan,
+ * attention over it), for AMD Instinct MI355X (gfx950).
  *
  * What the calls compute is defined by these sources:
  *   [PR30924]  prhub report of sglang PR #30924, "[JIT] Trait-driven
@@ -321,6 +322,67 @@ int fp8q_grouped_gemm_contiguous(const uint8_t* a, int64_t lda,
                                  int64_t T, int64_t W, int64_t N, int64_t K, void* stream);
 
 /*
+ * fp8q_mxfp4_quant, fp8q_silu_mul_mxfp4_quant — rows as e2m1 codes with one UE8M0 scale per 32
+ * elements (MXFP4), the operands of fp8q_gemm_mxfp4
+ *
+ * x is [M][K] of in_dtype (row m at x + m*x_sm), or for the silu call [M][2K], gate | up, of which
+ * y = silu(gate) * up, as defined by fp8q_silu_mul_group_quant, is quantized in the place of x. For
+ * every group of 32 consecutive elements of a row, by the rule of the 4-bit cache below:
+ *   amax = max(max |x_i|, 1e-10f); 2^(byte-127) is the smallest power of two >= amax / 6;
+ *   code_i = e2m1_round_nearest_even( x_i / 2^(byte-127) )
+ * q holds K / 2 bytes per row (row m at q + m*q_sm bytes): e2m1 codes (sign, 2 exponent and 1 mantissa
+ * bits: 0, 0.5, 1, 1.5, 2, 3, 4, 6), element 2i in the low half of byte i. The scale of group g of
+ * row m is at s + m*s_sm + g*s_sg as in fp8q_group_quant: scale_fmt UE8M0 (bytes) or UE8M0_PACKED
+ * (words of four groups; K % 128 == 0), row- or column-major by the strides.
+ *
+ * fp8q_mxfp4_dequant — such rows back as x [M][K] of out_dtype: code times scale, rounded to out_dtype
+ * (exact in F32, and in BF16 from scale byte 2 on); a value past the type's largest finite one becomes
+ * that one. (Codes round up: 57344 and more written in F16 may be held as 65536.) A scale byte of 255
+ * gives NaN. x rows must not overlap.
+ *
+ * Requirements (else the status in brackets): dtype in {BF16, F16, F32}, scale_fmt as above, K <= 2^30
+ * [EUNSUPPORTED]; K % 32 == 0 (packed: 128), M, K >= 0, strides non-negative, written rows not
+ * overlapping, scale strides row- or column-major [EINVAL]; x, q and their row strides 16-byte aligned,
+ * packed words 4-byte [EALIGN].
+ */
+int fp8q_mxfp4_quant(const void* x, int in_dtype, int64_t M, int64_t K, int64_t x_sm,
+                     uint8_t* q, int64_t q_sm, void* s, int scale_fmt, int64_t s_sm, int64_t s_sg, void* stream);
+
+int fp8q_silu_mul_mxfp4_quant(const void* x, int in_dtype, int64_t M, int64_t K, int64_t x_sm,
+                              uint8_t* q, int64_t q_sm, void* s, int scale_fmt, int64_t s_sm, int64_t s_sg,
+                              void* stream);
+
+int fp8q_mxfp4_dequant(const uint8_t* q, int64_t q_sm, const void* s, int scale_fmt, int64_t s_sm, int64_t s_sg,
+                       void* x, int out_dtype, int64_t M, int64_t K, int64_t x_sm, void* stream);
+
+/*
+ * fp8q_gemm_mxfp4 — Y = dequant(A) * dequant(B)^T of two MXFP4 operands, bf16 output
+ *
+ * A is [M][K] and B [N][K] in e2m1 codes, K / 2 bytes per row (row m of A at a + m*lda bytes, row n of B at
+ * b + n*ldb), element 2i in the low half of byte i; Y is [M][N] bf16 (row m at y + m*ldy elements):
+ *   Y[m][n] = bf16_rne( sum_k 2^(sa-127) dec(A[m][k]) * 2^(sb-127) dec(B[n][k]) )
+ * with one UE8M0 byte per (row, k/32). sa_fmt UE8M0_PACKED: byte k/32 % 4 of the 32-bit word at
+ * sa + 4*(m*sa_sm + (k/128)*sa_sk) bytes, any strides (column-major words, as the quantizer writes them, are
+ * read fastest); sa_fmt UE8M0: row-major bytes (sa_sk == 1) whose rows lie a multiple of 4 bytes apart. sb
+ * likewise. Accumulation is fp32; byte 0 counts as 2^-127, and 255 gives NaN.
+ *
+ * fp8q_gemm_mxfp4_workspace_size returns the bytes of workspace with which the call splits K over more of
+ * the device (0: it does not, or the sizes are refused). With a smaller or NULL workspace the call runs
+ * unsplit: same results up to the order of fp32 sums, each deterministic. The library writes only that many
+ * bytes; calls that overlap in time must not share a workspace.
+ *
+ * Requirements: scale formats as above [EUNSUPPORTED]; M, N, K >= 0 and below 2^31 [EUNSUPPORTED], K % 128 == 0
+ * [EINVAL]; lda, ldb >= K / 2, ldy >= N [EINVAL]; a, b and their row strides and the workspace 16-byte
+ * aligned, scales and their rows 4-byte, y 2-byte [EALIGN].
+ */
+int64_t fp8q_gemm_mxfp4_workspace_size(int64_t M, int64_t N, int64_t K);
+
+int fp8q_gemm_mxfp4(const uint8_t* a, int64_t lda, const void* sa, int sa_fmt, int64_t sa_sm, int64_t sa_sk,
+                    const uint8_t* b, int64_t ldb, const void* sb, int sb_fmt, int64_t sb_sn, int64_t sb_sk,
+                    uint16_t* y, int64_t ldy, int64_t M, int64_t N, int64_t K,
+                    void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
  * fp8q_rms_norm_group_quant — root-mean-square norm of each row, with the residual's addition
  * before it and group quantization to e4m3 after it
  *
@@ -444,6 +506,81 @@ int fp8q_kv4_attention(const void* q, int dtype, int64_t q_st, int64_t q_sh,
                        void* out, int64_t o_st, int64_t o_sh, float* lse, int64_t l_st,
                        int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
                        float sm_scale, int causal, void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * fp8q_kv4_window_attention — attention over the last `window` tokens and the first `sinks`
+ *
+ * fp8q_kv4_attention with causal == 1 in which a query that would see tokens 0 .. p (its own place p being
+ * the last) sees those j of them with j > p - window or j < sinks: `window` tokens with its own, and the
+ * first `sinks` of the sequence. Pages that no query of a sequence sees are not read; their table entries may
+ * be anything. window >= 1, sinks >= 0 [EINVAL]. Everything else is as there, the workspace's size by
+ * fp8q_kv4_window_attention_workspace_size.
+ */
+int64_t fp8q_kv4_window_attention_workspace_size(int dtype, int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                                                 int64_t max_tokens, int64_t window, int64_t sinks);
+
+int fp8q_kv4_window_attention(const void* q, int dtype, int64_t q_st, int64_t q_sh,
+                              const uint8_t* kc, const uint8_t* ks, const uint8_t* vc, const uint8_t* vs,
+                              int64_t pages, int64_t page_size,
+                              int64_t c_sp, int64_t c_st, int64_t c_sh, int64_t s_sp, int64_t s_st, int64_t s_sh,
+                              const int32_t* table, int64_t table_sb, int64_t max_pages, const int32_t* kv_lens,
+                              const int32_t* q_indptr,
+                              void* out, int64_t o_st, int64_t o_sh, float* lse, int64_t l_st,
+                              int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                              float sm_scale, int64_t window, int64_t sinks,
+                              void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * fp8q_kv4_tree_attention — attention of drafted tokens that form a tree
+ *
+ * fp8q_kv4_attention in which the n query rows of a sequence are drafted tokens, held at its last n cached
+ * places in the order of the rows. Drafted token i sees every token before the draft (the first
+ * kv_lens[b] - n) and drafted token j exactly if bit j % 32 of word tree_mask[t*tree_st + j / 32] is set, t its
+ * row of q: for a tree, itself and its ancestors (itself too only if its bit is set). tree_mask is a DEVICE
+ * int32 [T][tree_words]; drafted tokens from 32 * tree_words on are not seen, and bits past the draft, or of
+ * drafted tokens that kv_lens[b] < n leaves out of the cache (the first n - kv_lens[b]), do nothing. tree_words
+ * <= 2^26 [EUNSUPPORTED], tree_words, tree_st >= 0, tree_mask not NULL unless tree_words == 0 [EINVAL],
+ * 4-byte aligned [EALIGN]. Everything else is as there, the workspace's size too
+ * (fp8q_kv4_attention_workspace_size).
+ */
+int fp8q_kv4_tree_attention(const void* q, int dtype, int64_t q_st, int64_t q_sh,
+                            const uint8_t* kc, const uint8_t* ks, const uint8_t* vc, const uint8_t* vs,
+                            int64_t pages, int64_t page_size,
+                            int64_t c_sp, int64_t c_st, int64_t c_sh, int64_t s_sp, int64_t s_st, int64_t s_sh,
+                            const int32_t* table, int64_t table_sb, int64_t max_pages, const int32_t* kv_lens,
+                            const int32_t* q_indptr,
+                            void* out, int64_t o_st, int64_t o_sh, float* lse, int64_t l_st,
+                            int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                            float sm_scale, const int32_t* tree_mask, int64_t tree_st, int64_t tree_words,
+                            void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * fp8q_kv4_plan — page bookkeeping of one serving step over the paged cache, from the requests' lengths
+ *
+ * All arrays are DEVICE int32. Sequence b of B holds kv_lens[b] cached tokens (clamped to [0, max_pages *
+ * page_size]) and gets q_lens[b] new ones (negative: none); they are packed one sequence after the other:
+ *   q_indptr[b] ([B + 1]): new tokens before sequence b; new_lens[b] = kv_lens[b] + those of b
+ *   slots[t], positions[t] ([T]; positions may be NULL): of the i-th new token of b, its position
+ *     kv_lens[b] + i and the slot of that position, as fp8q_kv4_write takes it
+ *   table ([B][max_pages], row b at table + b*table_sb): entries of the pages that b newly needs, those from
+ *     ceil(kv_lens[b] / page_size) on, are written; the others are kept, and the last page that is held
+ *     already is read if it has room
+ *   pages_taken[0]: the new pages of all sequences. They are free_pages[0], free_pages[1], ... ([F]), given to
+ *     the sequences in their order.
+ * New tokens past T are left out everywhere. A position past the table's row has slot -1 and does not count in
+ * new_lens. Where the free pages do not suffice (pages_taken[0] > F), or a page is not in [0, pages), the
+ * entry and the slots are -1; new_lens and q_indptr are as if it had a page, and the caller, who sees
+ * pages_taken[0], has to take the step back. slots and positions past the last new token are -1. B == 0 and
+ * T == 0 are ordinary calls. The arrays written must share no memory with any other [EINVAL].
+ *
+ * Requirements: B <= 4096, page_size a power of two, pages * page_size < 2^31, max_pages * page_size <= 2^30,
+ * T < 2^30, F < 2^31, table_sb <= 2^40 [EUNSUPPORTED]; sizes and strides non-negative, table_sb >= max_pages (B > 1), pointers
+ * not NULL where there is something to hold [EINVAL]; 4-byte alignment [EALIGN].
+ */
+int fp8q_kv4_plan(const int32_t* kv_lens, const int32_t* q_lens, int64_t B, const int32_t* free_pages, int64_t F,
+                  int32_t* table, int64_t table_sb, int64_t max_pages, int64_t pages, int64_t page_size,
+                  int32_t* new_lens, int32_t* q_indptr, int32_t* slots, int32_t* positions, int64_t T,
+                  int32_t* pages_taken, void* stream);
 
 /* Human-readable name of a status code. Never returns NULL. */
 const char* fp8q_status_string(int status);
