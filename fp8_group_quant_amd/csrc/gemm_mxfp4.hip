@@ -10,27 +10,45 @@ namespace {
 
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v16f __attribute__((ext_vector_type(16)));
+typedef float v4f __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kFp4 = 4;     // operand format of the matrix instruction
-constexpr int kStepK = 128;  // elements of K per step
-constexpr int kRowBytes = kStepK / 2;
+constexpr int kStepK = 128;  // K is split, and scale words are counted, in units of 128 elements
+constexpr int kUnit = kStepK / 2;  // their bytes
 
-template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, int STAGES_, int BLOCKS_>
+// A block's tile: BM x BN outputs by WAVES_M x WAVES_N waves, in steps of QUARTERS * 64 elements of K, STAGES of them in
+// LDS, BLOCKS of a CU.
+template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, int QUARTERS_, int STAGES_, int BLOCKS_>
 struct Tile {
-  static constexpr int BM = BM_, BN = BN_, WAVES_M = WAVES_M_, WAVES_N = WAVES_N_, STAGES = STAGES_;
-  static constexpr int kBlocks = BLOCKS_;  // of a CU
+  static constexpr int BM = BM_, BN = BN_, WAVES_M = WAVES_M_, WAVES_N = WAVES_N_, QUARTERS = QUARTERS_, STAGES = STAGES_;
+  static constexpr int kBlocks = BLOCKS_;
+  static constexpr bool kSplit = false;  // whether K is split
   static constexpr int kWaves = WAVES_M * WAVES_N, kThreads = 64 * kWaves;
   static constexpr int WTM = BM / WAVES_M, WTN = BN / WAVES_N, SM = WTM / 32, SN = WTN / 32;
-  // one stage: rows of A and B, then their scale words
-  static constexpr int kB = BM * kRowBytes, kSA = kB + BN * kRowBytes, kSB = kSA + 4 * BM, kStage = kSB + 4 * BN;
+  static constexpr int kRow = 32 * QUARTERS, kWords = kRow / kUnit;  // bytes and scale words of a row and step
+  // one stage: rows of A and B, then their scale words [kWords][BM], [kWords][BN]
+  static constexpr int kB = BM * kRow, kSA = kB + BN * kRow, kSB = kSA + 4 * kWords * BM, kStage = kSB + 4 * kWords * BN;
   static constexpr int kLds = STAGES * kStage;
-  // loads of a wave and step: 1 KB pieces of 8 rows, and 64 scale words each
-  static constexpr int kLA = BM / 16 / kWaves, kLB = BN / 16 / kWaves, kLS = (BM + BN) / 64 / kWaves;
-  static constexpr int kLoads = kLA + kLB + kLS, kMma = SM * SN, kFirst = kLoads / 2;
-  static_assert(kLA * kWaves * 16 == BM && kLB * kWaves * 16 == BN && kLS * kWaves * 64 == BM + BN, "load split");
+  // loads of a wave and step: 1 KB pieces of kPiece rows, and 64 scale words each
+  static constexpr int kPiece = 1024 / kRow, kLA = BM / kPiece / kWaves, kLB = BN / kPiece / kWaves;
+  static constexpr int kGroups = (BM + BN) / 64, kPer = (kGroups + kWaves - 1) / kWaves;  // groups of 64 scale rows
+  static constexpr int kLoads = kLA + kLB + kPer * kWords, kMma = SM * SN;
+  static constexpr int kFirst = kLoads / 2;  // that go out in a step's last quarter, the others in the next one's first
+  static_assert(QUARTERS == 2 || QUARTERS == 4, "64 or 128 bytes");
+  static_assert(kLA * kWaves * kPiece == BM && kLB * kWaves * kPiece == BN && BM % 64 == 0 && BN % 64 == 0, "load split");
+  static_assert(kRow == 64 || (kLA % 2 == 0 && kLB % 2 == 0), "a wave's pieces alternate from an even one on");
+  static_assert(SN % 2 == 0, "outputs go through LDS in pairs of subtiles");
   static_assert(kBlocks * (kLds + kWaves * 32 * 144) <= 160 * 1024, "LDS");
+
+  // Rows that the same lanes of a fragment read lie in all banks: 16-byte chunk c of a row is at c ^ swizzle(row).
+  static __device__ __forceinline__ int swizzle(int row) { return kRow == 64 ? (row >> 2) & 3 : (row >> 1) & 7; }
+};
+
+template <class T>
+struct Splitting : T {
+  static constexpr bool kSplit = true;
 };
 
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
@@ -60,8 +78,6 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
          static_cast<uint32_t>(__builtin_bit_cast(uint16_t, static_cast<__bf16>(b))) << 16;
 }
 
-__device__ __forceinline__ int swizzle(int row) { return (row >> 2) & 3; }
-
 constexpr int kGroupM = 4;
 
 // The kernel's arguments, read again where they are used, so that they hold no registers in the loop.
@@ -72,31 +88,38 @@ __device__ __forceinline__ Args arguments() {
   return a;
 }
 
+__device__ __forceinline__ int32_t uniform(int32_t v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// Unit t of the work: a tile and one of p->splits ranges of K (units first .. first + units - 1). The host makes sure
+// that there are fewer than 2^31.
 struct Place {
   int64_t m0, n0;
+  int split, first, units;
 };
-// The host makes sure that there are fewer than 2^31 tiles.
 template <class C>
 __device__ __forceinline__ Place place_of(Args p, int32_t t) {
   const int32_t tiles_m = static_cast<int32_t>((p->M + C::BM - 1) / C::BM), tiles_n = static_cast<int32_t>((p->N + C::BN - 1) / C::BN);
-  const int32_t group = t / tiles_n / kGroupM;  // of kGroupM rows of tiles
-  const int32_t first = group * kGroupM, rows = min(tiles_m - first, kGroupM), at = t - first * tiles_n;
-  const int32_t n = at / rows;
-  return Place{int64_t(first + at - n * rows) * C::BM, int64_t(n) * C::BN};
+  const int32_t split = C::kSplit ? uniform(t / (tiles_m * tiles_n)) : 0;
+  t -= split * tiles_m * tiles_n;
+  const int32_t first = uniform(t / tiles_n / kGroupM) * kGroupM;  // rows of tiles are taken kGroupM at a time
+  const int32_t rows = min(tiles_m - first, kGroupM), at = t - first * tiles_n, n = uniform(at / rows);
+  const int32_t all = static_cast<int32_t>(p->K / kStepK);  // splits * all < 2^31
+  const int32_t k0 = C::kSplit ? uniform(all * split / p->splits) : 0, k1 = C::kSplit ? uniform(all * (split + 1) / p->splits) : all;
+  return Place{int64_t(first + at - n * rows) * C::BM, int64_t(n) * C::BN, split, k0, k1 - k0};
 }
 
 // What a block's loads of one tile start from: the operands' rows as buffers (what lies past the last row's end is not
 // read), and the scale words of the lanes' rows.
 template <class C>
 struct Source {
-  static constexpr int kPer = (C::BM + C::BN) / 64 / C::kWaves;  // groups of 64 scale rows per wave
   v4i a, b;
-  const uint8_t* s_base[kPer];
-  uint32_t s_off[kPer];
+  const uint8_t* s_base[C::kPer];
+  uint32_t s_off[C::kPer];
 
-  // Of scale group q of a wave: whether it is A's, and its first row.
-  static __device__ __forceinline__ bool of_a(int q, int wave) { return q * C::kWaves + wave < C::BM / 64; }
-  static __device__ __forceinline__ int first(int q, int wave) { return (q * C::kWaves + wave - (of_a(q, wave) ? 0 : C::BM / 64)) * 64; }
+  // Of scale group q of a wave: whether it is A's, and its first row. (Where the groups do not divide, some are loaded twice.)
+  static __device__ __forceinline__ int group(int q, int wave) { return (q * C::kWaves + wave) % C::kGroups; }
+  static __device__ __forceinline__ bool of_a(int q, int wave) { return group(q, wave) < C::BM / 64; }
+  static __device__ __forceinline__ int first(int q, int wave) { return (group(q, wave) - (of_a(q, wave) ? 0 : C::BM / 64)) * 64; }
   static __device__ __forceinline__ v4i buffer(const uint8_t* base, int64_t rows, int64_t ld, int64_t bytes) {
     const uint64_t at = reinterpret_cast<uint64_t>(base);
     const uint32_t size = static_cast<uint32_t>(min((rows - 1) * ld + bytes, int64_t(0xFFFFFFFF)));
@@ -105,46 +128,50 @@ struct Source {
   __device__ __forceinline__ void enter(int32_t tile, int lane, int wave) {
     const Args p = arguments();
     const Place at = place_of<C>(p, tile);
-    a = buffer(p->a + at.m0 * p->lda, p->M - at.m0, p->lda, p->K / 2);
-    b = buffer(p->b + at.n0 * p->ldb, p->N - at.n0, p->ldb, p->K / 2);
+    const int64_t skip = int64_t(at.first) * kUnit, bytes = p->K / 2 - skip;
+    a = buffer(p->a + at.m0 * p->lda + skip, p->M - at.m0, p->lda, bytes);
+    b = buffer(p->b + at.n0 * p->ldb + skip, p->N - at.n0, p->ldb, bytes);
 #pragma unroll
-    for (int q = 0; q < kPer; q++) {
+    for (int q = 0; q < C::kPer; q++) {
       const bool is_a = of_a(q, wave);
       const int64_t sm = is_a ? p->sa_sm : p->sb_sn, rows = is_a ? p->M - 1 - at.m0 : p->N - 1 - at.n0;
-      s_base[q] = is_a ? p->sa + at.m0 * sm * 4 : p->sb + at.n0 * sm * 4;
+      s_base[q] = (is_a ? p->sa + at.m0 * sm * 4 : p->sb + at.n0 * sm * 4) + at.first * (is_a ? p->sa_sk : p->sb_sk) * 4;
       s_off[q] = static_cast<uint32_t>(min(int64_t(first(q, wave) + lane), rows) * sm * 4);
     }
   }
 };
 
 // The loads of a block's steps, one after the other through its tiles; past the last tile its steps again, so that every
-// step issues the same loads. Rows past an operand's end bring anything: their products are not stored. The
-// last step of an odd number of K halves brings bytes of the next row (or nothing), which are not used.
+// step issues the same loads. Rows past an operand's end bring anything: their products are not stored. Where a step holds
+// two units of K, the last one may hold only one: the other's bytes are the next row's (or nothing), and not used.
 template <class C>
 struct Loader {
-  static constexpr int kPer = Source<C>::kPer;
   const uint32_t lds;
-  const int lane, wave, steps;
-  const int32_t stride, stop;   // of the tiles
-  const uint32_t lda16, ldb16;    // bytes of 8 rows
-  uint32_t a_off, b_off;  // the lane's part: pieces of 8 rows, even and odd ones
-  int64_t s_step[kPer];         // bytes between the words of two K halves
-  const bool odd;
+  const int lane, wave, units, steps;  // units of K, steps
+  const int32_t stride, stop;          // of the tiles
+  const uint32_t lda_piece, ldb_piece;  // bytes of a piece's rows
+  uint32_t a_off[2], b_off[2];          // the lane's part: even and odd pieces
+  int64_t s_step[C::kPer];              // bytes between the words of two units
   int32_t tile;
   int step;
   uint32_t stage;  // its offset
   Source<C> now, next;
 
-  __device__ __forceinline__ Loader(const TileSpan& s, uint32_t lds_at, int lane_, int wave_, int n, bool odd_)
-      : lds(lds_at), lane(lane_), wave(wave_), steps(n), stride(static_cast<int32_t>(s.stride)), stop(static_cast<int32_t>(s.end)),
-        lda16(static_cast<uint32_t>(16 * arguments()->lda)), ldb16(static_cast<uint32_t>(16 * arguments()->ldb)), odd(odd_),
+  __device__ __forceinline__ Loader(const TileSpan& s, uint32_t lds_at, int lane_, int wave_, int units_)
+      : lds(lds_at), lane(lane_), wave(wave_), units(units_), steps((units_ + C::kWords - 1) / C::kWords),
+        stride(static_cast<int32_t>(s.stride)), stop(static_cast<int32_t>(s.end)),
+        lda_piece(static_cast<uint32_t>(C::kPiece * arguments()->lda)), ldb_piece(static_cast<uint32_t>(C::kPiece * arguments()->ldb)),
         tile(static_cast<int32_t>(s.beg)), step(0), stage(0) {
-    const int row = lane >> 2;
-    const uint32_t chunk = 16 * ((lane & 3) ^ swizzle(row));
-    a_off = row * (lda16 >> 4) + chunk;
-    b_off = row * (ldb16 >> 4) + chunk;
+    constexpr int kChunks = C::kRow / 16;
+    const int row = lane / kChunks;
 #pragma unroll
-    for (int q = 0; q < kPer; q++) s_step[q] = 4 * (Source<C>::of_a(q, wave) ? arguments()->sa_sk : arguments()->sb_sk);
+    for (int q = 0; q < 2; q++) {
+      const uint32_t chunk = 16 * ((lane % kChunks) ^ C::swizzle(C::kPiece * q + row));
+      a_off[q] = row * (lda_piece / C::kPiece) + chunk;
+      b_off[q] = row * (ldb_piece / C::kPiece) + chunk;
+    }
+#pragma unroll
+    for (int q = 0; q < C::kPer; q++) s_step[q] = 4 * (Source<C>::of_a(q, wave) ? arguments()->sa_sk : arguments()->sb_sk);
     now.enter(tile, lane, wave);
   }
   // Looks up the tile after the loads' present one, once per tile that is computed: every tile has one step at which the
@@ -157,14 +184,15 @@ struct Loader {
   __device__ __forceinline__ void issue(int n) {
     const uint32_t at = lds + stage;
     if (n < C::kLA) {
-      dma16(at + (wave * C::kLA + n) * 1024, now.a, a_off, (wave * C::kLA + n) * lda16 + step * kRowBytes);
+      dma16(at + (wave * C::kLA + n) * 1024, now.a, a_off[n & 1], (wave * C::kLA + n) * lda_piece + step * C::kRow);
     } else if (n < C::kLA + C::kLB) {
       const int q = n - C::kLA;
-      dma16(at + C::kB + (wave * C::kLB + q) * 1024, now.b, b_off, (wave * C::kLB + q) * ldb16 + step * kRowBytes);
+      dma16(at + C::kB + (wave * C::kLB + q) * 1024, now.b, b_off[q & 1], (wave * C::kLB + q) * ldb_piece + step * C::kRow);
     } else {
-      const int q = n - C::kLA - C::kLB;
-      const bool is_a = Source<C>::of_a(q, wave);
-      dma4(at + (is_a ? C::kSA : C::kSB) + 4 * Source<C>::first(q, wave), now.s_base[q], now.s_off[q]);
+      const int q = (n - C::kLA - C::kLB) / C::kWords, word = (n - C::kLA - C::kLB) % C::kWords;
+      const bool is_a = Source<C>::of_a(q, wave), there = word == 0 || C::kWords * step + word < units;
+      dma4(at + (is_a ? C::kSA + 4 * word * C::BM : C::kSB + 4 * word * C::BN) + 4 * Source<C>::first(q, wave),
+           now.s_base[q] + (word > 0 && there ? s_step[q] : 0), now.s_off[q]);
     }
   }
   // On to the next step (without a branch, across which products could be moved).
@@ -178,8 +206,8 @@ struct Loader {
       now.b[i] = last ? next.b[i] : now.b[i];
     }
 #pragma unroll
-    for (int q = 0; q < kPer; q++) {
-      now.s_base[q] = last ? next.s_base[q] : now.s_base[q] + s_step[q];
+    for (int q = 0; q < C::kPer; q++) {
+      now.s_base[q] = last ? next.s_base[q] : now.s_base[q] + C::kWords * s_step[q];
       now.s_off[q] = last ? next.s_off[q] : now.s_off[q];
     }
   }
@@ -190,27 +218,28 @@ struct Loader {
   }
 };
 
+// v_mfma_scale_f32_32x32x64: lane (r, h) of an operand holds row r's 32 elements of K block h and that block's scale byte.
 template <class C>
 struct Compute {
   const uint8_t* smem;
-  uint32_t a_at[2], b_at[2];  // LDS offsets of the lane's first subtile for each half of a step
-  uint32_t sa_at, sb_at, shift;
+  uint32_t a_at[C::QUARTERS], b_at[C::QUARTERS];  // LDS offsets of the lane's first subtile for each quarter of a step
+  uint32_t sa_at, sb_at, pick;
   u32x4 fa[2][C::SM], fb[2][C::SN];
-  uint32_t wa[C::SM], wb[C::SN];  // scale words of the next step
-  uint32_t ea[C::SM], eb[C::SN];  // of this one: its halves' bytes are 0 and 2
+  uint32_t wa[C::kWords][C::SM], wb[C::kWords][C::SN];  // scale words of the next step
+  uint32_t ea[C::SM], eb[C::SN];                        // scale bytes of this step's quarters
   v16f acc[C::SM][C::SN];
 
   __device__ __forceinline__ Compute(const uint8_t* s, int lane, int wm, int wn) : smem(s) {
     const int r = lane & 31, h = lane >> 5;
 #pragma unroll
-    for (int k = 0; k < 2; k++) {
-      const int chunk = 16 * ((2 * k + h) ^ swizzle(r));
-      a_at[k] = (wm * C::WTM + r) * kRowBytes + chunk;
-      b_at[k] = C::kB + (wn * C::WTN + r) * kRowBytes + chunk;
+    for (int k = 0; k < C::QUARTERS; k++) {
+      const int chunk = 16 * ((2 * k + h) ^ C::swizzle(r));
+      a_at[k] = (wm * C::WTM + r) * C::kRow + chunk;
+      b_at[k] = C::kB + (wn * C::WTN + r) * C::kRow + chunk;
     }
     sa_at = C::kSA + 4 * (wm * C::WTM + r);
     sb_at = C::kSB + 4 * (wn * C::WTN + r);
-    shift = 8 * h;
+    pick = C::kWords == 1 ? 8 * h : h ? 0x07050301u : 0x06040200u;
   }
   __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -218,41 +247,40 @@ struct Compute {
 #pragma unroll
       for (int j = 0; j < C::SN; j++) acc[i][j] = v16f{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   }
-  // Read number n of half K of the stage at offset `st`: operands of A and B, then (K = 0) the scale words.
+  static constexpr int kReads = C::SM + C::SN, kReads0 = (1 + C::kWords) * kReads;
+  // Read number n of quarter K of the stage at offset `st`: operands of A and B, then (K = 0) the scale words.
   template <int K>
   __device__ __forceinline__ void read(int n, uint32_t st) {
     if (n < C::SM) {
-      fa[K][n] = *reinterpret_cast<const u32x4*>(smem + st + a_at[K] + n * 32 * kRowBytes);
-    } else if (n < C::SM + C::SN) {
-      fb[K][n - C::SM] = *reinterpret_cast<const u32x4*>(smem + st + b_at[K] + (n - C::SM) * 32 * kRowBytes);
-    } else if (K == 0 && n < 2 * C::SM + C::SN) {
-      wa[n - C::SM - C::SN] = *reinterpret_cast<const uint32_t*>(smem + st + sa_at + 128 * (n - C::SM - C::SN));
-    } else if (K == 0 && n < 2 * (C::SM + C::SN)) {
-      wb[n - 2 * C::SM - C::SN] = *reinterpret_cast<const uint32_t*>(smem + st + sb_at + 128 * (n - 2 * C::SM - C::SN));
+      fa[K & 1][n] = *reinterpret_cast<const u32x4*>(smem + st + a_at[K] + n * 32 * C::kRow);
+    } else if (n < kReads) {
+      fb[K & 1][n - C::SM] = *reinterpret_cast<const u32x4*>(smem + st + b_at[K] + (n - C::SM) * 32 * C::kRow);
+    } else if (K == 0 && n < kReads0) {
+      const int i = (n - kReads) / C::kWords, w = (n - kReads) % C::kWords;
+      if (i < C::SM) wa[w][i] = *reinterpret_cast<const uint32_t*>(smem + st + sa_at + 4 * w * C::BM + 128 * i);
+      else wb[w][i - C::SM] = *reinterpret_cast<const uint32_t*>(smem + st + sb_at + 4 * w * C::BN + 128 * (i - C::SM));
     }
   }
-  static constexpr int kReads = C::SM + C::SN, kReads0 = 2 * kReads;
-
+  // The lane's bytes of the step that was read: of quarter k byte k (two units), or 2 k.
   __device__ __forceinline__ void scales() {
 #pragma unroll
-    for (int i = 0; i < C::SM; i++) ea[i] = wa[i] >> shift;
+    for (int i = 0; i < C::SM; i++) ea[i] = C::kWords == 1 ? wa[0][i] >> pick : __builtin_amdgcn_perm(wa[C::kWords - 1][i], wa[0][i], pick);
 #pragma unroll
-    for (int j = 0; j < C::SN; j++) eb[j] = wb[j] >> shift;
+    for (int j = 0; j < C::SN; j++) eb[j] = C::kWords == 1 ? wb[0][j] >> pick : __builtin_amdgcn_perm(wb[C::kWords - 1][j], wb[0][j], pick);
   }
-
-  // The products of half K, between them the reads of half NEXT from the stage at `st`.
+  // The products of quarter K, between them the reads of quarter NEXT from the stage at `st` and `more` of each one.
   template <int K, int NEXT, class F>
-  __device__ __forceinline__ void half(uint32_t st, F extra) {
-    constexpr int kMma = C::SM * C::SN, kN = NEXT == 0 ? kReads0 : kReads;
+  __device__ __forceinline__ void quarter(uint32_t st, F more) {
+    constexpr int kN = NEXT == 0 ? kReads0 : kReads, kByte = C::kWords == 1 ? 2 * K : K;
     int done = 0;
 #pragma unroll
-    for (int t = 0; t < kMma; t++) {
+    for (int t = 0; t < C::kMma; t++) {
       const int i = t / C::SN, j = t % C::SN;
-      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(fb[K][j]), operand(fa[K][i]), acc[i][j], kFp4, kFp4, 2 * K,
-                                                                  static_cast<int>(eb[j]), 2 * K, static_cast<int>(ea[i]));
+      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(fb[K & 1][j]), operand(fa[K & 1][i]), acc[i][j], kFp4, kFp4,
+                                                                  kByte, static_cast<int>(eb[j]), kByte, static_cast<int>(ea[i]));
 #pragma unroll
-      for (; done < (t + 1) * kN / kMma; done++) read<NEXT>(done, st);
-      extra(t);
+      for (; done < (t + 1) * kN / C::kMma; done++) read<NEXT>(done, st);
+      more(t);
       __builtin_amdgcn_sched_barrier(0);
     }
   }
@@ -263,10 +291,51 @@ struct Compute {
 constexpr int kOutRow = 128 + 16;       // LDS bytes of a row of 64 columns
 constexpr int kOutWave = 32 * kOutRow;  // of a wave
 
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// The sums of one range of K, [split][M][N4] fp32 with rows of N4 = N rounded up to 4: a subtile of 32 x 32 at a time.
+template <class C>
+__device__ __forceinline__ void store_part(uint8_t* lds, Args p, const Place& at, const Compute<C>& c, int lane, int wm, int wn) {
+  const int64_t n4 = (p->N + 3) & ~int64_t(3), m0 = at.m0 + wm * C::WTM, n0 = at.n0 + wn * C::WTN;
+  uint8_t* const put = lds + (lane & 31) * kOutRow + 16 * (lane >> 5);
+  const uint8_t* const get = lds + (lane >> 3) * kOutRow + 16 * (lane & 7);
+  float* row = p->ws + (at.split * p->M + m0 + (lane >> 3)) * n4 + n0 + 4 * (lane & 7);
+  const int rows = static_cast<int>(min(p->M - m0, int64_t(C::WTM))) - (lane >> 3);
+  const int cols = static_cast<int>(min(n4 - n0, int64_t(C::WTN))) - 4 * (lane & 7);
+#pragma unroll
+  for (int i = 0; i < C::SM; i++) {
+#pragma unroll
+    for (int j = 0; j < C::SN; j++) {
+#pragma unroll
+      for (int g = 0; g < 4; g++) {
+        const v16f& v = c.acc[i][j];
+        *reinterpret_cast<v4f*>(put + 32 * g) = v4f{v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]};
+      }
+      wave_fence();
+#pragma unroll
+      for (int k = 0; k < 4; k++) {
+        const v4f w = *reinterpret_cast<const v4f*>(get + 8 * k * kOutRow);
+        if (32 * i + 8 * k < rows && 32 * j < cols) *reinterpret_cast<v4f*>(row + 8 * k * n4 + 32 * j) = w;
+      }
+      wave_fence();
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    row += 32 * n4;
+  }
+}
+
 template <class C>
 __device__ __forceinline__ void store_tile(uint8_t* lds, int32_t tile, const Compute<C>& c, int lane, int wm, int wn) {
   const Args p = arguments();
   const Place at = place_of<C>(p, tile);
+  if constexpr (C::kSplit) {
+    store_part<C>(lds, p, at, c, lane, wm, wn);
+    return;
+  }
   const int64_t m0 = at.m0 + wm * C::WTM, n0 = at.n0 + wn * C::WTN, ldy = p->ldy;
   uint8_t* const put = lds + (lane & 31) * kOutRow + 8 * (lane >> 5);
   const uint8_t* const get = lds + (lane >> 3) * kOutRow + 16 * (lane & 7);
@@ -285,9 +354,7 @@ __device__ __forceinline__ void store_tile(uint8_t* lds, int32_t tile, const Com
           const v16f& v = c.acc[i][j + q];
           *reinterpret_cast<u32x2*>(put + 64 * q + 16 * g) = u32x2{bf16_pair(v[4 * g], v[4 * g + 1]), bf16_pair(v[4 * g + 2], v[4 * g + 3])};
         }
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+      wave_fence();
       u32x4 w[4];
 #pragma unroll
       for (int k = 0; k < 4; k++) w[k] = *reinterpret_cast<const u32x4*>(get + 8 * k * kOutRow);
@@ -305,9 +372,7 @@ __device__ __forceinline__ void store_tile(uint8_t* lds, int32_t tile, const Com
           }
         }
       }
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+      wave_fence();
       __builtin_amdgcn_sched_barrier(0);
     }
     row += 32 * ldy;
@@ -319,12 +384,13 @@ __global__ __launch_bounds__(C::kThreads, C::kBlocks) void gemm_mxfp4_kernel(Mxf
   __shared__ __attribute__((aligned(16))) uint8_t smem[C::kLds + C::kWaves * kOutWave];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave % C::WAVES_M, wn = wave / C::WAVES_M;
-  const int64_t tiles = ((p.M + C::BM - 1) / C::BM) * ((p.N + C::BN - 1) / C::BN);
+  const int64_t tiles = ((p.M + C::BM - 1) / C::BM) * ((p.N + C::BN - 1) / C::BN) * (C::kSplit ? p.splits : 1);
   const TileSpan span = tile_span(tiles, blockIdx.x, gridDim.x, p.xcds);
   if (span.beg >= span.end) return;
-  const int steps = static_cast<int>((p.K + kStepK - 1) / kStepK);
-  const bool odd = (p.K & 128) != 0;
-  Loader<C> load(span, lds_addr(smem), lane, wave, steps, odd);
+  // (a call that splits K has a tile for each block, so that all of a block's tiles have as many steps)
+  const int units = C::kSplit ? place_of<C>(arguments(), static_cast<int32_t>(span.beg)).units : static_cast<int>(p.K / kStepK);
+  const int whole = units / C::kWords;
+  Loader<C> load(span, lds_addr(smem), lane, wave, units);
   Compute<C> c(smem, lane, wm, wn);
 #pragma unroll
   for (int s = 0; s < C::STAGES - 1; s++) {
@@ -352,21 +418,35 @@ __global__ __launch_bounds__(C::kThreads, C::kBlocks) void gemm_mxfp4_kernel(Mxf
       st = st + C::kStage == C::kLds ? 0 : st + C::kStage;
     };
     auto none = [](int) {};
-    auto loads3 = [&](int n) {
+    // a step's first loads go out after the turn that frees their stage, the others in the next step's first quarter
+    auto loads_first = [&](int n) {
 #pragma unroll
       for (int i = n * C::kFirst / C::kMma; i < (n + 1) * C::kFirst / C::kMma; i++) load.issue(i);
     };
-    auto loads0 = [&](int n) {
+    auto loads_rest = [&](int n) {
       constexpr int kRest = C::kLoads - C::kFirst;
 #pragma unroll
       for (int i = n * kRest / C::kMma; i < (n + 1) * kRest / C::kMma; i++) load.issue(C::kFirst + i);
     };
-    for (int s = 0; s < steps; s++) {
+    for (int s = 0; s < whole; s++) {
       c.scales();
-      c.template half<0, 1>(st, loads0);
+      c.template quarter<0, 1>(st, loads_rest);
       load.advance();
+      if constexpr (C::QUARTERS == 4) {
+        c.template quarter<1, 2>(st, none);
+        c.template quarter<2, 3>(st, none);
+      }
       turn();
-      c.template half<1, 0>(st, loads3);
+      c.template quarter<C::QUARTERS - 1, 0>(st, loads_first);
+    }
+    if constexpr (C::QUARTERS == 4) {
+      if (units % C::kWords != 0) {  // a last step of one unit
+        c.scales();
+        c.template quarter<0, 1>(st, loads_rest);
+        load.advance();
+        turn();
+        c.template quarter<1, 0>(st, loads_first);
+      }
     }
     store_tile<C>(smem + C::kLds + wave * kOutWave, t, c, lane, wm, wn);
     load.look_ahead();
@@ -374,28 +454,217 @@ __global__ __launch_bounds__(C::kThreads, C::kBlocks) void gemm_mxfp4_kernel(Mxf
   wait_vmcnt<0>();  // nothing is under way into LDS when the block ends
 }
 
-using Large = Tile<256, 256, 2, 2, 4, 1>;
-using Medium = Tile<128, 128, 2, 2, 3, 2>;
+using Large = Tile<256, 256, 2, 2, 2, 4, 1>;
+using Deep = Tile<128, 128, 2, 2, 4, 4, 1>;
+using Flat = Tile<64, 128, 2, 2, 4, 4, 1>;
+
+// Y = bf16( the splits' sums added in their order ): four columns per thread.
+constexpr int kMostSplits = 16;
+__global__ __launch_bounds__(256) void gemm_mxfp4_join_kernel(Mxfp4GemmParams p) {
+  const int64_t quads = (p.N + 3) / 4, total = p.M * quads, plane = p.M * quads;
+  const bool wide = p.ldy % 4 == 0 && (reinterpret_cast<uintptr_t>(p.y) & 7) == 0;
+  for (int64_t t = blockIdx.x * int64_t(256) + threadIdx.x; t < total; t += gridDim.x * int64_t(256)) {
+    const v4f* src = reinterpret_cast<const v4f*>(p.ws) + t;
+    v4f v[kMostSplits];
+#pragma unroll
+    for (int s = 0; s < kMostSplits; s++)
+      if (s < p.splits) v[s] = src[s * plane];
+    v4f sum = v[0];
+#pragma unroll
+    for (int s = 1; s < kMostSplits; s++)
+      if (s < p.splits) {
+#pragma unroll
+        for (int q = 0; q < 4; q++) sum[q] += v[s][q];
+      }
+    const int64_t m = t / quads, n = (t - m * quads) * 4;
+    uint16_t* y = p.y + m * p.ldy + n;
+    const u32x2 w = {bf16_pair(sum[0], sum[1]), bf16_pair(sum[2], sum[3])};
+    if (wide && n + 4 <= p.N) {
+      *reinterpret_cast<u32x2*>(y) = w;
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; q++)
+        if (n + q < p.N) y[q] = static_cast<uint16_t>(w[q >> 1] >> (16 * (q & 1)));
+    }
+  }
+}
+
+// ------------------------------------------------------------------ few rows
+// Up to 16 SM rows of A: a block has 16 rows of B and all of K, its waves contiguous ranges of it; operands go from
+// memory straight to registers, P steps of 128 elements at a time, and the waves' sums meet in LDS, added in their
+// order. (v_mfma_scale_f32_16x16x128: lane (r, h) holds row r, the 32 elements of K block h, and its scale byte.) A lane
+// loads the scale word of one row for one of four steps (lane group h the h-th), which the others get by exchanges.
+template <int SM>
+struct Few {
+  static constexpr int kWaves = 8, P = SM == 4 ? 4 : 8;
+};
+
+// The words that lane groups 0 .. 3 hold for row r, for every lane of it.
+__device__ __forceinline__ void spread(uint32_t w, uint32_t (&all)[4]) {
+  const auto x = __builtin_amdgcn_permlane16_swap(w, w, false, false);  // groups 0 0 2 2, 1 1 3 3
+  const auto a = __builtin_amdgcn_permlane32_swap(x[0], x[0], false, false);
+  const auto b = __builtin_amdgcn_permlane32_swap(x[1], x[1], false, false);
+  all[0] = a[0];
+  all[2] = a[1];
+  all[1] = b[0];
+  all[3] = b[1];
+}
+
+template <int SM>
+__global__ __launch_bounds__(64 * Few<SM>::kWaves, 1) void gemm_mxfp4_few_kernel(Mxfp4GemmParams p) {
+  constexpr int W = Few<SM>::kWaves, P = Few<SM>::P;
+  __shared__ v4f red[W][SM][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, h = lane >> 4;
+  const int64_t n0 = int64_t(blockIdx.x) * 16;
+  const int all = static_cast<int>(p.K / 128), beg = static_cast<int>(int64_t(all) * wave / W), end = static_cast<int>(int64_t(all) * (wave + 1) / W);
+  const uint8_t* const b = p.b + min(n0 + r, p.N - 1) * p.ldb + 16 * h;
+  const uint8_t* const sb = p.sb + min(n0 + r, p.N - 1) * p.sb_sn * 4;
+  const uint8_t* a[SM];
+  const uint8_t* sa[SM];
+#pragma unroll
+  for (int i = 0; i < SM; i++) {
+    const int64_t m = min(int64_t(16 * i + r), p.M - 1);
+    a[i] = p.a + m * p.lda + 16 * h;
+    sa[i] = p.sa + m * p.sa_sm * 4;
+  }
+  v4f acc[SM];
+#pragma unroll
+  for (int i = 0; i < SM; i++) acc[i] = v4f{0.f, 0.f, 0.f, 0.f};
+  for (int k = beg; k < end; k += P) {
+    u32x4 fb[P], fa[P][SM];
+    uint32_t wb[P / 4], wa[P / 4][SM];
+#pragma unroll
+    for (int u = 0; u < P; u++) {  // past the range's end its last step again, which is not used
+      const int64_t at = int64_t(min(k + u, end - 1)) * kUnit;
+      fb[u] = *reinterpret_cast<const u32x4*>(b + at);
+#pragma unroll
+      for (int i = 0; i < SM; i++) fa[u][i] = *reinterpret_cast<const u32x4*>(a[i] + at);
+    }
+#pragma unroll
+    for (int g = 0; g < P / 4; g++) {
+      const int64_t at = min(k + 4 * g + h, end - 1);
+      wb[g] = *reinterpret_cast<const uint32_t*>(sb + at * p.sb_sk * 4);
+#pragma unroll
+      for (int i = 0; i < SM; i++) wa[g][i] = *reinterpret_cast<const uint32_t*>(sa[i] + at * p.sa_sk * 4);
+    }
+#pragma unroll
+    for (int g = 0; g < P / 4; g++) {
+      uint32_t eb[4], ea[SM][4];
+      spread(wb[g], eb);
+#pragma unroll
+      for (int i = 0; i < SM; i++) spread(wa[g][i], ea[i]);
+#pragma unroll
+      for (int u = 0; u < 4; u++) {
+        if (k + 4 * g + u < end) {
+#pragma unroll
+          for (int i = 0; i < SM; i++)
+            acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(fb[4 * g + u]), operand(fa[4 * g + u][i]), acc[i], kFp4, kFp4, 0,
+                                                                      static_cast<int>(eb[u] >> (8 * h)), 0,
+                                                                      static_cast<int>(ea[i][u] >> (8 * h)));
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < SM; i++) red[wave][i][lane] = acc[i];
+  __syncthreads();
+  if (wave >= SM) return;
+  v4f sum = red[0][wave][lane];
+#pragma unroll
+  for (int w = 1; w < W; w++) {
+    const v4f o = red[w][wave][lane];
+#pragma unroll
+    for (int q = 0; q < 4; q++) sum[q] += o[q];
+  }
+  const int64_t m = 16 * wave + r, n = n0 + 4 * h;
+  if (m >= p.M) return;
+  uint16_t* y = p.y + m * p.ldy + n;
+  const u32x2 w = {bf16_pair(sum[0], sum[1]), bf16_pair(sum[2], sum[3])};
+  if (n + 4 <= p.N && (reinterpret_cast<uintptr_t>(y) & 7) == 0) {
+    *reinterpret_cast<u32x2*>(y) = w;
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; q++)
+      if (n + q < p.N) y[q] = static_cast<uint16_t>(w[q >> 1] >> (16 * (q & 1)));
+  }
+}
+
+// ------------------------------------------------------------------ launch
+enum class Kind { kFew, kLarge, kDeep, kFlat };
+struct Shape {
+  Kind kind;
+  int splits;
+  int64_t ws;  // bytes
+};
+
+int64_t tiles_of(int64_t M, int64_t N, int bm, int bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); }
+
+// Up to 64 rows take the kernel without LDS staging. Above, the tile and the ranges of K with the least estimated time:
+// rounds of tiles over the CUs, each its steps of 256 elements and a fixed part. Splitting adds a launch and the partial
+// sums' way to memory and back.
+Shape shape_of(int64_t M, int64_t N, int64_t K, int cus) {
+  if (M <= 64) return {Kind::kFew, 1, 0};
+  struct Model {
+    Kind kind;
+    int bm, bn;
+    double step, fixed;  // us
+    bool split;
+  };
+  constexpr Model kModels[] = {{Kind::kLarge, 256, 256, 2.2, 6.0, false}, {Kind::kDeep, 128, 128, 0.70, 2.5, true}, {Kind::kFlat, 64, 128, 0.46, 2.0, true}};
+  const double steps = static_cast<double>(K) / 256;
+  const int64_t n4 = (N + 3) / 4 * 4;
+  Shape best{Kind::kLarge, 1, 0};
+  double least = 1e300;
+  for (const Model& m : kModels) {
+    const int64_t tiles = tiles_of(M, N, m.bm, m.bn);
+    const int64_t most = m.split ? std::max<int64_t>(1, std::min<int64_t>({cus / tiles, K / 1024, kMostSplits})) : 1;
+    for (int64_t s = 1; s <= most; s++) {
+      const double rounds = static_cast<double>((tiles * s + cus - 1) / cus), bytes = static_cast<double>(s * M * n4 * 4);
+      const double time = rounds * (steps / s * m.step + m.fixed) + (s > 1 ? 4.0 + 2 * bytes / 3e6 : 0.0);
+      if (time < least) {
+        least = time;
+        best = {m.kind, static_cast<int>(s), s > 1 ? s * M * n4 * 4 : 0};
+      }
+    }
+  }
+  return best;
+}
 
 template <class C>
 void launch(const Mxfp4GemmParams& p, const DeviceShape& ds, hipStream_t stream) {
-  const int64_t tiles = ((p.M + C::BM - 1) / C::BM) * ((p.N + C::BN - 1) / C::BN);
-  int64_t grid = std::min<int64_t>(tiles, int64_t(ds.cus) * C::kBlocks);
+  const int64_t units = tiles_of(p.M, p.N, C::BM, C::BN) * p.splits;
+  int64_t grid = std::min<int64_t>(units, int64_t(ds.cus) * C::kBlocks);
   grid = std::max<int64_t>((grid + ds.xcds - 1) / ds.xcds * ds.xcds, ds.xcds);
   hipLaunchKernelGGL((gemm_mxfp4_kernel<C>), dim3(static_cast<unsigned>(grid)), dim3(C::kThreads), 0, stream, p);
 }
 
 }  // namespace
 
-int64_t mxfp4_gemm_workspace_bytes(int64_t, int64_t, int64_t) { return 0; }
+int64_t mxfp4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) { return shape_of(M, N, K, current_device_shape().cus).ws; }
 
 int launch_mxfp4_gemm(const Mxfp4GemmParams& p_in, hipStream_t stream) {
   const DeviceShape ds = current_device_shape();
   Mxfp4GemmParams p = p_in;
   p.xcds = ds.xcds;
-  const int64_t large = ((p.M + 255) / 256) * ((p.N + 255) / 256);
-  if (large >= ds.cus) launch<Large>(p, ds, stream);
-  else launch<Medium>(p, ds, stream);
+  Shape s = shape_of(p.M, p.N, p.K, ds.cus);
+  if (s.ws > 0 && (p.ws == nullptr || p.ws_bytes < s.ws)) s.splits = 1;
+  p.splits = s.splits;
+  switch (s.kind) {
+    case Kind::kFew: {
+      const dim3 grid(static_cast<unsigned>((p.N + 15) / 16));
+      if (p.M <= 16) hipLaunchKernelGGL((gemm_mxfp4_few_kernel<1>), grid, dim3(64 * Few<1>::kWaves), 0, stream, p);
+      else if (p.M <= 32) hipLaunchKernelGGL((gemm_mxfp4_few_kernel<2>), grid, dim3(64 * Few<2>::kWaves), 0, stream, p);
+      else hipLaunchKernelGGL((gemm_mxfp4_few_kernel<4>), grid, dim3(64 * Few<4>::kWaves), 0, stream, p);
+      break;
+    }
+    case Kind::kLarge: launch<Large>(p, ds, stream); break;
+    case Kind::kDeep: p.splits > 1 ? launch<Splitting<Deep>>(p, ds, stream) : launch<Deep>(p, ds, stream); break;
+    case Kind::kFlat: p.splits > 1 ? launch<Splitting<Flat>>(p, ds, stream) : launch<Flat>(p, ds, stream); break;
+  }
+  if (p.splits > 1) {
+    const int64_t quads = p.M * ((p.N + 3) / 4);
+    hipLaunchKernelGGL(gemm_mxfp4_join_kernel, dim3(static_cast<unsigned>(std::min<int64_t>((quads + 255) / 256, 4096))), dim3(256), 0, stream, p);
+  }
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess) return fail(FP8Q_ELAUNCH, std::string("mxfp4 product launch: ") + hipGetErrorString(err));
   return FP8Q_OK;

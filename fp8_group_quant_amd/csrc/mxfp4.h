@@ -37,6 +37,7 @@ struct Mxfp4GemmParams {
   float* ws;
   int64_t ws_bytes;
   int xcds;
+  int splits;        // ranges of K
 };
 
 int64_t mxfp4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
