@@ -74,6 +74,7 @@ _SIGNATURES = {
                                   _P, _I64, _I64, _P, _P, _P, _I64, _I64, _P, _I64, _I64, _I64, _I64, _I64, _I64, _F32,
                                   _I64, _I64, _P, _I64, _P],
     "fp8q_kv4_window_attention_workspace_size": [_INT, _I64, _I64, _I64, _I64, _I64, _I64, _I64, _I64],
+    "fp8q_kv4_tree_attention_workspace_size": [_INT, _I64, _I64, _I64, _I64, _I64, _I64],
     "fp8q_kv4_tree_attention": [_P, _INT, _I64, _I64, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _I64, _I64, _I64,
                                 _P, _I64, _I64, _P, _P, _P, _I64, _I64, _P, _I64, _I64, _I64, _I64, _I64, _I64, _F32,
                                 _P, _I64, _I64, _P, _I64, _P],
@@ -725,8 +726,7 @@ def _kv4_attend(entry: str, sizes: tuple, extra: tuple, q, cache, block_table, k
     handle = _stream_on(stream, q.get_device())
     lib = load_library()
     if workspace is None:
-        size = lib.fp8q_kv4_window_attention_workspace_size if sizes else lib.fp8q_kv4_attention_workspace_size
-        workspace = _alloc_workspace(size(dt, B, T, H, kv_heads, D, max_pages * page, *sizes), q.device, stream)
+        workspace = _alloc_workspace(getattr(lib, entry + "_workspace_size")(dt, B, T, H, kv_heads, D, max_pages * page, *sizes), q.device, stream)
     _check(getattr(lib, entry)(
         q.data_ptr(), dt, q_st, q_sh, *args, block_table.data_ptr(), table_sb, max_pages, kv_lens.data_ptr(), ip_ptr,
         out.data_ptr(), o_st, o_sh, lse_ptr, l_st, B, T, H, kv_heads, D, sm_scale, *extra,
@@ -784,6 +784,14 @@ def kv4_window_attention(q: torch.Tensor, cache: Kv4Cache, block_table: torch.Te
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     fp8q_kv4_window_attention(q, cache, block_table, kv_lens, out, sm_scale, window, sinks, q_indptr, None, stream)
     return out
+
+
+def fp8q_kv4_tree_attention_workspace_size(dtype: torch.dtype, seqs: int, tokens: int, heads: int, kv_heads: int,
+                                           head_dim: int, max_kv_tokens: int) -> int:
+    """Bytes of workspace with which fp8q_kv4_tree_attention splits long caches over more of the current device (0: it
+    needs none)."""
+    return int(load_library().fp8q_kv4_tree_attention_workspace_size(_DTYPES[dtype], seqs, tokens, heads, kv_heads,
+                                                                     head_dim, max_kv_tokens))
 
 
 def fp8q_kv4_tree_attention(q: torch.Tensor, cache: Kv4Cache, block_table: torch.Tensor, kv_lens: torch.Tensor,

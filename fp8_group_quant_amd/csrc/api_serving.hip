@@ -5,7 +5,6 @@
 #include <cmath>
 #include <limits>
 
-#include "kv4_attention_shape.h"
 #include "serving.h"
 
 namespace fp8q {
@@ -206,12 +205,11 @@ int check_attention_sizes(const std::string& pre, int64_t B, int64_t T, int64_t 
 }
 
 // What tells the three attention calls apart.
-enum AttnKind { kAttnAll, kAttnWindow, kAttnTree };
 struct AttnMask {
-  AttnKind kind;
-  int causal;                // kAttnAll
-  int64_t window, sinks;     // kAttnWindow
-  const int32_t* tree;       // kAttnTree
+  Mask kind;
+  int causal;                // kAll
+  int64_t window, sinks;     // kWindow
+  const int32_t* tree;       // kTree
   int64_t tree_st, tree_words;
 };
 
@@ -241,15 +239,15 @@ int attention_entry(const std::string& pre, const AttnMask& mask, const void* q,
   if (q_st < 0 || q_sh < 0 || o_st < 0 || o_sh < 0 || l_st < 0 || table_sb < 0)
     return fail(FP8Q_EINVAL, pre + "negative stride");
   if (!std::isfinite(sm_scale)) return fail(FP8Q_EINVAL, pre + "sm_scale must be finite");
-  if (mask.kind == kAttnWindow && (rc = check_window(pre, mask.window, mask.sinks)) != FP8Q_OK) return rc;
-  if (mask.kind == kAttnTree && (mask.tree_words < 0 || mask.tree_st < 0))
+  if (mask.kind == kWindow && (rc = check_window(pre, mask.window, mask.sinks)) != FP8Q_OK) return rc;
+  if (mask.kind == kTree && (mask.tree_words < 0 || mask.tree_st < 0))
     return fail(FP8Q_EINVAL, pre + "negative size or stride of the tree mask");
   if (workspace_bytes < 0) return fail(FP8Q_EINVAL, pre + "workspace_bytes must be >= 0");
   if (B == 0 || T == 0 || Hq == 0) return FP8Q_OK;
   if (!q || !out || !kv_lens || (!table && max_pages > 0)) return fail(FP8Q_EINVAL, pre + "null tensor pointer");
   if (!q_indptr && T != B) return fail(FP8Q_EINVAL, pre + "without q_indptr every sequence has one query (T == B)");
-  if (mask.kind == kAttnTree && mask.tree_words > 0 && !mask.tree) return fail(FP8Q_EINVAL, pre + "null tree mask");
-  if (mask.kind == kAttnTree && mask.tree_words > (int64_t(1) << 26))
+  if (mask.kind == kTree && mask.tree_words > 0 && !mask.tree) return fail(FP8Q_EINVAL, pre + "null tree mask");
+  if (mask.kind == kTree && mask.tree_words > (int64_t(1) << 26))
     return fail(FP8Q_EUNSUPPORTED, pre + "at most 2^26 words of the tree mask for a query");
   if (!disjoint(D, {T, o_st}, {Hq, o_sh})) return fail(FP8Q_EINVAL, pre + "output rows overlap");
   if (lse && T > 1 && l_st < Hq) return fail(FP8Q_EINVAL, pre + "lse rows overlap (l_st < Hq)");
@@ -289,13 +287,13 @@ int attention_entry(const std::string& pre, const AttnMask& mask, const void* q,
                           std::numeric_limits<float>::max());
   p.q_sign = sm_scale < 0.0f ? 0x80008000u : 0u;
   const hipStream_t st = static_cast<hipStream_t>(stream);
-  if (mask.kind == kAttnWindow) {
+  if (mask.kind == kWindow) {
     p.window = static_cast<int32_t>(at_most_tokens(mask.window));
     p.sinks = static_cast<int32_t>(at_most_tokens(mask.sinks));
     p.sink_end = static_cast<int32_t>(sink_stretch(p.sinks));
     return launch_kv4_window_attention(dtype, D, p, workspace, workspace_bytes, st);
   }
-  if (mask.kind == kAttnTree) {
+  if (mask.kind == kTree) {
     p.tree = mask.tree;
     p.tree_st = mask.tree_st;
     p.tree_words = static_cast<int32_t>(mask.tree_words);
@@ -310,12 +308,12 @@ int64_t attention_workspace(const char* pre, int dtype, int64_t B, int64_t T, in
   set_error("");
   if (check_attention_sizes(pre, B, T, Hq, Hkv, D, max_tokens) != FP8Q_OK ||
       (dtype != FP8Q_DTYPE_BF16 && dtype != FP8Q_DTYPE_F16) || B == 0 || T == 0 || Hq == 0 ||
-      (mask.kind == kAttnWindow && check_window(pre, mask.window, mask.sinks) != FP8Q_OK) ||
+      (mask.kind == kWindow && check_window(pre, mask.window, mask.sinks) != FP8Q_OK) ||
       check_current_device() != FP8Q_OK)
     return 0;
-  if (mask.kind == kAttnWindow)
+  if (mask.kind == kWindow)
     max_tokens = window_tokens(max_tokens, at_most_tokens(mask.window), at_most_tokens(mask.sinks));
-  return kv4_attention_workspace(dtype, B, T, Hq, Hkv, D, max_tokens);
+  return kv4_attention_workspace(dtype, B, T, Hq, Hkv, D, max_tokens, mask.kind);
 }
 
 // ------------------------------------------------------------------ page plan
@@ -412,7 +410,7 @@ int fp8q_kv4_read(void* k, int64_t k_st, int64_t k_sh, void* v, int64_t v_st, in
 int64_t fp8q_kv4_attention_workspace_size(int dtype, int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
                                           int64_t max_tokens) {
   return fp8q::attention_workspace("fp8q_kv4_attention_workspace_size: ", dtype, B, T, Hq, Hkv, D, max_tokens,
-                                   {fp8q::kAttnAll, 1, 0, 0, nullptr, 0, 0});
+                                   {fp8q::kAll, 1, 0, 0, nullptr, 0, 0});
 }
 
 int fp8q_kv4_attention(
@@ -422,7 +420,7 @@ int fp8q_kv4_attention(
     const int32_t* kv_lens, const int32_t* q_indptr, void* out, int64_t o_st, int64_t o_sh, float* lse, int64_t l_st,
     int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, float sm_scale, int causal, void* workspace,
     int64_t workspace_bytes, void* stream) {
-  return fp8q::attention_entry("fp8q_kv4_attention: ", {fp8q::kAttnAll, causal, 0, 0, nullptr, 0, 0}, q, dtype, q_st, q_sh, kc, ks, vc, vs,
+  return fp8q::attention_entry("fp8q_kv4_attention: ", {fp8q::kAll, causal, 0, 0, nullptr, 0, 0}, q, dtype, q_st, q_sh, kc, ks, vc, vs,
                                pages, page_size, c_sp, c_st, c_sh, s_sp, s_st, s_sh, table, table_sb, max_pages, kv_lens,
                                q_indptr, out, o_st, o_sh, lse, l_st, B, T, Hq, Hkv, D, sm_scale, workspace,
                                workspace_bytes, stream);
@@ -431,7 +429,7 @@ int fp8q_kv4_attention(
 int64_t fp8q_kv4_window_attention_workspace_size(int dtype, int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
                                                  int64_t max_tokens, int64_t window, int64_t sinks) {
   return fp8q::attention_workspace("fp8q_kv4_window_attention_workspace_size: ", dtype, B, T, Hq, Hkv, D, max_tokens,
-                                   {fp8q::kAttnWindow, 1, window, sinks, nullptr, 0, 0});
+                                   {fp8q::kWindow, 1, window, sinks, nullptr, 0, 0});
 }
 
 int fp8q_kv4_window_attention(
@@ -441,10 +439,16 @@ int fp8q_kv4_window_attention(
     const int32_t* kv_lens, const int32_t* q_indptr, void* out, int64_t o_st, int64_t o_sh, float* lse, int64_t l_st,
     int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, float sm_scale, int64_t window, int64_t sinks,
     void* workspace, int64_t workspace_bytes, void* stream) {
-  return fp8q::attention_entry("fp8q_kv4_window_attention: ", {fp8q::kAttnWindow, 1, window, sinks, nullptr, 0, 0}, q, dtype, q_st, q_sh, kc, ks, vc, vs,
+  return fp8q::attention_entry("fp8q_kv4_window_attention: ", {fp8q::kWindow, 1, window, sinks, nullptr, 0, 0}, q, dtype, q_st, q_sh, kc, ks, vc, vs,
                                pages, page_size, c_sp, c_st, c_sh, s_sp, s_st, s_sh, table, table_sb, max_pages, kv_lens,
                                q_indptr, out, o_st, o_sh, lse, l_st, B, T, Hq, Hkv, D, sm_scale, workspace,
                                workspace_bytes, stream);
+}
+
+int64_t fp8q_kv4_tree_attention_workspace_size(int dtype, int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                                               int64_t max_tokens) {
+  return fp8q::attention_workspace("fp8q_kv4_tree_attention_workspace_size: ", dtype, B, T, Hq, Hkv, D, max_tokens,
+                                   {fp8q::kTree, 0, 0, 0, nullptr, 0, 0});
 }
 
 int fp8q_kv4_tree_attention(
@@ -454,7 +458,7 @@ int fp8q_kv4_tree_attention(
     const int32_t* kv_lens, const int32_t* q_indptr, void* out, int64_t o_st, int64_t o_sh, float* lse, int64_t l_st,
     int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, float sm_scale, const int32_t* tree_mask,
     int64_t tree_st, int64_t tree_words, void* workspace, int64_t workspace_bytes, void* stream) {
-  return fp8q::attention_entry("fp8q_kv4_tree_attention: ", {fp8q::kAttnTree, 0, 0, 0, tree_mask, tree_st, tree_words}, q, dtype, q_st, q_sh, kc, ks, vc, vs,
+  return fp8q::attention_entry("fp8q_kv4_tree_attention: ", {fp8q::kTree, 0, 0, 0, tree_mask, tree_st, tree_words}, q, dtype, q_st, q_sh, kc, ks, vc, vs,
                                pages, page_size, c_sp, c_st, c_sh, s_sp, s_st, s_sh, table, table_sb, max_pages, kv_lens,
                                q_indptr, out, o_st, o_sh, lse, l_st, B, T, Hq, Hkv, D, sm_scale, workspace,
                                workspace_bytes, stream);

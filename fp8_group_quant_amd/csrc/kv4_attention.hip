@@ -3,8 +3,9 @@
 
 namespace fp8q {
 
-int64_t kv4_attention_workspace(int dtype, int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_tokens) {
-  return attention_shape(current_device_shape().cus, dtype, B, T, Hq, Hkv, D, max_tokens).bytes;
+int64_t kv4_attention_workspace(int dtype, int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_tokens,
+                                Mask mask) {
+  return attention_shape(current_device_shape().cus, dtype, B, T, Hq, Hkv, D, max_tokens, mask).bytes;
 }
 
 int launch_kv4_attention(int dtype, int64_t D, const Kv4AttnParams& p, void* ws, int64_t ws_bytes, hipStream_t stream) {

@@ -107,10 +107,6 @@ __device__ __forceinline__ Seq sequence(const Kv4AttnParams& p, int32_t b) {
   return s;
 }
 
-// Which tokens up to its limit a row sees (Rows): all; the last `window` and the first `sinks`; of the drafted
-// ones those that its mask names.
-enum Mask { kAll = 0, kWindow = 1, kTree = 2 };
-
 // A window call's unit sees two stretches of the cache: the first tokens and those from its first row's window
 // on. Its places, counted by the loops and the spans, run through the first kSinkStep * n tokens that hold the
 // sinks and go on with the window's, `skip` tokens later; both stretches begin at a multiple of the longest step.
@@ -321,9 +317,12 @@ struct Rows {
   }
 };
 
-// Bits 0 .. 63: whether a query sees the tokens of `from` drafted tokens on (negative: before the draft), by its
-// words of the mask.
-__device__ __forceinline__ uint64_t drafted(const Kv4AttnParams& p, const int32_t* words, int64_t from) {
+// Bits 0 .. 63: whether row i of a sequence sees the tokens of `from` drafted tokens on (negative: before the draft), by
+// its query's words of the mask. They are looked up where they are needed, in a unit's last steps: held from its
+// beginning on, their addresses cost the registers that the loop has none of.
+template <int MASK>
+__device__ __forceinline__ uint64_t drafted(const Kv4AttnParams& p, const Seq& s, const Rows<MASK>& rows, int32_t i, int64_t from) {
+  const int32_t* words = p.tree + (s.q0 + rows.query(p, i)) * p.tree_st;
   const int64_t at = from >> 5;
   const uint32_t bit = from & 31;
   uint32_t w[3];
@@ -491,6 +490,26 @@ __device__ __forceinline__ Pages<PAGE, N> load_pages(const Kv4AttnParams& p, con
     g.n[i] = PAGE == kByToken ? table[at] : read_int(table, at);
   }
   return g;
+}
+
+// Bits of a step's tokens that lie before `limit` and from `lower` on or before `sinks`, all counted from the step's first.
+__device__ __forceinline__ uint64_t below(int32_t n) { return n <= 0 ? 0 : n >= 64 ? ~0ull : (1ull << n) - 1; }
+__device__ __forceinline__ uint64_t windowed(int32_t limit, int32_t lower, int32_t sinks) {
+  return below(limit) & (~below(lower) | below(sinks));
+}
+
+// Scores of a step's tokens 16 c + 4 h + i whose bit of `see` is not set become -infinity, 16 tokens after the other:
+// all comparisons at once take scalar registers that there are not.
+template <int N>
+__device__ __forceinline__ void hide(f32x4 (&s)[N], uint64_t see, int h) {
+  see >>= 4 * h;
+#pragma unroll
+  for (int c = 0; c < N; c++) {
+    const uint32_t bits = static_cast<uint32_t>(see >> (16 * c));
+#pragma unroll
+    for (int i = 0; i < 4; i++) s[c][i] = bits & (1u << i) ? s[c][i] : kNegInf;
+    __builtin_amdgcn_sched_barrier(0);
+  }
 }
 
 // Makes the wave wait for pages that it has asked for.
@@ -668,7 +687,6 @@ __global__ __launch_bounds__(64 * WAVES, waves_per_simd(D, DT, N)) void kv4_atte
     // every row sees the tokens before `low` (of a window: from `high` on)
     const int32_t limit = tr.seen(p, seq, idx), low = MASK == kTree ? tr.before - 1 : tr.seen(p, seq, first);
     const int32_t lower = MASK == kWindow ? tr.lower(p, idx) : 0, high = MASK == kWindow ? tr.lower(p, last) : 0;
-    const int32_t* words = MASK == kTree ? p.tree + (seq.q0 + qi) * p.tree_st : nullptr;
     const int32_t end = MASK == kWindow ? tr.seen(p, seq, last) : min(w.t1, tr.seen(p, seq, last));  // of the tokens
     const int32_t t_end = MASK == kWindow ? min(w.t1, end - tr.skip) : end;                          // of the places
 
@@ -705,8 +723,6 @@ __global__ __launch_bounds__(64 * WAVES, waves_per_simd(D, DT, N)) void kv4_atte
 
     for (; t < t_end; t += kStep) {
       const int32_t tok = tr.token(p, t);  // the step's first token
-      uint64_t named = ~0ull;
-      if (MASK == kTree && tok + kTile > low) named = drafted(p, words, int64_t(tok) - low);
       f32x4 s[N];
       Mult<D> mk[N], mv[N];
       spread_scales<D, N>(st.ks, h, mk);
@@ -742,15 +758,21 @@ __global__ __launch_bounds__(64 * WAVES, waves_per_simd(D, DT, N)) void kv4_atte
       pages = load_pages<PAGE, N>(p, table, tr.token(p, t + 2 * kStep), end);
 
       if (part) {
+        if constexpr (MASK == kTree) {
+          uint64_t see = there;
+          if (tok + kTile > low) see &= drafted<MASK>(p, seq, tr, min(first + r, last), int64_t(tok) - low);
+          hide<N>(s, see, h);
+        } else if constexpr (MASK == kWindow) {
+          hide<N>(s, there & windowed(limit - tok, lower - tok, p.sinks - tok), h);
+        } else {
 #pragma unroll
-        for (int c = 0; c < N; c++)
+          for (int c = 0; c < N; c++)
 #pragma unroll
-          for (int i = 0; i < 4; i++) {
-            const int n = 16 * c + 4 * h + i;
-            if (((there >> n) & 1u) == 0u || tok + n >= limit) s[c][i] = kNegInf;
-            if (MASK == kWindow && tok + n < lower && tok + n >= p.sinks) s[c][i] = kNegInf;
-            if (MASK == kTree && ((named >> n) & 1u) == 0u) s[c][i] = kNegInf;
-          }
+            for (int i = 0; i < 4; i++) {
+              const int n = 16 * c + 4 * h + i;
+              if (((there >> n) & 1u) == 0u || tok + n >= limit) s[c][i] = kNegInf;
+            }
+        }
       }
       float mx = kNegInf;
 #pragma unroll
@@ -948,7 +970,6 @@ __global__ __launch_bounds__(64 * kWideWaves, wide_waves_per_simd(D, DT, QT, SPL
 
     bf16x8 q[QT][PARTS][kSteps];
     int32_t limit[QT], lower[QT];
-    const int32_t* words[QT];
 #pragma unroll
     for (int n = 0; n < QT; n++) {
       const int32_t row = wfirst + 16 * n + r;
@@ -956,7 +977,6 @@ __global__ __launch_bounds__(64 * kWideWaves, wide_waves_per_simd(D, DT, QT, SPL
       const int32_t idx = there ? row : tr.last, qi = idx / p.group, qh = head * p.group + idx - qi * p.group;
       limit[n] = tr.seen(p, seq, idx);
       lower[n] = MASK == kWindow ? tr.lower(p, idx) : 0;
-      words[n] = MASK == kTree ? p.tree + (seq.q0 + qi) * p.tree_st : nullptr;
       const uint16_t* src = static_cast<const uint16_t*>(p.q) + (seq.q0 + qi) * p.q_st + qh * p.q_sh + D / 4 * h;
 #pragma unroll
       for (int j = 0; j < kSteps; j++) {
@@ -991,12 +1011,6 @@ __global__ __launch_bounds__(64 * kWideWaves, wide_waves_per_simd(D, DT, QT, SPL
       f32x4 s[QT][kHalves];
       const uint64_t there = k_there;
       const int32_t tok = tr.token(p, t);  // the step's first token
-      uint64_t named[QT];
-#pragma unroll
-      for (int n = 0; n < QT; n++) {
-        named[n] = ~0ull;
-        if (MASK == kTree && tok + kStepW > low) named[n] = drafted(p, words[n], int64_t(tok) - low);
-      }
       // the pages after next, waited for (below) before any LDS read is under way: scalar loads
       // return in no order, so that with one outstanding every LDS read would wait for all
       Pages<PAGE, kHalves> next_k;
@@ -1038,15 +1052,21 @@ __global__ __launch_bounds__(64 * kWideWaves, wide_waves_per_simd(D, DT, QT, SPL
 #pragma unroll
         for (int n = 0; n < QT; n++) {
           if (part) {
+            if constexpr (MASK == kTree) {
+              uint64_t see = there;
+              if (tok + kStepW > low) see &= drafted<MASK>(p, seq, tr, min(wfirst + 16 * n + r, tr.last), int64_t(tok) - low);
+              hide<kHalves>(s[n], see, h);
+            } else if constexpr (MASK == kWindow) {
+              hide<kHalves>(s[n], there & windowed(limit[n] - tok, lower[n] - tok, p.sinks - tok), h);
+            } else {
 #pragma unroll
-            for (int c = 0; c < kHalves; c++)
+              for (int c = 0; c < kHalves; c++)
 #pragma unroll
-              for (int i = 0; i < 4; i++) {
-                const int at = 16 * c + 4 * h + i;
-                if (((there >> at) & 1u) == 0u || tok + at >= limit[n]) s[n][c][i] = kNegInf;
-                if (MASK == kWindow && tok + at < lower[n] && tok + at >= p.sinks) s[n][c][i] = kNegInf;
-                if (MASK == kTree && ((named[n] >> at) & 1u) == 0u) s[n][c][i] = kNegInf;
-              }
+                for (int i = 0; i < 4; i++) {
+                  const int at = 16 * c + 4 * h + i;
+                  if (((there >> at) & 1u) == 0u || tok + at >= limit[n]) s[n][c][i] = kNegInf;
+                }
+            }
           }
           float mx = kNegInf;
 #pragma unroll
@@ -1261,7 +1281,7 @@ struct Launch {
 // Chooses the shape of a call and launches it; `max_tokens`: the most of a sequence's tokens that a unit reads.
 template <int MASK>
 int launch_masked(int dtype, int64_t D, Kv4AttnParams p, int64_t max_tokens, void* ws, int64_t ws_bytes, hipStream_t stream) {
-  const AttnShape s = attention_shape(current_device_shape().cus, dtype, p.B, p.T, p.Hq, p.Hkv, D, max_tokens);
+  const AttnShape s = attention_shape(current_device_shape().cus, dtype, p.B, p.T, p.Hq, p.Hkv, D, max_tokens, static_cast<Mask>(MASK));
   const bool split = s.bytes > 0 && ws && ws_bytes >= s.bytes;
   p.max_units = s.units;
   p.span_shift = s.span_shift;

@@ -12,6 +12,10 @@
 
 namespace fp8q {
 
+// Which tokens up to its limit a row sees: all; the last `window` and the first `sinks`; of the drafted ones those that its
+// mask names.
+enum Mask { kAll = 0, kWindow = 1, kTree = 2 };
+
 constexpr int kRows = 16;   // query rows of a tile of the kernel for few rows
 constexpr int kMinRun = 2;  // spans of a block's run at least
 constexpr int kStepW = 64;  // tokens of a step of the kernel for many rows
@@ -95,6 +99,14 @@ inline int64_t window_tokens(int64_t max_tokens, int64_t window, int64_t sinks) 
   return std::min(max_tokens, sink_stretch(sinks) + window + 128 - 1 + 64 - 1);
 }
 
+// Tiles of a window or tree call: 16 rows while there are few of them, which then use more of the device than tiles of 64
+// (us for 16 and 64 rows, 32 heads on 8 cached ones of 128: a tree of 25 over 1000 tokens 13.2 and 17.2, of 60 over 4000 22 and
+// 28, 4 trees of 25 over 2000 20 and 28, 256 queries with a window of 512 15 and 19; 8 trees of 60 over 1000, which have 960
+// tiles of 16 rows, 33 and 28).
+inline bool few_narrow_tiles(int cus, int64_t B, int64_t rows_each, int64_t Hkv) {
+  return Hkv * B * ((rows_each + kRows - 1) / kRows) <= 2 * static_cast<int64_t>(cus);
+}
+
 struct AttnShape {
   int rows;        // of a tile
   bool tall;
@@ -109,16 +121,19 @@ struct AttnShape {
 // units are fewer than 8 * blocks, the bound at most twice as many), so the line of spans always finds a
 // span short enough.
 inline AttnShape attention_shape(int cus, int dtype, int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
-                                 int64_t max_tokens) {
+                                 int64_t max_tokens, Mask mask = kAll) {
   AttnShape s;
   // rows and units of sequences of mean length
   const int64_t group = Hq / Hkv, rows_each = (T * group + B - 1) / B;
-  s.rows = tile_rows(cus, dtype, B, rows_each, Hkv, D, max_tokens);
+  s.rows = mask != kAll && few_narrow_tiles(cus, B, rows_each, Hkv) ? kRows : tile_rows(cus, dtype, B, rows_each, Hkv, D, max_tokens);
   const int64_t units = Hkv * B * ((rows_each + s.rows - 1) / s.rows);
   s.units = Hkv * std::min((T * group + s.rows - 1) / s.rows + std::min(B, T), T * group);
   const bool narrow = s.rows == kRows;
   s.blocks = static_cast<int64_t>(cus) * (narrow ? narrow_blocks(dtype, D) : 2);
-  const Cut cut = narrow ? narrow_cut(cus, dtype, D, units, max_tokens, s.blocks) : wide_cut(units, max_tokens, s.blocks);
+  // Windows are about equally long, so that nothing is gained by cutting them once every CU has two units (64 single tokens
+  // with windows of 4096, 8 cached heads of 128: 65 us whole, 70 split).
+  const Cut cut = narrow && mask == kWindow && units >= 2 * static_cast<int64_t>(cus) ? Cut::kWhole
+                  : narrow ? narrow_cut(cus, dtype, D, units, max_tokens, s.blocks) : wide_cut(units, max_tokens, s.blocks);
   s.tall = cut == Cut::kTall;
   // spans of 128 tokens, or longer ones where a split call's line could have 2^31 places
   s.span_shift = 7;

@@ -3,6 +3,7 @@
 #pragma once
 
 #include "fp8q_internal.h"
+#include "kv4_attention_shape.h"
 
 namespace fp8q {
 
@@ -87,7 +88,8 @@ struct Kv4AttnParams {
 
 // Bytes of workspace with which attention of this shape splits the cache axis on the current
 // device (0: it never does).
-int64_t kv4_attention_workspace(int dtype, int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_tokens);
+int64_t kv4_attention_workspace(int dtype, int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_tokens,
+                                Mask mask);
 int launch_kv4_attention(int dtype, int64_t D, const Kv4AttnParams& p, void* ws, int64_t ws_bytes, hipStream_t stream);
 int launch_kv4_window_attention(int dtype, int64_t D, const Kv4AttnParams& p, void* ws, int64_t ws_bytes, hipStream_t stream);
 int launch_kv4_tree_attention(int dtype, int64_t D, const Kv4AttnParams& p, void* ws, int64_t ws_bytes, hipStream_t stream);

@@ -540,9 +540,12 @@ int fp8q_kv4_window_attention(const void* q, int dtype, int64_t q_st, int64_t q_
  * int32 [T][tree_words]; drafted tokens from 32 * tree_words on are not seen, and bits past the draft, or of
  * drafted tokens that kv_lens[b] < n leaves out of the cache (the first n - kv_lens[b]), do nothing. tree_words
  * <= 2^26 [EUNSUPPORTED], tree_words, tree_st >= 0, tree_mask not NULL unless tree_words == 0 [EINVAL],
- * 4-byte aligned [EALIGN]. Everything else is as there, the workspace's size too
- * (fp8q_kv4_attention_workspace_size).
+ * 4-byte aligned [EALIGN]. Everything else is as there, the workspace's size by
+ * fp8q_kv4_tree_attention_workspace_size.
  */
+int64_t fp8q_kv4_tree_attention_workspace_size(int dtype, int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                                               int64_t max_tokens);
+
 int fp8q_kv4_tree_attention(const void* q, int dtype, int64_t q_st, int64_t q_sh,
                             const uint8_t* kc, const uint8_t* ks, const uint8_t* vc, const uint8_t* vs,
                             int64_t pages, int64_t page_size,

@@ -182,6 +182,18 @@ def test_window_split_many_rows(D, page, dtype):
     check("window", [150, 140, 90, 160], [900, 140, 600, 230], 32, 8, D, page, dtype, window=256, sinks=1, q_scale=0.05)
 
 
+def assert_both_near(a, b, q, c, table, lens, q_lens):
+    """Two results of causal attention. Their bits need not agree: calls with masks have tile sizes of their own, whose
+    sums run in another order. Each is off by at most the bound, |a - x| <= e and |b - x| <= e, so |a - b| <= 2 e."""
+    k64, v64 = (ref.dequantize(x.cpu(), y.cpu()) for x, y in ((c.k, c.k_scales), (c.v, c.v_scales)))
+    o, l, mass, slack = masked.attention(q.cpu(), k64, v64, table, lens, q_lens, c.k.shape[1], c.k.shape[0], 0.1,
+                                         lambda b, n, length, at: masked.window_sees(n, length, length, 0))
+    bound = ref.attention_bounds(o, l, mass, slack, q.shape[2], max(lens), q.dtype)[0]
+    for x in (a, b):
+        assert bool(((x.cpu().double() - o).abs() <= bound).all())
+    assert bool(((a.cpu().double() - b.cpu().double()).abs() <= 2 * bound).all())
+
+
 def test_window_that_reaches_everything_is_causal_attention():
     f = fq()
     lens, q_lens = [500, 70, 9, 3000], [3, 70, 1, 20]
@@ -196,7 +208,7 @@ def test_window_that_reaches_everything_is_causal_attention():
                  lambda o: f.fp8q_kv4_window_attention(q, c, table.cuda(), kv, o, 0.1, 3000, 0, ip, workspace=none)):
         outs.append(torch.empty_like(q))
         call(outs[-1])
-    assert torch.equal(outs[0], outs[1])
+    assert_both_near(*outs, q, c, table, lens, q_lens)
 
 
 # ------------------------------------------------------------------ draft trees
@@ -261,7 +273,7 @@ def test_chain_is_causal_attention():
     a, b = torch.empty_like(q), torch.empty_like(q)
     f.fp8q_kv4_attention(q, c, table.cuda(), kv, a, 0.1, True, ip, workspace=none)
     f.fp8q_kv4_tree_attention(q, c, table.cuda(), kv, b, 0.1, mask, ip, workspace=none)
-    assert torch.equal(a, b)
+    assert_both_near(a, b, q, c, table, lens, q_lens)
 
 
 @pytest.mark.parametrize("kind", ["window", "tree"])

@@ -75,6 +75,8 @@ def test_workspace_sizes_without_a_device_or_with_refused_sizes():
     size = fq.load_library().fp8q_kv4_window_attention_workspace_size
     assert size(0, 1, 1, 32, 8, 128, 100000, 50000, 4) == 0 and size(0, 1, 1, 32, 8, 128, 100000, 0, 4) == 0
     assert size(0, 1, 1, 32, 8, 96, 100000, 50000, -4) == 0
+    size = fq.load_library().fp8q_kv4_tree_attention_workspace_size
+    assert size(0, 1, 1, 32, 8, 128, 100000) == 0 and size(2, 1, 1, 32, 8, 128, 100000) == 0
 
 
 SHARED = CACHE_CASES + [
