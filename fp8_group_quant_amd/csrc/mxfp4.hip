@@ -6,9 +6,13 @@
 // The division is exact and no element saturates, so the rounding to e2m1 is the only one (silu * up is fp32).
 //
 // Both directions are bound by HBM traffic: 2 bytes per element on the model's side (bf16), 0.53 on the
-// codes'. A lane owns 8 consecutive elements of kRows rows: 16 bytes per access next to the neighbour's, and
-// four scale bytes of a column-major layout lie next to each other. Small calls take one row per lane, so
-// that their loads are spread over more CUs.
+// codes'. A lane owns 8 consecutive elements: 16 bytes per access next to the neighbour's, and a block's four
+// lanes are a quad. The quantizer's lanes take one row each (2, 4 and 8 rows to a lane: 0 to 2, 1 to 12 and 2 to 20 %
+// slower); the way back, whose loads are small, takes four where that still fills the device (1 row to a lane: 2 to 5 %
+// slower on large tensors).
+//
+// us, bf16 in one launch, and bytes moved per second: 4096 x 7168 quantized 17.5 (4.2 TB/s) and back 13.9 (5.3); fp16
+// gate | up 6007 x 2 x 2080 15 (3.8) and back 6.4 (4.9, mostly within the caches).
 #include <algorithm>
 
 #include "e2m1_device.h"
@@ -21,16 +25,23 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// Inputs above the L2s' 32 MB are loaded past them, so that they do not push out the codes: 4096 x 7168 in bf16 1.0
+// us less, 6007 x 2 x 2080 in fp16 1.8; 2048 x 4096, which the L2s may hold, would take 0.9 more.
+constexpr int64_t kStreamed = int64_t(32) << 20;
+
 struct Grid {
   uint32_t units, per;  // lanes with work; those of one group of rows
   Divider by_per;
 };
 
-template <int DT>
+template <int DT, bool STREAMED>
 __device__ __forceinline__ Raw8<DT> load8(const uint8_t* p) {
   Raw8<DT> r;
 #pragma unroll
-  for (int j = 0; j < (DT == FP8Q_DTYPE_F32 ? 2 : 1); j++) r.w[j] = reinterpret_cast<const u32x4*>(p)[j];
+  for (int j = 0; j < (DT == FP8Q_DTYPE_F32 ? 2 : 1); j++) {
+    const u32x4* w = reinterpret_cast<const u32x4*>(p) + j;
+    r.w[j] = STREAMED ? __builtin_nontemporal_load(w) : *w;
+  }
   return r;
 }
 
@@ -58,45 +69,31 @@ __device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
   return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(static_cast<int>(v), static_cast<int>(v), CTRL, 0xF, 0xF, false));
 }
 
-template <int DT, bool SILU, int ROWS>
+template <int DT, bool SILU, bool STREAMED>
 __global__ __launch_bounds__(kThreads) void mxfp4_quant_kernel(Mxfp4RowsParams p, Grid g) {
   constexpr int kEsz = DT == FP8Q_DTYPE_F32 ? 4 : 2;
   constexpr int kIn = SILU ? FP8Q_DTYPE_F32 : DT;  // what is encoded
   const uint32_t u = blockIdx.x * kThreads + threadIdx.x;
   if (u >= g.units) return;  // (whole quads, and with packed scales whole rows of 16 lanes)
-  const uint32_t group = divide(u, g.by_per);
-  const int64_t row = static_cast<int64_t>(group) * ROWS, k = static_cast<int64_t>(u - group * g.per) * kEl;
+  const uint32_t row32 = divide(u, g.by_per);
+  const int64_t row = row32, k = static_cast<int64_t>(u - row32 * g.per) * kEl;
   const uint8_t* x = static_cast<const uint8_t*>(p.x) + (row * p.x_sm + k) * kEsz;
-  Raw8<DT> raw[ROWS], up[SILU ? ROWS : 1];
-#pragma unroll
-  for (int i = 0; i < ROWS; i++) {  // rows past the last one: that row again, not stored
-    const int64_t at = (row + i < p.M ? i : p.M - 1 - row) * p.x_sm * kEsz;
-    raw[i] = load8<DT>(x + at);
-    if constexpr (SILU) up[i] = load8<DT>(x + at + p.K * kEsz);
-  }
-#pragma unroll
-  for (int i = 0; i < ROWS; i++) {
-    Raw8<kIn> v;
-    if constexpr (SILU) v = silu_mul8<DT>(raw[i], up[i]);
-    else v = raw[i];
-    // a scale block's four lanes are a quad
-    float amax = amax8<kIn>(v);
-    amax = fmaxf(amax, dpp<0xB1>(amax));
-    amax = fmaxf(amax, dpp<0x4E>(amax));
-    const uint32_t byte = e2m1_scale_byte(fmaxf(amax, kEps));
-    const uint32_t c = encode8<kIn>(v, __uint_as_float(byte << 23));
+  Raw8<kIn> v;
+  if constexpr (SILU) v = silu_mul8<DT>(load8<DT, STREAMED>(x), load8<DT, STREAMED>(x + p.K * kEsz));
+  else v = load8<DT, STREAMED>(x);
+  // a scale block's four lanes are a quad
+  float amax = amax8<kIn>(v);
+  amax = fmaxf(amax, dpp<0xB1>(amax));
+  amax = fmaxf(amax, dpp<0x4E>(amax));
+  const uint32_t byte = e2m1_scale_byte(fmaxf(amax, kEps));
+  *reinterpret_cast<uint32_t*>(p.q + row * p.q_sm + k / 2) = encode8<kIn>(v, __uint_as_float(byte << 23));
+  if (p.packed) {  // the bytes of 16 lanes' four blocks
     uint32_t word = byte << (k & 96) / 4;
-    if (p.packed) {  // the bytes of 16 lanes' four blocks
-      word |= dpp_u32<0x124>(word);  // row_ror:4
-      word |= dpp_u32<0x128>(word);  // row_ror:8
-    }
-    if (row + i >= p.M) continue;
-    *reinterpret_cast<uint32_t*>(p.q + (row + i) * p.q_sm + k / 2) = c;
-    if (p.packed) {
-      if ((k & 127) == 0) reinterpret_cast<uint32_t*>(p.s)[(row + i) * p.s_sm + k / 128 * p.s_sg] = word;
-    } else if ((k & 31) == 0) {
-      p.s[(row + i) * p.s_sm + k / kMxBlock * p.s_sg] = static_cast<uint8_t>(byte);
-    }
+    word |= dpp_u32<0x124>(word);  // row_ror:4
+    word |= dpp_u32<0x128>(word);  // row_ror:8
+    if ((k & 127) == 0) reinterpret_cast<uint32_t*>(p.s)[row * p.s_sm + k / 128 * p.s_sg] = word;
+  } else if ((k & 31) == 0) {
+    p.s[row * p.s_sm + k / kMxBlock * p.s_sg] = static_cast<uint8_t>(byte);
   }
 }
 
@@ -142,15 +139,10 @@ void by_ranges(const Mxfp4RowsParams& p, int rows, int esz, F one) {
   }
 }
 
-// Four rows to a lane where that still gives every CU two blocks.
-bool tall(const Mxfp4RowsParams& p) {
-  return p.M >= 4 && p.M / 4 * (p.K / kEl) >= int64_t(2) * kThreads * current_device_shape().cus;
-}
-
-template <int DT, bool SILU, int ROWS>
+template <int DT, bool SILU, bool STREAMED>
 void quant(const Mxfp4RowsParams& p, hipStream_t stream) {
-  by_ranges(p, ROWS, DT == FP8Q_DTYPE_F32 ? 4 : 2, [&](const Mxfp4RowsParams& r, dim3 grid, const Grid& g) {
-    hipLaunchKernelGGL((mxfp4_quant_kernel<DT, SILU, ROWS>), grid, dim3(kThreads), 0, stream, r, g);
+  by_ranges(p, 1, DT == FP8Q_DTYPE_F32 ? 4 : 2, [&](const Mxfp4RowsParams& r, dim3 grid, const Grid& g) {
+    hipLaunchKernelGGL((mxfp4_quant_kernel<DT, SILU, STREAMED>), grid, dim3(kThreads), 0, stream, r, g);
   });
 }
 template <int DT, int ROWS>
@@ -162,12 +154,15 @@ void dequant(const Mxfp4RowsParams& p, hipStream_t stream) {
 
 template <int DT>
 void quant_any(bool silu, const Mxfp4RowsParams& p, hipStream_t stream) {
-  if (silu) tall(p) ? quant<DT, true, 4>(p, stream) : quant<DT, true, 1>(p, stream);
-  else tall(p) ? quant<DT, false, 4>(p, stream) : quant<DT, false, 1>(p, stream);
+  const bool streamed = p.M > kStreamed / (p.K * (silu ? 2 : 1) * (DT == FP8Q_DTYPE_F32 ? 4 : 2));
+  if (silu) streamed ? quant<DT, true, true>(p, stream) : quant<DT, true, false>(p, stream);
+  else streamed ? quant<DT, false, true>(p, stream) : quant<DT, false, false>(p, stream);
 }
+// Four rows to a lane where that still gives every CU two blocks.
 template <int DT>
 void dequant_any(const Mxfp4RowsParams& p, hipStream_t stream) {
-  tall(p) ? dequant<DT, 4>(p, stream) : dequant<DT, 1>(p, stream);
+  const bool tall = p.M >= 4 && p.M / 4 * (p.K / kEl) >= int64_t(2) * kThreads * current_device_shape().cus;
+  tall ? dequant<DT, 4>(p, stream) : dequant<DT, 1>(p, stream);
 }
 
 int finish(const char* what) {
