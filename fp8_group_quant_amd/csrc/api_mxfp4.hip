@@ -50,6 +50,12 @@ int rows_entry(const char* name, bool quant, bool silu, void* x, int dtype, int6
   return quant ? launch_mxfp4_quant(dtype, silu, p, st) : launch_mxfp4_dequant(dtype, p, st);
 }
 
+constexpr int64_t kMostStride = int64_t(1) << 24;  // bytes
+bool gemm_sizes(int64_t M, int64_t N, int64_t K) {
+  constexpr int64_t kMost = int64_t(1) << 26;
+  return M <= kMost && N <= kMost && M * N <= (int64_t(1) << 40) && K < (int64_t(1) << 25);
+}
+
 // One operand's scales as words of four: packed words with any strides, or row-major bytes in whole words.
 int scale_words(const std::string& pre, const char* which, const void* s, int fmt, int64_t rows, int64_t K, int64_t sm,
                 int64_t sk, int64_t& word_sm, int64_t& word_sk) {
@@ -63,6 +69,8 @@ int scale_words(const std::string& pre, const char* which, const void* s, int fm
     word_sk = 1;
   }
   if (!aligned(s, 4)) return fail(FP8Q_EALIGN, pre + which + " scales must be 4-byte aligned");
+  if (rows > 1 && word_sm >= kMostStride / 4)
+    return fail(FP8Q_EUNSUPPORTED, pre + which + " rows of scales must be less than 2^24 bytes apart");
   return FP8Q_OK;
 }
 
@@ -75,8 +83,7 @@ int gemm_entry(const uint8_t* a, int64_t lda, const void* sa, int sa_fmt, int64_
   if (!e8(sa_fmt) || !e8(sb_fmt)) return fail(FP8Q_EUNSUPPORTED, pre + "scales must be UE8M0 or UE8M0_PACKED");
   if (M < 0 || N < 0 || K < 0) return fail(FP8Q_EINVAL, pre + "negative size");
   if (K % 128 != 0) return fail(FP8Q_EINVAL, pre + "K must be a multiple of 128");
-  if (M >= (int64_t(1) << 31) || N >= (int64_t(1) << 31) || K >= (int64_t(1) << 31))
-    return fail(FP8Q_EUNSUPPORTED, pre + "sizes below 2^31");
+  if (!gemm_sizes(M, N, K)) return fail(FP8Q_EUNSUPPORTED, pre + "M and N up to 2^26, M * N up to 2^40, K below 2^25");
   if (lda < 0 || ldb < 0 || ldy < 0 || sa_sm < 0 || sa_sk < 0 || sb_sn < 0 || sb_sk < 0)
     return fail(FP8Q_EINVAL, pre + "negative stride");
   if (workspace_bytes < 0) return fail(FP8Q_EINVAL, pre + "negative workspace size");
@@ -85,6 +92,9 @@ int gemm_entry(const uint8_t* a, int64_t lda, const void* sa, int sa_fmt, int64_
   if (!a || !b || !y || !sa || !sb) return fail(FP8Q_EINVAL, pre + "null tensor pointer");
   if ((M > 1 && lda < K / 2) || (N > 1 && ldb < K / 2)) return fail(FP8Q_EINVAL, pre + "lda and ldb must be >= K / 2");
   if (M > 1 && ldy < N) return fail(FP8Q_EINVAL, pre + "ldy must be >= N (rows of y overlap)");
+  // (a tile's rows lie within 32 bits of its first one)
+  if ((M > 1 && lda >= kMostStride) || (N > 1 && ldb >= kMostStride))
+    return fail(FP8Q_EUNSUPPORTED, pre + "lda and ldb must be below 2^24");
   if (!aligned(a, 16) || !aligned(b, 16) || (M > 1 && lda % 16 != 0) || (N > 1 && ldb % 16 != 0))
     return fail(FP8Q_EALIGN, pre + "a, b and their row strides must be 16-byte aligned");
   if (!aligned(y, 2)) return fail(FP8Q_EALIGN, pre + "y must be 2-byte aligned");
@@ -137,9 +147,7 @@ int fp8q_mxfp4_dequant(const uint8_t* q, int64_t q_sm, const void* s, int scale_
 int64_t fp8q_gemm_mxfp4_workspace_size(int64_t M, int64_t N, int64_t K) {
   using namespace fp8q;
   set_error("");
-  const int64_t most = int64_t(1) << 31;
-  if (M <= 0 || N <= 0 || K <= 0 || M >= most || N >= most || K >= most || K % 128 != 0 || check_current_device() != FP8Q_OK)
-    return 0;
+  if (M <= 0 || N <= 0 || K <= 0 || !gemm_sizes(M, N, K) || K % 128 != 0 || check_current_device() != FP8Q_OK) return 0;
   return mxfp4_gemm_workspace_bytes(M, N, K);
 }
 

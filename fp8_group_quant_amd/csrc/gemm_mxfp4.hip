@@ -56,9 +56,9 @@ __device__ __forceinline__ uint32_t lds_addr(const void* p) {
   return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((const lds_u8*)p));
 }
 typedef int v4i __attribute__((ext_vector_type(4)));
-// lane l: LDS [lds + 16 l, + 16) <- buffer [voff + soff, + 16)
-__device__ __forceinline__ void dma16(uint32_t lds, v4i buffer, uint32_t voff, uint32_t soff) {
-  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds), "v"(voff), "s"(buffer), "s"(soff) : "memory");
+// lane l: LDS [lds + 16 l, + 16) <- buffer [voff, + 16), all of the offset in the register that the bounds check looks at
+__device__ __forceinline__ void dma16(uint32_t lds, v4i buffer, uint32_t voff) {
+  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(voff), "s"(buffer) : "memory");
 }
 // lane l: LDS [lds + 4 l, + 4) <- global [base + voff, + 4)
 __device__ __forceinline__ void dma4(uint32_t lds, const uint8_t* base, uint32_t voff) {
@@ -184,10 +184,10 @@ struct Loader {
   __device__ __forceinline__ void issue(int n) {
     const uint32_t at = lds + stage;
     if (n < C::kLA) {
-      dma16(at + (wave * C::kLA + n) * 1024, now.a, a_off[n & 1], (wave * C::kLA + n) * lda_piece + step * C::kRow);
+      dma16(at + (wave * C::kLA + n) * 1024, now.a, a_off[n & 1] + ((wave * C::kLA + n) * lda_piece + step * C::kRow));
     } else if (n < C::kLA + C::kLB) {
       const int q = n - C::kLA;
-      dma16(at + C::kB + (wave * C::kLB + q) * 1024, now.b, b_off[q & 1], (wave * C::kLB + q) * ldb_piece + step * C::kRow);
+      dma16(at + C::kB + (wave * C::kLB + q) * 1024, now.b, b_off[q & 1] + ((wave * C::kLB + q) * ldb_piece + step * C::kRow));
     } else {
       const int q = (n - C::kLA - C::kLB) / C::kWords, word = (n - C::kLA - C::kLB) % C::kWords;
       const bool is_a = Source<C>::of_a(q, wave), there = word == 0 || C::kWords * step + word < units;

@@ -371,9 +371,10 @@ int fp8q_mxfp4_dequant(const uint8_t* q, int64_t q_sm, const void* s, int scale_
  * unsplit: same results up to the order of fp32 sums, each deterministic. The library writes only that many
  * bytes; calls that overlap in time must not share a workspace.
  *
- * Requirements: scale formats as above [EUNSUPPORTED]; M, N, K >= 0 and below 2^31 [EUNSUPPORTED], K % 128 == 0
- * [EINVAL]; lda, ldb >= K / 2, ldy >= N [EINVAL]; a, b and their row strides and the workspace 16-byte
- * aligned, scales and their rows 4-byte, y 2-byte [EALIGN].
+ * Requirements: scale formats as above, M and N up to 2^26, M * N up to 2^40, K below 2^25, lda and ldb below 2^24,
+ * rows of scales less than 2^24 bytes apart [EUNSUPPORTED]; M, N, K >= 0, K % 128 == 0 [EINVAL]; lda, ldb >= K / 2,
+ * ldy >= N [EINVAL]; a, b and their row strides and the workspace 16-byte aligned, scales and their rows 4-byte,
+ * y 2-byte [EALIGN].
  */
 int64_t fp8q_gemm_mxfp4_workspace_size(int64_t M, int64_t N, int64_t K);
 

@@ -58,6 +58,11 @@ GEMM = dict(a=0x10000, lda=256, sa=0x20000, sa_fmt=2, sa_sm=1, sa_sk=8, b=0x3000
     (dict(sa_fmt=1, sa_sm=18, sa_sk=1), EALIGN), (dict(sa_fmt=1, sa_sm=16, sa_sk=1, sa=0x20002), EALIGN), (dict(sb=0x40001), EALIGN),
     (dict(M=-1), EINVAL), (dict(N=-1), EINVAL), (dict(K=-128), EINVAL), (dict(K=192), EINVAL),
     (dict(M=1 << 31), EUNSUPPORTED), (dict(N=1 << 31), EUNSUPPORTED), (dict(K=1 << 31), EUNSUPPORTED),
+    (dict(M=1 << 26), EDEVICE), (dict(M=(1 << 26) + 1), EUNSUPPORTED), (dict(M=1 << 20, N=1 << 20, ldy=1 << 20), EDEVICE),
+    (dict(M=1 << 21, N=1 << 20, ldy=1 << 20), EUNSUPPORTED), (dict(K=1 << 25, lda=1 << 24, ldb=1 << 24), EUNSUPPORTED),
+    (dict(lda=(1 << 24) - 16), EDEVICE), (dict(lda=1 << 24), EUNSUPPORTED), (dict(M=1, lda=1 << 24), EDEVICE),
+    (dict(ldb=1 << 24), EUNSUPPORTED), (dict(sa_sm=1 << 22, sa_sk=1), EUNSUPPORTED), (dict(sa_sm=(1 << 22) - 1, sa_sk=1), EDEVICE),
+    (dict(sb_fmt=1, sb_sn=1 << 24, sb_sk=1), EUNSUPPORTED), (dict(sa_sk=1 << 40), EDEVICE),
     (dict(lda=-16), EINVAL), (dict(sb_sk=-1), EINVAL), (dict(ldy=-1), EINVAL),
     (dict(a=None), EINVAL), (dict(b=None), EINVAL), (dict(y=None), EINVAL), (dict(sa=None), EINVAL), (dict(sb=None), EINVAL),
     (dict(lda=240), EINVAL), (dict(ldb=128), EINVAL), (dict(ldy=99), EINVAL), (dict(M=1, lda=0, ldy=0), EDEVICE),
