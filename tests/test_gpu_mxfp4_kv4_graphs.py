@@ -1,0 +1,288 @@
+"""The 4-bit product's chain and a serving step (plan, cache write, window and tree attention) captured and replayed, also
+two graphs at once; offsets past 32 bits; rows behind the last sequence."""
+import pytest
+import torch
+
+import masked_oracle as masked
+import serving_oracle as ref
+
+pytestmark = pytest.mark.gpu
+
+
+def fq():
+    import fp8_group_quant_amd
+    return fp8_group_quant_amd
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def captured(run):
+    """A graph of run() on a stream of its own (after one eager run there)."""
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        run()
+    st.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=st):
+        run()
+    return g
+
+
+class Layer:
+    """x through quantizer, product, silu quantizer and product; the sizes split K in the first product."""
+
+    def __init__(self, seed, M):
+        f, g = fq(), gen(seed)
+        D, I = 4096, 512
+        self.b1, self.t1 = f.mxfp4_quant(torch.randn(2 * I, D, generator=g).cuda())
+        self.b2, self.t2 = f.mxfp4_quant(torch.randn(D, I, generator=g).cuda())
+        self.x = torch.empty(M, D, dtype=torch.bfloat16, device="cuda")
+        self.h = torch.empty(M, 2 * I, dtype=torch.bfloat16, device="cuda")
+        self.y = torch.empty(M, D, dtype=torch.bfloat16, device="cuda")
+        self.fill(seed)
+
+    def fill(self, seed):
+        self.x.copy_(torch.randn(self.x.shape, generator=gen(seed)).to(torch.bfloat16))
+
+    def run(self):
+        f = fq()
+        q, s = f.mxfp4_quant(self.x)
+        f.fp8q_gemm_mxfp4(q, s, self.b1, self.t1, self.h)
+        q, s = f.mxfp4_quant(self.h, silu=True)
+        f.fp8q_gemm_mxfp4(q, s, self.b2, self.t2, self.y)
+        self.back = f.mxfp4_dequant(q, s)
+
+    def results(self):
+        return [t.clone() for t in (self.h, self.y, self.back)]
+
+
+class Step:
+    """A decode step: page plan, cache write, attention with a window and of a tree over the same lengths."""
+
+    def __init__(self, seed, B, n):
+        f = fq()
+        self.B, self.n = B, n
+        g = gen(seed)
+        H, D, page, width = 2, 128, 16, 200
+        i32 = dict(dtype=torch.int32, device="cuda")
+        pages = B * (width + 10)  # the last 10 B are free: no slot is two tokens'
+        self.c = f.alloc_kv4_cache(pages, page, H, D)
+        for t in (self.c.k, self.c.v):
+            t.copy_(torch.randint(0, 256, t.shape, generator=g, dtype=torch.uint8))
+        for t in (self.c.k_scales, self.c.v_scales):
+            t.copy_(torch.randint(122, 130, t.shape, generator=g, dtype=torch.uint8))
+        self.lens = torch.randint(1, 2500, (B,), generator=g).to(torch.int32).cuda()
+        self.table = torch.arange(B * width, **i32).view(B, width).flip(0).contiguous()
+        self.free = (B * width + torch.randperm(10 * B, generator=g)).to(torch.int32).cuda()
+        self.new = torch.full((B,), n, **i32)
+        self.mask = torch.tensor([(2 << i) - 1 for i in range(n)] * B, **i32).view(-1, 1)
+        self.q = torch.empty(B * n, 8, D, dtype=torch.bfloat16, device="cuda")
+        self.k, self.v = (torch.empty(B * n, H, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        self.fill(seed)
+
+    def fill(self, seed):
+        g = gen(seed)
+        for t in (self.q, self.k, self.v):
+            t.copy_(torch.randn(t.shape, generator=g).to(torch.bfloat16))
+
+    def run(self):
+        f = fq()
+        self.plan = f.kv4_plan(self.c, self.lens, self.new, self.free, self.table, self.B * self.n)
+        f.fp8q_kv4_write(self.k, self.v, self.plan.slots, self.c)
+        self.w = f.kv4_window_attention(self.q, self.c, self.table, self.plan.kv_lens, 0.1, 700, 4, self.plan.q_indptr)
+        self.t = f.kv4_tree_attention(self.q, self.c, self.table, self.plan.kv_lens, 0.1, self.mask, self.plan.q_indptr)
+
+    def go_on(self):
+        """The step is done: its pages are no longer free, its tokens are cached."""
+        self.free.copy_(self.free.roll(-int(self.plan.pages_taken)))
+        self.lens.copy_(self.plan.kv_lens)
+
+    def results(self):
+        return [t.clone() for t in (*self.plan, self.w, self.t, self.table)]
+
+
+def equal(a, b):
+    return all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("make", [lambda s: Layer(s, 1), lambda s: Layer(s, 40), lambda s: Layer(s, 130), lambda s: Step(s, 1, 1),
+                                  lambda s: Step(s, 3, 5), lambda s: Step(s, 40, 2)],
+                         ids=["layer1", "layer40", "layer130", "step1x1", "step3x5", "step40x2"])
+def test_captured_and_replayed(make):
+    """Every replay, with other inputs and the program's own work before it, against the eager run on a twin."""
+    work, twin = make(1), make(1)
+    graph = captured(work.run)
+    graph.replay()  # (what it writes is only there once it has run)
+    twin.run()
+    for seed in (2, 3, 4, 5):
+        work.fill(seed)
+        twin.fill(seed)
+        if isinstance(work, Step):
+            work.go_on()
+            twin.go_on()
+        torch.randn(1000, 1000, device="cuda").sum().item()
+        graph.replay()
+        twin.run()
+        torch.cuda.synchronize()
+        assert equal(work.results(), twin.results())
+
+
+@pytest.mark.parametrize("make", [lambda s: Layer(s, 130), lambda s: Step(s, 2, 5)], ids=["layer", "step"])
+def test_two_graphs_at_once(make):
+    """Two graphs, each with the workspaces of its own allocations, replayed at the same time on two streams."""
+    works, wants = [], []
+    for seed in (1, 2):
+        works.append(make(seed))
+        twin = make(seed)
+        twin.run()
+        torch.cuda.synchronize()
+        wants.append(twin.results())
+    graphs = [captured(w.run) for w in works]
+    streams = [torch.cuda.Stream() for _ in works]
+    for _ in range(3):
+        torch.cuda.synchronize()
+        for _ in range(5):
+            for g, st in zip(graphs, streams):
+                with torch.cuda.stream(st):
+                    g.replay()
+        torch.cuda.synchronize()
+        for w, want in zip(works, wants):
+            assert equal(w.results(), want)
+
+
+# ------------------------------------------------------------------ offsets past 32 bits
+def far_rows(t, stride):
+    """Rows of a 2-D tensor, `stride` elements apart."""
+    holder = torch.empty((t.shape[0] - 1) * stride + t.shape[1], dtype=t.dtype, device="cuda")
+    out = holder.as_strided(t.shape, (stride, 1))
+    out.copy_(t)
+    return out
+
+
+@pytest.mark.parametrize("M,N", [(300, 40), (40, 300), (700, 290)])
+def test_product_rows_far_apart(M, N):
+    """The largest strides that are allowed: rows past 4 GiB from the first, in codes, scales and outputs."""
+    f = fq()
+    K = 640
+    a, sa = f.mxfp4_quant(torch.randn(M, K, generator=gen(1)).cuda(), "ue8m0_packed", "row")
+    b, sb = f.mxfp4_quant(torch.randn(N, K, generator=gen(2)).cuda(), "ue8m0_packed", "row")
+    want = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    f.fp8q_gemm_mxfp4(a, sa, b, sb, want)
+    far = (1 << 24) - 16
+    y = far_rows(torch.zeros_like(want), 1 << 23)
+    f.fp8q_gemm_mxfp4(far_rows(a, far), far_rows(sa, far // 4 + 3), far_rows(b, far), far_rows(sb, far // 4 + 3), y)
+    assert torch.equal(y, want)
+
+
+def test_quant_rows_far_apart():
+    f = fq()
+    x = torch.randn(40, 512, generator=gen(1)).to(torch.bfloat16).cuda()
+    q, s = f.mxfp4_quant(x, "ue8m0", "row")
+    far_q, far_s = far_rows(torch.zeros_like(q), 1 << 28), far_rows(torch.zeros_like(s), 1 << 28)
+    f.fp8q_mxfp4_quant(far_rows(x, 1 << 28), far_q, far_s)
+    assert torch.equal(far_q, q) and torch.equal(far_s, s)
+    back = far_rows(torch.zeros_like(x), 1 << 28)
+    f.fp8q_mxfp4_dequant(far_q, far_s, back)
+    assert torch.equal(back, f.mxfp4_dequant(q, s))
+
+
+def far_cache(near, pages):
+    """A cache of many pages, the last ones those of `near`: (cache, their first page)."""
+    f = fq()
+    n, page, heads, width = near.k.shape
+    at = pages - n
+
+    def grown(t):
+        out = torch.empty(pages, heads, page, t.shape[3], dtype=torch.uint8, device="cuda").transpose(1, 2)
+        out[at:] = t
+        return out
+
+    return f.Kv4Cache(*(grown(t) for t in near)), at
+
+
+@pytest.mark.parametrize("q_len", [1, 6, 100])
+@pytest.mark.parametrize("kind", ["window", "tree"])
+def test_pages_past_4_gib(kind, q_len):
+    f = fq()
+    page, pages, lens = 64, 30, [900, 700]
+    near = f.alloc_kv4_cache(pages, page, 8, 256)
+    for t, lo, hi in ((near.k, 0, 256), (near.v, 0, 256), (near.k_scales, 120, 130), (near.v_scales, 120, 130)):
+        t.copy_(torch.randint(lo, hi, t.shape, generator=gen(3), dtype=torch.uint8))
+    c, at = far_cache(near, 80000)  # 64 KiB a page
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").view(2, 15)
+    q = torch.randn(2 * q_len, 16, 256, generator=gen(4)).to(torch.bfloat16).cuda()
+    ip = torch.tensor([0, q_len, 2 * q_len], dtype=torch.int32).cuda()
+    kv = torch.tensor(lens, dtype=torch.int32).cuda()
+    mask = torch.full((2 * q_len, 4), -1, dtype=torch.int32, device="cuda")
+    outs = [f.kv4_window_attention(q, cc, tb, kv, 0.05, 400, 4, ip) if kind == "window" else
+            f.kv4_tree_attention(q, cc, tb, kv, 0.05, mask, ip) for cc, tb in ((near, table), (c, table + at))]
+    assert torch.equal(*outs)
+
+
+@pytest.mark.parametrize("q_len", [1, 3, 90])
+def test_window_at_the_end_of_the_longest_cache(q_len):
+    """2^30 cached tokens of which all but the window's and the sinks' pages are nowhere."""
+    f = fq()
+    page, window, sinks = 128, 300, 4
+    near = f.alloc_kv4_cache(8, page, 2, 64)
+    for t, lo, hi in ((near.k, 0, 256), (near.v, 0, 256), (near.k_scales, 120, 130), (near.v_scales, 120, 130)):
+        t.copy_(torch.randint(lo, hi, t.shape, generator=gen(3), dtype=torch.uint8))
+    long = 1 << 30
+    table = torch.full((1, long // page), -1, dtype=torch.int32)
+    order = [5, 2, 7, 1, 0]
+    table[0, 0] = 6
+    table[0, -5:] = torch.tensor(order, dtype=torch.int32)
+    q = torch.randn(q_len, 8, 64, generator=gen(4)).to(torch.bfloat16)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    ip = torch.tensor([0, q_len], **i32)
+    got = f.kv4_window_attention(q.cuda(), near, table.cuda(), torch.tensor([long], **i32), 0.1, window, sinks, ip)
+    # the same rows where only the first page and the last five are cached
+    small = torch.tensor([[6] + order], dtype=torch.int32)
+    k64, v64 = (ref.dequantize(a.cpu(), b.cpu()) for a, b in ((near.k, near.k_scales), (near.v, near.v_scales)))
+    n = 6 * page
+    o, l, mass, slack = masked.attention(q, k64, v64, small, [n], [q_len], page, 8, 0.1,
+                                         lambda b, m, length, at: masked.window_sees(m, length, window, sinks))
+    bound, _ = ref.attention_bounds(o, l, mass, slack, 64, n, torch.bfloat16)
+    assert bool(((got.cpu().double() - o).abs() <= bound).all())
+
+
+# ------------------------------------------------------------------ rows behind the last sequence
+@pytest.mark.parametrize("T,ends", [(9, [0, 2, 5]), (200, [0, 70, 130]), (40, [3, 10, 10, 30])])
+@pytest.mark.parametrize("kind", ["window", "tree"])
+def test_rows_of_no_sequence_stay(kind, T, ends):
+    f = fq()
+    B = len(ends) - 1
+    c = f.alloc_kv4_cache(40, 16, 2, 64)
+    for t in c:
+        t.copy_(torch.randint(120, 130, t.shape, generator=gen(3), dtype=torch.uint8))
+    table = torch.arange(10 * B, dtype=torch.int32, device="cuda").view(B, 10)
+    q = torch.randn(T, 4, 64, generator=gen(4)).to(torch.bfloat16).cuda()
+    ip = torch.tensor(ends, dtype=torch.int32).cuda()
+    kv = torch.full((B,), 150, dtype=torch.int32).cuda()
+    out = torch.full((T, 4, 64), 77.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((T, 4), 77.0, device="cuda")
+    if kind == "window":
+        f.fp8q_kv4_window_attention(q, c, table, kv, out, 0.1, 50, 2, ip, lse)
+    else:
+        f.fp8q_kv4_tree_attention(q, c, table, kv, out, 0.1, torch.full((T, 3), -1, dtype=torch.int32, device="cuda"), ip, lse)
+    for a, b in ((0, ends[0]), (ends[-1], T)):
+        assert bool((out[a:b] == 77).all()) and bool((lse[a:b] == 77).all())
+    assert not bool((out[ends[0]:ends[-1]] == 77).all(-1).any()) and not bool((lse[ends[0]:ends[-1]] == 77).any())
+
+
+def test_one_page_for_two_sequences():
+    """A shared prefix: two sequences whose tables name the same pages see the same tokens."""
+    f = fq()
+    c = f.alloc_kv4_cache(12, 16, 2, 64)
+    for t in c:
+        t.copy_(torch.randint(120, 130, t.shape, generator=gen(3), dtype=torch.uint8))
+    table = torch.arange(10, dtype=torch.int32, device="cuda").repeat(2, 1)
+    q = torch.randn(3, 4, 64, generator=gen(4)).to(torch.bfloat16).cuda().repeat(2, 1, 1)
+    ip = torch.tensor([0, 3, 6], dtype=torch.int32).cuda()
+    kv = torch.full((2,), 150, dtype=torch.int32).cuda()
+    mask = torch.tensor([[1], [3], [5]] * 2, dtype=torch.int32).cuda()
+    for out in (f.kv4_window_attention(q, c, table, kv, 0.1, 50, 2, ip), f.kv4_tree_attention(q, c, table, kv, 0.1, mask, ip)):
+        assert torch.equal(out[:3], out[3:])
