@@ -1143,16 +1143,18 @@ __global__ __launch_bounds__(64 * kWideWaves, wide_waves_per_simd(D, DT, QT, SPL
   }
 }
 
-// Joins the pieces of query rows, WAVES waves for each: they take the pieces in turn, every
-// lane D / 64 elements.
+// Joins the pieces of query rows. WAVES = 1: 256 / D rows to a wave, four elements to a lane (a row's lookups are a
+// chain of loads, which as few waves as this go through; with a row to a wave the rows of 16 trees of up to 64 tokens
+// and 32 heads of 64 take 19 us, now 8). More waves: all of a block take one row's pieces in turn, every lane D / 64 elements.
 template <int MASK, int D, int DT, int ROWS, int WAVES>
 __global__ __launch_bounds__(64 * kJoinWaves) void kv4_join_kernel(Kv4AttnParams p) {
-  constexpr int kPer = D / 64;
+  constexpr int kPer = WAVES == 1 ? 4 : D / 64, kLanes = D / kPer, kRowsWave = 64 / kLanes;
   constexpr int kStepF = ROWS * (D + 2);  // floats of a piece
   __shared__ float lds_o[WAVES][D], lds_l[WAVES];
-  const int tid = threadIdx.x, lane = tid & 63, wave = wave_index();
-  const int32_t row = blockIdx.x * (kJoinWaves / WAVES) + (WAVES == 1 ? wave : 0);  // of T * Hq
-  if (row >= static_cast<int32_t>(p.T) * p.Hq) return;
+  const int tid = threadIdx.x, lane = tid & (kLanes - 1), wave = wave_index();  // lane: of the row's
+  const int64_t row64 = WAVES == 1 ? (int64_t(blockIdx.x) * kJoinWaves + wave) * kRowsWave + (tid & 63) / kLanes : blockIdx.x;  // of T * Hq
+  if (row64 >= p.T * p.Hq) return;
+  const int32_t row = static_cast<int32_t>(row64);
   const int32_t t = row / p.Hq, qh = row - t * p.Hq;
   int32_t b = t;
   if (p.q_indptr) {  // the sequence that holds row t: the last one whose clamped start is not after it
@@ -1177,8 +1179,13 @@ __global__ __launch_bounds__(64 * kJoinWaves) void kv4_join_kernel(Kv4AttnParams
   const float* ml = base + ROWS * D + 2 * at;
 
   float top = kNegInf;
-  for (int32_t c = lane; c < pieces; c += 64) top = fmaxf(top, ml[static_cast<int64_t>(c) * kStepF]);
-  top = wave_max(top);
+  for (int32_t c = lane; c < pieces; c += kLanes) top = fmaxf(top, ml[static_cast<int64_t>(c) * kStepF]);
+  if constexpr (kLanes == 64) {
+    top = wave_max(top);
+  } else {  // (a row's lanes are here together)
+#pragma unroll
+    for (int off = 1; off < kLanes; off <<= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
+  }
   const float ts = top == kNegInf ? 0.0f : top;
   float acc[kPer], l = 0.0f;
 #pragma unroll
@@ -1188,8 +1195,15 @@ __global__ __launch_bounds__(64 * kJoinWaves) void kv4_join_kernel(Kv4AttnParams
     const int64_t off = static_cast<int64_t>(c) * kStepF;
     const float f = exp2_fast(ml[off] - ts);
     l += ml[off + 1] * f;
+    const float* o = base + off + at * D + kPer * lane;
+    if constexpr (kPer == 4) {
+      const f32x4 v = *reinterpret_cast<const f32x4*>(o);
 #pragma unroll
-    for (int i = 0; i < kPer; i++) acc[i] += base[off + at * D + kPer * lane + i] * f;
+      for (int i = 0; i < kPer; i++) acc[i] += v[i] * f;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPer; i++) acc[i] += o[i] * f;
+    }
   }
   if constexpr (WAVES > 1) {
 #pragma unroll
@@ -1209,11 +1223,12 @@ __global__ __launch_bounds__(64 * kJoinWaves) void kv4_join_kernel(Kv4AttnParams
   }
   const float inv = l == 0.0f ? 0.0f : 4.0f / l;
   uint16_t* dst = static_cast<uint16_t*>(p.out) + t * p.o_st + qh * p.o_sh + kPer * lane;
-  if constexpr (kPer == 1) {
+  if constexpr (kPer == 4) {
+    *reinterpret_cast<u32x2*>(dst) = u32x2{pack_out<DT>(acc[0] * inv, acc[1] * inv), pack_out<DT>(acc[2] * inv, acc[3] * inv)};
+  } else if constexpr (kPer == 1) {
     *dst = static_cast<uint16_t>(pack_out<DT>(acc[0] * inv, 0.0f));
   } else {
-#pragma unroll
-    for (int i = 0; i < kPer; i += 2) *reinterpret_cast<uint32_t*>(dst + i) = pack_out<DT>(acc[i] * inv, acc[i + 1] * inv);
+    *reinterpret_cast<uint32_t*>(dst) = pack_out<DT>(acc[0] * inv, acc[1] * inv);
   }
   if (p.lse && lane == 0) p.lse[t * p.l_st + qh] = l == 0.0f ? kNegInf : (ts + __builtin_amdgcn_logf(l)) * kLn2;
 }
@@ -1246,9 +1261,10 @@ struct Launch {
     }
     if constexpr (SPLIT) {
       const int64_t rows = p.T * p.Hq;
-      // a wave per row, or where the units are cut into many pieces a block
+      // some rows per wave, or where the units are cut into many pieces a block per row
+      constexpr int kBlock = kJoinWaves * 256 / D;
       if (shape.blocks < 8 * shape.units)
-        hipLaunchKernelGGL((kv4_join_kernel<MASK, D, DT, ROWS, 1>), dim3(static_cast<unsigned>((rows + kJoinWaves - 1) / kJoinWaves)),
+        hipLaunchKernelGGL((kv4_join_kernel<MASK, D, DT, ROWS, 1>), dim3(static_cast<unsigned>((rows + kBlock - 1) / kBlock)),
                            dim3(64 * kJoinWaves), 0, stream, p);
       else
         hipLaunchKernelGGL((kv4_join_kernel<MASK, D, DT, ROWS, kJoinWaves>), dim3(static_cast<unsigned>(rows)),
