@@ -52,6 +52,7 @@
 namespace fp8q {
 namespace {
 
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -68,6 +69,29 @@ constexpr float kHeadroom = 8.0f;
 constexpr float kNegInf = -__builtin_inff();
 
 __device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }
+
+// exp2(scale s - ms) of a row's four scores, added to l, as elements 4 at .. of an operand: bf16, or the sum of two parts
+// (two values to each conversion; a part's value in fp32 is its bits moved up).
+template <int PARTS>
+__device__ __forceinline__ void probabilities(const f32x4& s, float scale, float ms, float& l, bf16x8 (&to)[PARTS], int at) {
+#pragma unroll
+  for (int i = 0; i < 4; i += 2) {
+    const float e0 = exp2_fast(fmaf(s[i], scale, -ms)), e1 = exp2_fast(fmaf(s[i + 1], scale, -ms));
+    l += e0;
+    l += e1;
+    const f32x2 e = {e0, e1};
+    const bf16x2 hi = __builtin_convertvector(e, bf16x2);
+    to[0][4 * at + i] = hi[0];
+    to[0][4 * at + i + 1] = hi[1];
+    if constexpr (PARTS == 2) {
+      const uint32_t w = __builtin_bit_cast(uint32_t, hi);
+      const f32x2 rest = {e0 - __uint_as_float(w << 16), e1 - __uint_as_float(w & 0xFFFF0000u)};
+      const bf16x2 lo = __builtin_convertvector(rest, bf16x2);
+      to[1][4 * at + i] = lo[0];
+      to[1][4 * at + i + 1] = lo[1];
+    }
+  }
+}
 
 // Maximum and sum over the four lanes with the same l % 16.
 __device__ __forceinline__ float quad_max(float v) {
@@ -792,15 +816,7 @@ __global__ __launch_bounds__(64 * WAVES, waves_per_simd(D, DT, N)) void kv4_atte
       const float ms = m == kNegInf ? 0.0f : m;  // nothing seen yet: every p is 0
       bf16x8 pr[N / 2][PARTS];
 #pragma unroll
-      for (int c = 0; c < N; c++)
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-          const float e = exp2_fast(fmaf(s[c][i], p.scale_log2, -ms));
-          l += e;
-          const __bf16 hi = static_cast<__bf16>(e);
-          pr[c / 2][0][4 * (c % 2) + i] = hi;
-          if constexpr (PARTS == 2) pr[c / 2][1][4 * (c % 2) + i] = static_cast<__bf16>(e - static_cast<float>(hi));
-        }
+      for (int c = 0; c < N; c++) probabilities(s[c], p.scale_log2, ms, l, pr[c / 2], c % 2);
 
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
       __builtin_amdgcn_wave_barrier();
@@ -1048,7 +1064,7 @@ __global__ __launch_bounds__(64 * kWideWaves, wide_waves_per_simd(D, DT, QT, SPL
       {
         // wave-uniform
         const bool part = there != ~0ull || tok + kStepW > low || (MASK == kWindow && tok < high && tok + kStepW > p.sinks);
-        bf16x8 pr[QT][PARTS][kHalves / 2];
+        bf16x8 pr[QT][kHalves / 2][PARTS];
 #pragma unroll
         for (int n = 0; n < QT; n++) {
           if (part) {
@@ -1085,15 +1101,7 @@ __global__ __launch_bounds__(64 * kWideWaves, wide_waves_per_simd(D, DT, QT, SPL
           }
           const float ms = m[n] == kNegInf ? 0.0f : m[n];
 #pragma unroll
-          for (int c = 0; c < kHalves; c++)
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-              const float e = exp2_fast(fmaf(s[n][c][i], p.scale_log2, -ms));
-              l[n] += e;
-              const __bf16 hi = static_cast<__bf16>(e);
-              pr[n][0][c / 2][4 * (c % 2) + i] = hi;
-              if constexpr (PARTS == 2) pr[n][1][c / 2][4 * (c % 2) + i] = static_cast<__bf16>(e - static_cast<float>(hi));
-            }
+          for (int c = 0; c < kHalves; c++) probabilities(s[n][c], p.scale_log2, ms, l[n], pr[n][c / 2], c % 2);
         }
         // every operand is read one product ahead
 #pragma unroll
@@ -1106,7 +1114,7 @@ __global__ __launch_bounds__(64 * kWideWaves, wide_waves_per_simd(D, DT, QT, SPL
           for (int n = 0; n < QT; n++)
 #pragma unroll
             for (int a = 0; a < PARTS; a++)
-              o[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[g & 1], pr[n][a][c], o[n][d], 0, 0, 0);
+              o[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[g & 1], pr[n][c][a], o[n][d], 0, 0, 0);
           __builtin_amdgcn_sched_barrier(0);
         }
       }
