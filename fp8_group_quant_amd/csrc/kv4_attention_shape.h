@@ -67,13 +67,15 @@ constexpr int tall_waves(int DT, int64_t D) { return waves_per_simd(D, DT, 2) * 
 //   1 x  500  7.1  8.0 10.4    16 x  700  9.0  9.1 17.0    64 x  300 10.5 15.9 19.6
 //   1 x 2000 15   13.6 12.1    16 x 1500 15   12.4 19.2    64 x 1500 20.3 25.3 31.9
 //   2 x 4000 25   19.1 11.5    32 x 5000      33   39.6    64 x 3000 38.9 41.7 47
+// Trees stay whole for two steps more: one of 25 over 1000 tokens 13.3 and tall 14.6, 16 of 4 14.1 and 15.5 (but 8 single tokens
+// with windows of 700 11.9 and 10.9).
 enum class Cut { kWhole, kTall, kSplit };
 constexpr int kMostSteps = 16, kMostTallSteps = 12;
 
-inline Cut narrow_cut(int cus, int dtype, int64_t D, int64_t units, int64_t max_tokens, int64_t blocks) {
+inline Cut narrow_cut(int cus, int dtype, int64_t D, int64_t units, int64_t max_tokens, int64_t blocks, Mask mask = kAll) {
   const int64_t step = 16 * narrow_halves(dtype, D) * kNarrowWaves, tall_step = 32 * tall_waves(dtype, D);
   const int64_t whole = (max_tokens + step - 1) / step, tall = (max_tokens + tall_step - 1) / tall_step;
-  if (whole <= 2 || units >= 8 * blocks) return Cut::kWhole;
+  if (whole <= (mask == kTree ? 4 : 2) || units >= 8 * blocks) return Cut::kWhole;
   if (units > cus) return whole <= kMostSteps ? Cut::kWhole : Cut::kSplit;
   return tall <= kMostTallSteps && tall <= 3 * (units * max_tokens / (blocks * step) + 1) ? Cut::kTall : Cut::kSplit;
 }
@@ -133,7 +135,7 @@ inline AttnShape attention_shape(int cus, int dtype, int64_t B, int64_t T, int64
   // Windows are about equally long, so that nothing is gained by cutting them once every CU has two units (64 single tokens
   // with windows of 4096, 8 cached heads of 128: 65 us whole, 70 split).
   const Cut cut = narrow && mask == kWindow && units >= 2 * static_cast<int64_t>(cus) ? Cut::kWhole
-                  : narrow ? narrow_cut(cus, dtype, D, units, max_tokens, s.blocks) : wide_cut(units, max_tokens, s.blocks);
+                  : narrow ? narrow_cut(cus, dtype, D, units, max_tokens, s.blocks, mask) : wide_cut(units, max_tokens, s.blocks);
   s.tall = cut == Cut::kTall;
   // spans of 128 tokens, or longer ones where a split call's line could have 2^31 places
   s.span_shift = 7;
