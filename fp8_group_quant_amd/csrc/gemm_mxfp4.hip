@@ -2,6 +2,7 @@
 // (MXFP4), rounded to bf16 once:
 //   Y[m][n] = bf16( sum_k 2^(ea(m, k/32) - 127) A[m][k] * 2^(eb(n, k/32) - 127) B[n][k] )
 #include <algorithm>
+#include <type_traits>
 
 #include "mxfp4.h"
 
@@ -490,14 +491,17 @@ __global__ __launch_bounds__(256) void gemm_mxfp4_join_kernel(Mxfp4GemmParams p)
 }
 
 // ------------------------------------------------------------------ few rows
-// Up to 16 SM rows of A: a block has 16 rows of B and all of K, its waves contiguous ranges of it; operands go from
-// memory straight to registers, P steps of 128 elements at a time, and the waves' sums meet in LDS, added in their
+// Up to 16 SM rows of A: a block has 16 rows of B and all of K, its W waves contiguous ranges of it; operands go from
+// memory straight to registers, P units of 128 elements at a time, and the waves' sums meet in LDS, added in their
 // order. (v_mfma_scale_f32_16x16x128: lane (r, h) holds row r, the 32 elements of K block h, and its scale byte.) A lane
-// loads the scale word of one row for one of four steps (lane group h the h-th), which the others get by exchanges.
-template <int SM>
-struct Few {
-  static constexpr int kWaves = 8, P = SM == 4 ? 4 : 8;
-};
+// loads the scale word of one row for one of four units (lane group h the h-th), which the others get by exchanges.
+//
+// The weights' bytes bound it, for one row N x K (launch included): 4096 x 7168, 15.6 MB, 5.7 us; 16384 x 4096, 35.7 MB, 8.8
+// (4.0 TB/s); 28672 x 8192, 125 MB, 25.7 (4.9). A range that is not whole in P ends in a step of four units or of P with
+// clamped loads (steps of P only: 16384 x 4096, of 4 units to a wave, 12.9). Blocks are of 8 waves while no CU has two,
+// else of 4, which then have more loads each under way: us for 4 and 8, one row, 4096 x 7168 6.0 and 5.7, 16384 x 4096 8.8 and
+// 10.1, 28672 x 8192 25.7 and 29.8; 32 rows, 4096 x 7168 8.5 and 7.7, 8192 x 8192 15.4 and 15.9; 64 rows, 4096 x 7168 13.9 and
+// 11.3, 8192 x 8192 23.9 and 23.6.
 
 // The words that lane groups 0 .. 3 hold for row r, for every lane of it.
 __device__ __forceinline__ void spread(uint32_t w, uint32_t (&all)[4]) {
@@ -510,9 +514,10 @@ __device__ __forceinline__ void spread(uint32_t w, uint32_t (&all)[4]) {
   all[3] = b[1];
 }
 
-template <int SM>
-__global__ __launch_bounds__(64 * Few<SM>::kWaves, 1) void gemm_mxfp4_few_kernel(Mxfp4GemmParams p) {
-  constexpr int W = Few<SM>::kWaves, P = Few<SM>::P;
+template <int SM, int W>
+__global__ __launch_bounds__(64 * W, 1) void gemm_mxfp4_few_kernel(Mxfp4GemmParams p) {
+  constexpr int P = SM == 4 ? 4 : 8;
+  static_assert(SM <= W, "a wave adds up a row of subtiles");
   __shared__ v4f red[W][SM][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, h = lane >> 4;
   const int64_t n0 = int64_t(blockIdx.x) * 16;
@@ -530,32 +535,35 @@ __global__ __launch_bounds__(64 * Few<SM>::kWaves, 1) void gemm_mxfp4_few_kernel
   v4f acc[SM];
 #pragma unroll
   for (int i = 0; i < SM; i++) acc[i] = v4f{0.f, 0.f, 0.f, 0.f};
-  for (int k = beg; k < end; k += P) {
-    u32x4 fb[P], fa[P][SM];
-    uint32_t wb[P / 4], wa[P / 4][SM];
+  // units k .. k + U - 1 (a multiple of four); where they may pass the range's end, its last one again, which is not used
+  auto step = [&](auto count, auto past, int k) {
+    constexpr int U = decltype(count)::value;
+    constexpr bool kPast = decltype(past)::value;
+    u32x4 fb[U], fa[U][SM];
+    uint32_t wb[U / 4], wa[U / 4][SM];
 #pragma unroll
-    for (int u = 0; u < P; u++) {  // past the range's end its last step again, which is not used
-      const int64_t at = int64_t(min(k + u, end - 1)) * kUnit;
+    for (int u = 0; u < U; u++) {
+      const int64_t at = int64_t(kPast ? min(k + u, end - 1) : k + u) * kUnit;
       fb[u] = *reinterpret_cast<const u32x4*>(b + at);
 #pragma unroll
       for (int i = 0; i < SM; i++) fa[u][i] = *reinterpret_cast<const u32x4*>(a[i] + at);
     }
 #pragma unroll
-    for (int g = 0; g < P / 4; g++) {
-      const int64_t at = min(k + 4 * g + h, end - 1);
+    for (int g = 0; g < U / 4; g++) {
+      const int64_t at = kPast ? min(k + 4 * g + h, end - 1) : k + 4 * g + h;
       wb[g] = *reinterpret_cast<const uint32_t*>(sb + at * p.sb_sk * 4);
 #pragma unroll
       for (int i = 0; i < SM; i++) wa[g][i] = *reinterpret_cast<const uint32_t*>(sa[i] + at * p.sa_sk * 4);
     }
 #pragma unroll
-    for (int g = 0; g < P / 4; g++) {
+    for (int g = 0; g < U / 4; g++) {
       uint32_t eb[4], ea[SM][4];
       spread(wb[g], eb);
 #pragma unroll
       for (int i = 0; i < SM; i++) spread(wa[g][i], ea[i]);
 #pragma unroll
       for (int u = 0; u < 4; u++) {
-        if (k + 4 * g + u < end) {
+        if (!kPast || k + 4 * g + u < end) {
 #pragma unroll
           for (int i = 0; i < SM; i++)
             acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(fb[4 * g + u]), operand(fa[4 * g + u][i]), acc[i], kFp4, kFp4, 0,
@@ -564,7 +572,11 @@ __global__ __launch_bounds__(64 * Few<SM>::kWaves, 1) void gemm_mxfp4_few_kernel
         }
       }
     }
-  }
+  };
+  int k = beg;
+  for (; k + P <= end; k += P) step(std::integral_constant<int, P>{}, std::false_type{}, k);
+  if (end - k > 4) step(std::integral_constant<int, P>{}, std::true_type{}, k);
+  else if (k < end) step(std::integral_constant<int, 4>{}, std::true_type{}, k);
 #pragma unroll
   for (int i = 0; i < SM; i++) red[wave][i][lane] = acc[i];
   __syncthreads();
@@ -638,6 +650,14 @@ void launch(const Mxfp4GemmParams& p, const DeviceShape& ds, hipStream_t stream)
   hipLaunchKernelGGL((gemm_mxfp4_kernel<C>), dim3(static_cast<unsigned>(grid)), dim3(C::kThreads), 0, stream, p);
 }
 
+template <int W>
+void launch_few(const Mxfp4GemmParams& p, int64_t blocks, hipStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(blocks)), block(64 * W);
+  if (p.M <= 16) hipLaunchKernelGGL((gemm_mxfp4_few_kernel<1, W>), grid, block, 0, stream, p);
+  else if (p.M <= 32) hipLaunchKernelGGL((gemm_mxfp4_few_kernel<2, W>), grid, block, 0, stream, p);
+  else hipLaunchKernelGGL((gemm_mxfp4_few_kernel<4, W>), grid, block, 0, stream, p);
+}
+
 }  // namespace
 
 int64_t mxfp4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) { return shape_of(M, N, K, current_device_shape().cus).ws; }
@@ -651,10 +671,8 @@ int launch_mxfp4_gemm(const Mxfp4GemmParams& p_in, hipStream_t stream) {
   p.splits = s.splits;
   switch (s.kind) {
     case Kind::kFew: {
-      const dim3 grid(static_cast<unsigned>((p.N + 15) / 16));
-      if (p.M <= 16) hipLaunchKernelGGL((gemm_mxfp4_few_kernel<1>), grid, dim3(64 * Few<1>::kWaves), 0, stream, p);
-      else if (p.M <= 32) hipLaunchKernelGGL((gemm_mxfp4_few_kernel<2>), grid, dim3(64 * Few<2>::kWaves), 0, stream, p);
-      else hipLaunchKernelGGL((gemm_mxfp4_few_kernel<4>), grid, dim3(64 * Few<4>::kWaves), 0, stream, p);
+      const int64_t blocks = (p.N + 15) / 16;
+      blocks > ds.cus ? launch_few<4>(p, blocks, stream) : launch_few<8>(p, blocks, stream);
       break;
     }
     case Kind::kLarge: launch<Large>(p, ds, stream); break;
