@@ -1,6 +1,24 @@
 // gemm_mxfp4.hip — Y = A B^T of two matrices of e2m1 codes with one UE8M0 scale per 32 elements of a row
 // (MXFP4), rounded to bf16 once:
 //   Y[m][n] = bf16( sum_k 2^(ea(m, k/32) - 127) A[m][k] * 2^(eb(n, k/32) - 127) B[n][k] )
+//
+// A product of two codes and scales is exact; the sums are the matrix cores' fp32, in the order of K within a range, and
+// the rounding to bf16 is the only other one.
+//
+// Tiles (more than 64 rows). A block owns a tile of 256 x 256, 128 x 128 or 64 x 128 outputs and takes K in steps that four
+// stages of LDS hold, loaded straight there by the asynchronous loads, three steps ahead, so that the matrix cores are fed
+// without a pause also from one tile to the next: blocks are persistent, and the loads run on into the next tile while the
+// last one's outputs are stored. Between the products of a quarter step lie the LDS reads of the next one and the loads' issue.
+// Rows are swizzled in LDS so that no reads collide. The outputs go through LDS, 32 rows x 64 columns of a wave at a
+// time, so that every store writes whole lines (past the caches they are slower).
+//
+// What bounds it. 8192^3, tiles of 256 x 256: 305 us back to back = 3.6 PFLOP/s, 261 in calls with pauses between them (4.2):
+// the clock follows the power (products alone, without loads, reach 6.3 to 6.9 PFLOP/s on random codes and
+// 8.6 to 9.2 on zeros). The loads come next: 31 clocks of a CU for each 1 KB, so that 32
+// of a step's 36 KB take 992 clocks next to 1024 of products. Scale words by 16-byte loads, four in the place of eight of
+// the 40 instructions: 2 to 4 % less on column-major words, but no other layout; not done. 8 waves to a block, or tiles in
+// groups of 2 or 8 rows instead of 4: no faster. 4096^2 x 7168 66 us (3.6 PFLOP/s), 2048 x 4096 x 7168 43 (2.8), 1024 x 4096 x
+// 7168 22 (2.7), 333 x 4104 x 2176 9.2, 1024^3 6.6.
 #include <algorithm>
 #include <type_traits>
 
@@ -14,6 +32,9 @@ typedef float v16f __attribute__((ext_vector_type(16)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+// Outputs, whose rows may begin at any element (vector stores to global memory need no alignment here).
+typedef u32x2 __attribute__((aligned(2))) u32x2_any;
+typedef u32x4 __attribute__((aligned(2))) u32x4_any;
 
 constexpr int kFp4 = 4;     // operand format of the matrix instruction
 constexpr int kStepK = 128;  // K is split, and scale words are counted, in units of 128 elements
@@ -341,7 +362,7 @@ __device__ __forceinline__ void store_tile(uint8_t* lds, int32_t tile, const Com
   uint8_t* const put = lds + (lane & 31) * kOutRow + 8 * (lane >> 5);
   const uint8_t* const get = lds + (lane >> 3) * kOutRow + 16 * (lane & 7);
   uint16_t* row = p->y + (m0 + (lane >> 3)) * ldy + n0 + 8 * (lane & 7);
-  const bool whole = m0 + C::WTM <= p->M && n0 + C::WTN <= p->N && ldy % 8 == 0 && (reinterpret_cast<uintptr_t>(p->y) & 15) == 0;
+  const bool whole = m0 + C::WTM <= p->M && n0 + C::WTN <= p->N;
   const int rows = static_cast<int>(min(p->M - m0, int64_t(C::WTM))) - (lane >> 3);
   const int cols = static_cast<int>(min(p->N - n0, int64_t(C::WTN))) - 8 * (lane & 7);
 #pragma unroll
@@ -361,15 +382,20 @@ __device__ __forceinline__ void store_tile(uint8_t* lds, int32_t tile, const Com
       for (int k = 0; k < 4; k++) w[k] = *reinterpret_cast<const u32x4*>(get + 8 * k * kOutRow);
       if (whole) {
 #pragma unroll
-        for (int k = 0; k < 4; k++) *reinterpret_cast<u32x4*>(row + 8 * k * ldy + 32 * j) = w[k];
+        for (int k = 0; k < 4; k++) *reinterpret_cast<u32x4_any*>(row + 8 * k * ldy + 32 * j) = w[k];
       } else {
         const int left = cols - 32 * j;
 #pragma unroll
         for (int k = 0; k < 4; k++) {
           if (32 * i + 8 * k < rows) {
+            uint16_t* const to = row + 8 * k * ldy + 32 * j;
+            if (left >= 8) {
+              *reinterpret_cast<u32x4_any*>(to) = w[k];
+            } else {
 #pragma unroll
-            for (int q = 0; q < 8; q++)
-              if (q < left) row[8 * k * ldy + 32 * j + q] = static_cast<uint16_t>(w[k][q >> 1] >> (16 * (q & 1)));
+              for (int q = 0; q < 7; q++)
+                if (q < left) to[q] = static_cast<uint16_t>(w[k][q >> 1] >> (16 * (q & 1)));
+            }
           }
         }
       }
@@ -455,15 +481,16 @@ __global__ __launch_bounds__(C::kThreads, C::kBlocks) void gemm_mxfp4_kernel(Mxf
   wait_vmcnt<0>();  // nothing is under way into LDS when the block ends
 }
 
+// 256 x 256 outputs of 4 waves hold 512 registers a lane, with the loop free of scratch; the others leave half of them.
 using Large = Tile<256, 256, 2, 2, 2, 4, 1>;
 using Deep = Tile<128, 128, 2, 2, 4, 4, 1>;
 using Flat = Tile<64, 128, 2, 2, 4, 4, 1>;
 
-// Y = bf16( the splits' sums added in their order ): four columns per thread.
+// Y = bf16( the splits' sums added in their order, so that results do not change from call to call ): four columns per
+// thread.
 constexpr int kMostSplits = 16;
 __global__ __launch_bounds__(256) void gemm_mxfp4_join_kernel(Mxfp4GemmParams p) {
   const int64_t quads = (p.N + 3) / 4, total = p.M * quads, plane = p.M * quads;
-  const bool wide = p.ldy % 4 == 0 && (reinterpret_cast<uintptr_t>(p.y) & 7) == 0;
   for (int64_t t = blockIdx.x * int64_t(256) + threadIdx.x; t < total; t += gridDim.x * int64_t(256)) {
     const v4f* src = reinterpret_cast<const v4f*>(p.ws) + t;
     v4f v[kMostSplits];
@@ -480,11 +507,11 @@ __global__ __launch_bounds__(256) void gemm_mxfp4_join_kernel(Mxfp4GemmParams p)
     const int64_t m = t / quads, n = (t - m * quads) * 4;
     uint16_t* y = p.y + m * p.ldy + n;
     const u32x2 w = {bf16_pair(sum[0], sum[1]), bf16_pair(sum[2], sum[3])};
-    if (wide && n + 4 <= p.N) {
-      *reinterpret_cast<u32x2*>(y) = w;
+    if (n + 4 <= p.N) {
+      *reinterpret_cast<u32x2_any*>(y) = w;
     } else {
 #pragma unroll
-      for (int q = 0; q < 4; q++)
+      for (int q = 0; q < 3; q++)
         if (n + q < p.N) y[q] = static_cast<uint16_t>(w[q >> 1] >> (16 * (q & 1)));
     }
   }
@@ -592,11 +619,11 @@ __global__ __launch_bounds__(64 * W, 1) void gemm_mxfp4_few_kernel(Mxfp4GemmPara
   if (m >= p.M) return;
   uint16_t* y = p.y + m * p.ldy + n;
   const u32x2 w = {bf16_pair(sum[0], sum[1]), bf16_pair(sum[2], sum[3])};
-  if (n + 4 <= p.N && (reinterpret_cast<uintptr_t>(y) & 7) == 0) {
-    *reinterpret_cast<u32x2*>(y) = w;
+  if (n + 4 <= p.N) {
+    *reinterpret_cast<u32x2_any*>(y) = w;
   } else {
 #pragma unroll
-    for (int q = 0; q < 4; q++)
+    for (int q = 0; q < 3; q++)
       if (n + q < p.N) y[q] = static_cast<uint16_t>(w[q >> 1] >> (16 * (q & 1)));
   }
 }
@@ -613,7 +640,17 @@ int64_t tiles_of(int64_t M, int64_t N, int bm, int bn) { return ((M + bm - 1) / 
 
 // Up to 64 rows take the kernel without LDS staging. Above, the tile and the ranges of K with the least estimated time:
 // rounds of tiles over the CUs, each its steps of 256 elements and a fixed part. Splitting adds a launch and the partial
-// sums' way to memory and back.
+// sums' way to memory and back. us, and each kernel where it was forced (* with K split, where that was the better):
+//   M x N x K             chosen   256 x 256   128 x 128   64 x 128
+//   8192 x 8192 x 8192     305       308         379         503
+//   4096 x 4096 x 7168      66        66          77         106
+//   2048 x 4096 x 7168      43        54          43          57
+//   1024 x 4096 x 7168      22.6      44.7        22.3        28.0
+//   512 x 4096 x 7168       16.8      43.4        19.3        15.9 *
+//   128 x 4096 x 7168       15.7      41.5        17.3 *      14.6 (split 15.3)
+//   65 x 4096 x 7168        13.7      44.7        15.2 *      14.0 * (64 rows 11.3)
+//   333 x 4104 x 2176        9.2      24.6        11.2         9.2
+//   300 x 300 x 8192        10.8      55.1        11.9 *      10.9 * (17.0 unsplit)
 Shape shape_of(int64_t M, int64_t N, int64_t K, int cus) {
   if (M <= 64) return {Kind::kFew, 1, 0};
   struct Model {
