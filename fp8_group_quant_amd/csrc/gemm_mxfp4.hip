@@ -12,13 +12,13 @@
 // Rows are swizzled in LDS so that no reads collide. The outputs go through LDS, 32 rows x 64 columns of a wave at a
 // time, so that every store writes whole lines (past the caches they are slower).
 //
-// What bounds it. 8192^3, tiles of 256 x 256: 305 us back to back = 3.6 PFLOP/s, 261 in calls with pauses between them (4.2):
-// the clock follows the power (products alone, without loads, reach 6.3 to 6.9 PFLOP/s on random codes and
-// 8.6 to 9.2 on zeros). The loads come next: 31 clocks of a CU for each 1 KB, so that 32
-// of a step's 36 KB take 992 clocks next to 1024 of products. Scale words by 16-byte loads, four in the place of eight of
-// the 40 instructions: 2 to 4 % less on column-major words, but no other layout; not done. 8 waves to a block, or tiles in
-// groups of 2 or 8 rows instead of 4: no faster. 4096^2 x 7168 66 us (3.6 PFLOP/s), 2048 x 4096 x 7168 43 (2.8), 1024 x 4096 x
-// 7168 22 (2.7), 333 x 4104 x 2176 9.2, 1024^3 6.6.
+// What bounds it. 8192^3, tiles of 256 x 256: 280 to 305 us back to back (by the box; 3.6 to 3.9 PFLOP/s), 257 in calls with
+// pauses between them. The matrix pipe is busy in 58 % of the cycles of a clock that the power holds at 1.7 GHz (products
+// alone, without loads, reach 6.3 to 6.9 PFLOP/s on random codes and 8.6 to 9.2 on zeros). The loads come next: 31
+// clocks of a CU for each 1 KB, so that 32 of a step's 36 KB take 992 clocks next to 1024 of products. Scale words by
+// 16-byte loads, four in the place of eight of the 40 instructions: 2 to 4 % less on column-major words, but no other
+// layout; not done. 8 waves to a block, or tiles in groups of 2 or 8 rows instead of 4: no faster. 4096^2 x 7168 66 us (3.6
+// PFLOP/s), 2048 x 4096 x 7168 43 (2.8), 1024 x 4096 x 7168 22.5 (2.7), 333 x 4104 x 2176 9.1, 1024^3 6.6.
 #include <algorithm>
 #include <type_traits>
 
@@ -639,27 +639,32 @@ struct Shape {
 int64_t tiles_of(int64_t M, int64_t N, int bm, int bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); }
 
 // Up to 64 rows take the kernel without LDS staging. Above, the tile and the ranges of K with the least estimated time:
-// rounds of tiles over the CUs, each its steps of 256 elements and a fixed part. Splitting adds a launch and the partial
-// sums' way to memory and back. us, and each kernel where it was forced (* with K split, where that was the better):
-//   M x N x K             chosen   256 x 256   128 x 128   64 x 128
-//   8192 x 8192 x 8192     305       308         379         503
-//   4096 x 4096 x 7168      66        66          77         106
-//   2048 x 4096 x 7168      43        54          43          57
-//   1024 x 4096 x 7168      22.6      44.7        22.3        28.0
-//   512 x 4096 x 7168       16.8      43.4        19.3        15.9 *
-//   128 x 4096 x 7168       15.7      41.5        17.3 *      14.6 (split 15.3)
-//   65 x 4096 x 7168        13.7      44.7        15.2 *      14.0 * (64 rows 11.3)
-//   333 x 4104 x 2176        9.2      24.6        11.2         9.2
-//   300 x 300 x 8192        10.8      55.1        11.9 *      10.9 * (17.0 unsplit)
+// rounds of tiles over the CUs, each its steps of 256 elements and a part for its outputs, and a part for the call. Splitting
+// adds a launch and the partial sums' way to memory and back. us, each kernel where it was forced (* with K split, where that was
+// the better), the chosen one marked:
+//   M x N x K             256 x 256   128 x 128   64 x 128
+//   8192 x 8192 x 8192    > 308          379         503
+//   4096 x 4096 x 7168    >  66           77         106
+//   2048 x 8192 x 2048    >  28.8         32.9        40.6
+//   2048 x 4096 x 7168       54        >  43          57
+//   1024 x 4096 x 7168       44.7      >  22.3        28.0
+//   3000 x 3000 x  512       18.9      >  14.7        16.0
+//   1993 x 5920 x  256       19.2      >  15.0        17.5
+//    512 x 4096 x 7168       43.4         19.3      > 15.9
+//    128 x 4096 x 7168       41.5         17.3 *    > 14.6 (split 15.3)
+//     65 x 4096 x 7168       44.7         15.2 *    > 14.0 * (64 rows, without staging, 11.3)
+//    333 x 4104 x 2176       24.6         11.2      >  9.2
+//    300 x  300 x 8192       55.1         11.9 *    > 10.9 * (17.0 unsplit)
 Shape shape_of(int64_t M, int64_t N, int64_t K, int cus) {
   if (M <= 64) return {Kind::kFew, 1, 0};
   struct Model {
     Kind kind;
     int bm, bn;
-    double step, fixed;  // us
+    double step, round, call;  // us
     bool split;
   };
-  constexpr Model kModels[] = {{Kind::kLarge, 256, 256, 2.2, 6.0, false}, {Kind::kDeep, 128, 128, 0.70, 2.5, true}, {Kind::kFlat, 64, 128, 0.46, 2.0, true}};
+  constexpr Model kModels[] = {{Kind::kLarge, 256, 256, 1.85, 7.0, 7.0, false}, {Kind::kDeep, 128, 128, 0.58, 2.5, 4.0, true},
+                               {Kind::kFlat, 64, 128, 0.38, 2.0, 4.0, true}};
   const double steps = static_cast<double>(K) / 256;
   const int64_t n4 = (N + 3) / 4 * 4;
   Shape best{Kind::kLarge, 1, 0};
@@ -669,7 +674,7 @@ Shape shape_of(int64_t M, int64_t N, int64_t K, int cus) {
     const int64_t most = m.split ? std::max<int64_t>(1, std::min<int64_t>({cus / tiles, K / 1024, kMostSplits})) : 1;
     for (int64_t s = 1; s <= most; s++) {
       const double rounds = static_cast<double>((tiles * s + cus - 1) / cus), bytes = static_cast<double>(s * M * n4 * 4);
-      const double time = rounds * (steps / s * m.step + m.fixed) + (s > 1 ? 4.0 + 2 * bytes / 3e6 : 0.0);
+      const double time = m.call + rounds * (steps / s * m.step + m.round) + (s > 1 ? 4.0 + 2 * bytes / 3e6 : 0.0);
       if (time < least) {
         least = time;
         best = {m.kind, static_cast<int>(s), s > 1 ? s * M * n4 * 4 : 0};
