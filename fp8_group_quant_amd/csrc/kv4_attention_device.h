@@ -914,7 +914,7 @@ __global__ __launch_bounds__(64 * WAVES, waves_per_simd(D, DT, N)) void kv4_atte
 // ahead of its use (529 us for 2 x 2048 queries over 8192 tokens when the compiler placed the reads,
 // 484 so), and a step's 64 tokens take one page lookup where a page holds them (435).
 // Waves per SIMD that the registers are kept to (fp16, D = 128, 64 rows: 452 us at 3, 468 at 2, for 2 x
-// 1024 queries of 32 heads over 8192 tokens; bf16, D = 64, 128 rows: 353 and 388 for 2 x 2048). Up to 17
+// 1024 queries of 32 heads over 8192 tokens; bf16, D = 64, 128 rows: 353 and 388 for 2 x 2048). Up to 24
 // registers then go through memory: in fp16 at D = 128 and 256 with one page lookup per step or per token, in bf16
 // with one per token.
 constexpr int wide_waves_per_simd(int D, int DT, int QT, bool split) {
