@@ -286,3 +286,81 @@ def test_one_page_for_two_sequences():
     mask = torch.tensor([[1], [3], [5]] * 2, dtype=torch.int32).cuda()
     for out in (f.kv4_window_attention(q, c, table, kv, 0.1, 50, 2, ip), f.kv4_tree_attention(q, c, table, kv, 0.1, mask, ip)):
         assert torch.equal(out[:3], out[3:])
+
+
+def test_calls_of_several_threads():
+    """Host threads with a stream each, all of whose calls are under way at once."""
+    import threading
+    makes = [lambda: Layer(1, 130), lambda: Layer(2, 40), lambda: Step(3, 2, 5), lambda: Step(4, 30, 1)]
+    works, twins = [m() for m in makes], [m() for m in makes]
+    wants = []
+    for t in twins:
+        t.run()
+        torch.cuda.synchronize()
+        wants.append(t.results())
+    torch.cuda.synchronize()
+    got, errors = [None] * len(works), []
+
+    def go(i):
+        try:
+            st = torch.cuda.Stream()
+            with torch.cuda.stream(st):
+                for _ in range(10):
+                    works[i].run()
+                got[i] = works[i].results()
+            st.synchronize()
+        except Exception as e:  # noqa: BLE001 (the test reports it)
+            errors.append(e)
+
+    threads = [threading.Thread(target=go, args=(i,)) for i in range(len(works))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    for g, want in zip(got, wants):
+        assert equal(g, want)
+
+
+# ------------------------------------------------------------------ nothing to do
+def test_empty_calls():
+    f = fq()
+    i32 = dict(dtype=torch.int32, device="cuda")
+    q, s = f.mxfp4_quant(torch.empty(0, 256, dtype=torch.bfloat16, device="cuda"))
+    assert q.shape == (0, 128) and f.mxfp4_dequant(q, s).shape == (0, 256)
+    b, sb = f.mxfp4_quant(torch.randn(5, 256, device="cuda"))
+    f.fp8q_gemm_mxfp4(q, s, b, sb, torch.empty(0, 5, dtype=torch.bfloat16, device="cuda"))
+    y = torch.full((5, 3), 77.0, dtype=torch.bfloat16, device="cuda")
+    f.fp8q_gemm_mxfp4(b, sb, q, s, y[:, :0])
+    assert bool((y == 77).all())
+    c = f.alloc_kv4_cache(4, 16, 2, 64)
+    none = torch.empty(0, 4, 64, dtype=torch.bfloat16, device="cuda")
+    for lens, ip in ((torch.zeros(0, **i32), torch.zeros(1, **i32)), (torch.full((3,), 9, **i32), torch.zeros(4, **i32))):
+        table = torch.zeros(lens.numel(), 2, **i32)
+        assert f.kv4_window_attention(none, c, table, lens, 0.1, 5, 1, ip).shape == none.shape
+        assert f.kv4_tree_attention(none, c, table, lens, 0.1, torch.empty(0, 1, **i32), ip).shape == none.shape
+    # queries of sequences without cached tokens, and a table without columns
+    q = torch.randn(3, 4, 64, dtype=torch.bfloat16, device="cuda")
+    for table in (torch.zeros(3, 2, **i32), torch.zeros(3, 0, **i32)):
+        for o in (f.kv4_window_attention(q, c, table, torch.zeros(3, **i32), 0.1, 5, 1),
+                  f.kv4_tree_attention(q, c, table, torch.zeros(3, **i32), 0.1, torch.full((3, 1), -1, **i32))):
+            assert bool((o == 0).all())
+
+
+@pytest.mark.parametrize("M,N", [(7, 40), (40, 90), (130, 300), (300, 600)])
+def test_a_scale_of_nan_reaches_its_row_alone(M, N):
+    f = fq()
+    K = 640
+    a, sa = f.mxfp4_quant(torch.randn(M, K, generator=gen(1)).cuda(), "ue8m0", "row")
+    b, sb = f.mxfp4_quant(torch.randn(N, K, generator=gen(2)).cuda(), "ue8m0", "row")
+    want = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    f.fp8q_gemm_mxfp4(a, sa, b, sb, want)
+    sa, sb = sa.clone(), sb.clone()
+    sa[M - 2, 3] = 255
+    sb[N // 2, 19] = 255
+    y = torch.empty_like(want)
+    f.fp8q_gemm_mxfp4(a, sa, b, sb, y)
+    bad = torch.zeros(M, N, dtype=torch.bool, device="cuda")
+    bad[M - 2] = True
+    bad[:, N // 2] = True
+    assert torch.equal(torch.isnan(y), bad) and torch.equal(y[~bad], want[~bad])
