@@ -276,6 +276,7 @@ def _u8(t: torch.Tensor) -> torch.Tensor:
 
 
 _WS_SIZES: dict = {}
+_MXFP4_WS_SIZES: dict = {}
 
 
 def _allocating_on(stream, device):
@@ -431,8 +432,9 @@ def _mxfp4_rows(entry: str, x, q, s, width, stream) -> None:
     if dt is None or x.dim() != 2 or q.dim() != 2 or s.dim() != 2:
         raise ValueError("x (bf16, fp16 or fp32), q and s must be 2-D tensors")
     M = x.shape[0]
-    K = 2 * q.shape[1]
-    if q.element_size() != 1 or q.shape[0] != M or width != K:
+    rows, K = q.shape
+    K *= 2
+    if q.element_size() != 1 or rows != M or width != K:
         raise ValueError(f"q has shape {tuple(q.shape)} of {q.dtype}, expected bytes of {(M, width // 2)}")
     x_sm, x_in = x.stride()
     q_sm, q_in = q.stride()
@@ -521,13 +523,17 @@ def fp8q_gemm_mxfp4(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torc
     if not 0 <= a.get_device() == b.get_device() == y.get_device() == sa.get_device() == sb.get_device() \
             or (workspace is not None and workspace.get_device() != a.get_device()):
         raise ValueError(_ELSEWHERE)
-    handle = _stream_on(stream, a.get_device())
-    lib = load_library()
+    dev = a.get_device()
+    handle = _stream_on(stream, dev)
     if workspace is None:
-        workspace = _alloc_workspace(lib.fp8q_gemm_mxfp4_workspace_size(M, N, K), a.device, stream)
+        size = _MXFP4_WS_SIZES.get((dev, M, N, K))
+        if size is None:
+            size = _MXFP4_WS_SIZES[dev, M, N, K] = fp8q_gemm_mxfp4_workspace_size(M, N, K)
+        if size > 0:
+            workspace = _alloc_workspace(size, a.device, stream)
     sa_sm, sa_sk = sa.stride()
     sb_sn, sb_sk = sb.stride()
-    _check(lib.fp8q_gemm_mxfp4(a.data_ptr(), lda, sa.data_ptr(), fa, sa_sm, sa_sk, b.data_ptr(), ldb, sb.data_ptr(), fb, sb_sn,
+    _check(load_library().fp8q_gemm_mxfp4(a.data_ptr(), lda, sa.data_ptr(), fa, sa_sm, sa_sk, b.data_ptr(), ldb, sb.data_ptr(), fb, sb_sn,
                                sb_sk, y.data_ptr(), ldy, M, N, K, None if workspace is None else workspace.data_ptr(),
                                0 if workspace is None else workspace.numel() * workspace.element_size(), handle))
 
@@ -848,9 +854,10 @@ def fp8q_kv4_plan(kv_lens: torch.Tensor, q_lens: torch.Tensor, free_pages: torch
         raise ValueError("expected q_lens and new_lens [B], block_table [B, max_pages], q_indptr [B + 1], positions [T] "
                          "and pages_taken [1]")
     table_sb, table_in = block_table.stride()
-    if (table_in != 1 and max_pages > 1) or (B > 1 and not 1 == kv_lens.stride(0) == q_lens.stride(0) == new_lens.stride(0)) \
-            or (B > 0 and q_indptr.stride(0) != 1) or (T > 1 and slots.stride(0) != 1) \
-            or (F > 1 and free_pages.stride(0) != 1) or (positions is not None and T > 1 and positions.stride(0) != 1):
+    if (table_in != 1 and max_pages > 1) or not (
+            kv_lens.is_contiguous() and q_lens.is_contiguous() and new_lens.is_contiguous() and q_indptr.is_contiguous()
+            and slots.is_contiguous() and free_pages.is_contiguous()
+            and (positions is None or positions.is_contiguous())):
         raise ValueError("every tensor must be contiguous (block_table: its rows)")
     _check(load_library().fp8q_kv4_plan(
         kv_lens.data_ptr(), q_lens.data_ptr(), B, free_pages.data_ptr(), F, block_table.data_ptr(), table_sb, max_pages, pages,
