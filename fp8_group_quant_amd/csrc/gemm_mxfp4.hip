@@ -12,10 +12,10 @@
 // Rows are swizzled in LDS so that no reads collide. The outputs go through LDS, 32 rows x 64 columns of a wave at a
 // time, so that every store writes whole lines (past the caches they are slower).
 //
-// What bounds it. 8192^3, tiles of 256 x 256: 280 to 305 us back to back (by the box; 3.6 to 3.9 PFLOP/s), 257 in calls with
+// What bounds it. 8192^3, tiles of 256 x 256: 280 to 305 us back to back (by the card; 3.6 to 3.9 PFLOP/s), 257 in calls with
 // pauses between them. The matrix pipe is busy in 58 % of the cycles of a clock that the power holds at 1.7 GHz (products
 // alone, without loads, reach 6.3 to 6.9 PFLOP/s on random codes and 8.6 to 9.2 on zeros). The loads come next: 31
-// clocks of a CU for each 1 KB, so that 32 of a step's 36 KB take 992 clocks next to 1024 of products. Scale words by
+// clocks of a CU for each 1 KB, so that 32 of a step's 34 KB take 992 clocks next to 1024 of products. Scale words by
 // 16-byte loads, four in the place of eight of the 40 instructions: 2 to 4 % less on column-major words, but no other
 // layout; not done. 8 waves to a block, or tiles in groups of 2 or 8 rows instead of 4: no faster. 4096^2 x 7168 66 us (3.6
 // PFLOP/s), 2048 x 4096 x 7168 43 (2.8), 1024 x 4096 x 7168 22.5 (2.7), 333 x 4104 x 2176 9.1, 1024^3 6.6.
