@@ -5,7 +5,7 @@
 // A product of two codes and scales is exact; the sums are the matrix cores' fp32, in the order of K within a range, and
 // the rounding to bf16 is the only other one.
 //
-// Tiles (more than 64 rows). A block owns a tile of 256 x 256, 128 x 128 or 64 x 128 outputs and takes K in steps that four
+// Tiles. A block owns a tile of 256 x 256, 128 x 128 or 64 x 128 outputs and takes K in steps that four
 // stages of LDS hold, loaded straight there by the asynchronous loads, three steps ahead, so that the matrix cores are fed
 // without a pause also from one tile to the next: blocks are persistent, and the loads run on into the next tile while the
 // last one's outputs are stored. Between the products of a quarter step lie the LDS reads of the next one and the loads' issue.
@@ -638,10 +638,10 @@ struct Shape {
 
 int64_t tiles_of(int64_t M, int64_t N, int bm, int bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); }
 
-// Up to 64 rows take the kernel without LDS staging. Above, the tile and the ranges of K with the least estimated time:
-// rounds of tiles over the CUs, each its steps of 256 elements and a part for its outputs, and a part for the call. Splitting
-// adds a launch and the partial sums' way to memory and back. us, each kernel where it was forced (* with K split, where that was
-// the better), the chosen one marked:
+// The kernel, tile and ranges of K with the least estimated time: rounds of tiles over the CUs, each its steps of 256
+// elements and a part for its outputs, and a part for the call; not less than the bytes take. Splitting adds a launch and
+// the partial sums' way to memory and back. us, each kernel where it was forced (* with K split, where that was the
+// better), the chosen one marked:
 //   M x N x K             256 x 256   128 x 128   64 x 128
 //   8192 x 8192 x 8192    > 308          379         503
 //   4096 x 4096 x 7168    >  66           77         106
@@ -652,30 +652,41 @@ int64_t tiles_of(int64_t M, int64_t N, int bm, int bn) { return ((M + bm - 1) / 
 //   1993 x 5920 x  256       19.2      >  15.0        17.5
 //    512 x 4096 x 7168       43.4         19.3      > 15.9
 //    128 x 4096 x 7168       41.5         17.3 *    > 14.6 (split 15.3)
-//     65 x 4096 x 7168       44.7         15.2 *    > 14.0 * (64 rows, without staging, 11.3)
+//     65 x 4096 x 7168       44.7         15.2 *    > 14.0 *
 //    333 x 4104 x 2176       24.6         11.2      >  9.2
 //    300 x  300 x 8192       55.1         11.9 *    > 10.9 * (17.0 unsplit)
+// Up to 64 rows, without staging and with tiles of 64 x 128: B goes through the registers of every 16 rows, which is
+// the shorter way while there are few of them or few rounds.
+//   64 x  4096 x 7168   > 11.7   13.9 *      32 x  4096 x 7168   >  7.9   12.7 *
+//   64 x  8192 x 8192     24.1 > 18.5 *      32 x 14336 x 4096     14.0 > 11.3
+//   64 x 14336 x 4096     22.5 > 11.7        32 x 28672 x 8192     51.1 > 33.3
+//   64 x 28672 x 8192     81.9 > 33.8        16 x 28672 x 8192     37.5 > 31.7
+//   64 x  2048 x 4096   >  7.4   10.5 *      16 x  8192 x 8192   > 12.1   14.6 *
 Shape shape_of(int64_t M, int64_t N, int64_t K, int cus) {
-  if (M <= 64) return {Kind::kFew, 1, 0};
   struct Model {
     Kind kind;
     int bm, bn;
     double step, round, call;  // us
     bool split;
   };
-  constexpr Model kModels[] = {{Kind::kLarge, 256, 256, 1.85, 7.0, 7.0, false}, {Kind::kDeep, 128, 128, 0.58, 2.5, 4.0, true},
-                               {Kind::kFlat, 64, 128, 0.38, 2.0, 4.0, true}};
+  const Model models[] = {{Kind::kFew, 64, 16, M <= 16 ? 0.08 + 0.003 * M : M <= 32 ? 0.165 : 0.30, 0.4, 3.4, false},
+                          {Kind::kLarge, 256, 256, 1.85, 7.0, 7.0, false},
+                          {Kind::kDeep, 128, 128, 0.58, 2.5, 4.0, true},
+                          {Kind::kFlat, 64, 128, 0.38, 2.0, 4.0, true}};
   const double steps = static_cast<double>(K) / 256;
+  const double least_time = 4.0 + (static_cast<double>(M + N) * K * 17 / 32 + 2.0 * M * N) / 4.5e6;
   const int64_t n4 = (N + 3) / 4 * 4;
   Shape best{Kind::kLarge, 1, 0};
   double least = 1e300;
-  for (const Model& m : kModels) {
+  for (const Model& m : models) {
+    if (m.kind == Kind::kFew && M > m.bm) continue;
     const int64_t tiles = tiles_of(M, N, m.bm, m.bn);
     const int64_t most = m.split ? std::max<int64_t>(1, std::min<int64_t>({cus / tiles, K / 1024, kMostSplits})) : 1;
     for (int64_t s = 1; s <= most; s++) {
       const double rounds = static_cast<double>((tiles * s + cus - 1) / cus), bytes = static_cast<double>(s * M * n4 * 4);
-      const double time = m.call + rounds * (steps / s * m.step + m.round) + (s > 1 ? 4.0 + 2 * bytes / 3e6 : 0.0);
-      if (time < least) {
+      const double join = s > 1 ? 4.0 + 2 * bytes / 3e6 : 0.0;
+      const double time = std::max(m.call + rounds * (steps / s * m.step + m.round) + join, least_time);
+      if (time < least || (time == least && m.kind == best.kind)) {  // (of equal ones the most ranges: more CUs load)
         least = time;
         best = {m.kind, static_cast<int>(s), s > 1 ? s * M * n4 * 4 : 0};
       }
