@@ -78,13 +78,16 @@ __device__ __forceinline__ uint32_t lds_addr(const void* p) {
   return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((const lds_u8*)p));
 }
 typedef int v4i __attribute__((ext_vector_type(4)));
+// A load to LDS that reads M0 needs a wait state after the scalar instruction that writes it; in an asm statement the
+// compiler puts none.
 // lane l: LDS [lds + 16 l, + 16) <- buffer [voff, + 16), all of the offset in the register that the bounds check looks at
 __device__ __forceinline__ void dma16(uint32_t lds, v4i buffer, uint32_t voff) {
-  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(voff), "s"(buffer) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(voff), "s"(buffer)
+               : "memory", "m0");
 }
 // lane l: LDS [lds + 4 l, + 4) <- global [base + voff, + 4)
 __device__ __forceinline__ void dma4(uint32_t lds, const uint8_t* base, uint32_t voff) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(voff), "s"(base) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(voff), "s"(base) : "memory", "m0");
 }
 template <int N>
 __device__ __forceinline__ void wait_vmcnt() {
