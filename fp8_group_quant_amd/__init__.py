@@ -11,6 +11,9 @@ report section "实现拆解" item 2), as do rms_norm_group_quant(), mxfp4_quant
 kv4_read(), kv4_attention(), kv4_window_attention(), kv4_tree_attention() and kv4_plan();
 alloc_kv4_cache() allocates a cache.
 
+The 4-bit products, the page plan and the attention run on their tensors' GPU, whichever is current; the other
+calls on the current one.
+
 There is no fallback: if libfp8q.so is missing or the device is not a gfx950, calls
 raise.
 """
@@ -137,16 +140,12 @@ def _stream(stream) -> int:
     return int(stream)
 
 
-def _stream_on(stream, device: int) -> int:
-    """The stream's handle, for a call whose tensors are on GPU `device`: kernels run on the current one."""
-    if stream is None:
-        current = torch._C._cuda_getDevice()
-        if current != device:
-            raise ValueError("the tensors must be on the current GPU")
-        return torch._C._cuda_getCurrentRawStream(current)
-    if torch.cuda.is_initialized() and torch._C._cuda_getDevice() != device:
-        raise ValueError("the tensors must be on the current GPU")
-    return _stream(stream)
+def _other_gpu(device: int, stream) -> bool:
+    """Whether GPU `device`, which holds a call's tensors, is not the current one: kernels, their shapes and the
+    default stream go by that, so the call makes it current. (A stream's handle does not say whose it is.)"""
+    if isinstance(stream, torch.cuda.Stream) and stream.device_index != device:
+        raise ValueError("the stream must be one of the tensors' GPU")
+    return (stream is None or torch.cuda.is_initialized()) and torch._C._cuda_getDevice() != device
 
 
 def _ptr(t: torch.Tensor | None) -> int | None:
@@ -445,13 +444,16 @@ def _mxfp4_rows(entry: str, x, q, s, width, stream) -> None:
         raise ValueError(f"s has shape {tuple(s.shape)} of {s.dtype}, expected a scale per 32 of {(M, K)} elements")
     if not 0 <= x.get_device() == q.get_device() == s.get_device():
         raise ValueError(_ELSEWHERE)
+    if _other_gpu(x.get_device(), stream):
+        with torch.cuda.device(x.get_device()):
+            return _mxfp4_rows(entry, x, q, s, width, stream)
     s_sm, s_sg = s.stride()
     if entry == "fp8q_mxfp4_dequant":
         _check(load_library().fp8q_mxfp4_dequant(q.data_ptr(), q_sm, s.data_ptr(), fmt, s_sm, s_sg, x.data_ptr(), dt, M, K,
-                                                 x_sm, _stream_on(stream, x.get_device())))
+                                                 x_sm, _stream(stream)))
     else:
         _check(getattr(load_library(), entry)(x.data_ptr(), dt, M, K, x_sm, q.data_ptr(), q_sm, s.data_ptr(), fmt, s_sm, s_sg,
-                                              _stream_on(stream, x.get_device())))
+                                              _stream(stream)))
 
 
 def fp8q_mxfp4_quant(x: torch.Tensor, q: torch.Tensor, s: torch.Tensor, stream=None) -> None:
@@ -524,7 +526,10 @@ def fp8q_gemm_mxfp4(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torc
             or (workspace is not None and workspace.get_device() != a.get_device()):
         raise ValueError(_ELSEWHERE)
     dev = a.get_device()
-    handle = _stream_on(stream, dev)
+    if _other_gpu(dev, stream):
+        with torch.cuda.device(dev):
+            return fp8q_gemm_mxfp4(a, sa, b, sb, y, stream, workspace)
+    handle = _stream(stream)
     if workspace is None:
         size = _MXFP4_WS_SIZES.get((dev, M, N, K))
         if size is None:
@@ -729,7 +734,11 @@ def _kv4_attend(entry: str, sizes: tuple, extra: tuple, q, cache, block_table, k
             or (lse is not None and lse.get_device() != q.get_device()) \
             or (workspace is not None and workspace.get_device() != q.get_device()):
         raise ValueError(_ELSEWHERE)
-    handle = _stream_on(stream, q.get_device())
+    if _other_gpu(q.get_device(), stream):
+        with torch.cuda.device(q.get_device()):
+            return _kv4_attend(entry, sizes, extra, q, cache, block_table, kv_lens, out, sm_scale, q_indptr, lse, stream,
+                               workspace)
+    handle = _stream(stream)
     lib = load_library()
     if workspace is None:
         workspace = _alloc_workspace(getattr(lib, entry + "_workspace_size")(dt, B, T, H, kv_heads, D, max_pages * page, *sizes), q.device, stream)
@@ -844,6 +853,10 @@ def fp8q_kv4_plan(kv_lens: torch.Tensor, q_lens: torch.Tensor, free_pages: torch
             == q_indptr.get_device() == slots.get_device() == pages_taken.get_device() \
             or (positions is not None and positions.get_device() != dev):
         raise ValueError(_ELSEWHERE)
+    if _other_gpu(dev, stream):
+        with torch.cuda.device(dev):
+            return fp8q_kv4_plan(kv_lens, q_lens, free_pages, block_table, pages, page_size, new_lens, q_indptr, slots,
+                                 pages_taken, positions, stream)
     shape = kv_lens.shape
     if len(shape) != 1 or block_table.dim() != 2 or slots.dim() != 1 or free_pages.dim() != 1:
         raise ValueError("kv_lens, slots and free_pages must be 1-D, block_table 2-D")
@@ -862,7 +875,7 @@ def fp8q_kv4_plan(kv_lens: torch.Tensor, q_lens: torch.Tensor, free_pages: torch
     _check(load_library().fp8q_kv4_plan(
         kv_lens.data_ptr(), q_lens.data_ptr(), B, free_pages.data_ptr(), F, block_table.data_ptr(), table_sb, max_pages, pages,
         page_size, new_lens.data_ptr(), q_indptr.data_ptr(), slots.data_ptr(),
-        None if positions is None else positions.data_ptr(), T, pages_taken.data_ptr(), _stream_on(stream, dev)))
+        None if positions is None else positions.data_ptr(), T, pages_taken.data_ptr(), _stream(stream)))
 
 
 class Kv4Plan(NamedTuple):
