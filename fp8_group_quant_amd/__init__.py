@@ -21,6 +21,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 from typing import NamedTuple
 
@@ -274,10 +275,6 @@ def _u8(t: torch.Tensor) -> torch.Tensor:
     return t.view(torch.uint8) if t.dtype != torch.uint8 else t
 
 
-_WS_SIZES: dict = {}
-_MXFP4_WS_SIZES: dict = {}
-
-
 def _allocating_on(stream, device):
     """Context in which torch allocates on the stream that the kernels run on, so that the caching
     allocator hands the blocks to no other stream's work before they finish."""
@@ -298,10 +295,18 @@ def _alloc_workspace(nbytes: int, device, stream) -> torch.Tensor | None:
 def fp8q_gemm_workspace_size(M: int, N: int, K: int, mode: int = GEMM_BLOCK128) -> int:
     """Bytes of workspace with which fp8q_gemm_blockscaled_ws takes its split-K path for this
     shape on the current device (0: none needed)."""
-    key = (torch.cuda.current_device(), M, N, K, mode)
-    if key not in _WS_SIZES:
-        _WS_SIZES[key] = int(load_library().fp8q_gemm_workspace_size(M, N, K, mode))
-    return _WS_SIZES[key]
+    return _gemm_workspace_size(torch.cuda.current_device(), M, N, K, mode)
+
+
+# A size depends on the shape and the device alone. A server's M takes many values: the least recently used go.
+@functools.lru_cache(maxsize=8192)
+def _gemm_workspace_size(device: int, M: int, N: int, K: int, mode: int) -> int:
+    return int(load_library().fp8q_gemm_workspace_size(M, N, K, mode))
+
+
+@functools.lru_cache(maxsize=8192)
+def _gemm_mxfp4_workspace_size(device: int, M: int, N: int, K: int) -> int:
+    return int(load_library().fp8q_gemm_mxfp4_workspace_size(M, N, K))
 
 
 def fp8q_gemm_blockscaled(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torch.Tensor,
@@ -531,9 +536,7 @@ def fp8q_gemm_mxfp4(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torc
             return fp8q_gemm_mxfp4(a, sa, b, sb, y, stream, workspace)
     handle = _stream(stream)
     if workspace is None:
-        size = _MXFP4_WS_SIZES.get((dev, M, N, K))
-        if size is None:
-            size = _MXFP4_WS_SIZES[dev, M, N, K] = fp8q_gemm_mxfp4_workspace_size(M, N, K)
+        size = _gemm_mxfp4_workspace_size(dev, M, N, K)
         if size > 0:
             workspace = _alloc_workspace(size, a.device, stream)
     sa_sm, sa_sk = sa.stride()
