@@ -88,17 +88,26 @@ int gemm_entry(const uint8_t* a, int64_t lda, const void* sa, int sa_fmt, int64_
     return fail(FP8Q_EINVAL, pre + "negative stride");
   if (workspace_bytes < 0) return fail(FP8Q_EINVAL, pre + "negative workspace size");
   if (!aligned(workspace, 16)) return fail(FP8Q_EALIGN, pre + "workspace must be 16-byte aligned");
-  if (M == 0 || N == 0 || K == 0) return FP8Q_OK;
-  if (!a || !b || !y || !sa || !sb) return fail(FP8Q_EINVAL, pre + "null tensor pointer");
+  if (M == 0 || N == 0 || (K == 0 && !y)) return FP8Q_OK;
+  if (!y || (K > 0 && (!a || !b || !sa || !sb))) return fail(FP8Q_EINVAL, pre + "null tensor pointer");
   if ((M > 1 && lda < K / 2) || (N > 1 && ldb < K / 2)) return fail(FP8Q_EINVAL, pre + "lda and ldb must be >= K / 2");
   if (M > 1 && ldy < N) return fail(FP8Q_EINVAL, pre + "ldy must be >= N (rows of y overlap)");
+  if (!aligned(y, 2)) return fail(FP8Q_EALIGN, pre + "y must be 2-byte aligned");
+  Mxfp4GemmParams p{};
+  p.y = y;
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.ldy = ldy;
+  if (K == 0) {  // sums of nothing
+    const int rc = check_current_device();
+    return rc != FP8Q_OK ? rc : launch_mxfp4_zero(p, static_cast<hipStream_t>(stream));
+  }
   // (a tile's rows lie within 32 bits of its first one)
   if ((M > 1 && lda >= kMostStride) || (N > 1 && ldb >= kMostStride))
     return fail(FP8Q_EUNSUPPORTED, pre + "lda and ldb must be below 2^24");
   if (!aligned(a, 16) || !aligned(b, 16) || (M > 1 && lda % 16 != 0) || (N > 1 && ldb % 16 != 0))
     return fail(FP8Q_EALIGN, pre + "a, b and their row strides must be 16-byte aligned");
-  if (!aligned(y, 2)) return fail(FP8Q_EALIGN, pre + "y must be 2-byte aligned");
-  Mxfp4GemmParams p{};
   int rc = scale_words(pre, "a's", sa, sa_fmt, M, K, sa_sm, sa_sk, p.sa_sm, p.sa_sk);
   if (rc != FP8Q_OK) return rc;
   rc = scale_words(pre, "b's", sb, sb_fmt, N, K, sb_sn, sb_sk, p.sb_sn, p.sb_sk);
@@ -109,13 +118,8 @@ int gemm_entry(const uint8_t* a, int64_t lda, const void* sa, int sa_fmt, int64_
   p.sa = static_cast<const uint8_t*>(sa);
   p.b = b;
   p.sb = static_cast<const uint8_t*>(sb);
-  p.y = y;
-  p.M = M;
-  p.N = N;
-  p.K = K;
   p.lda = M > 1 ? lda : K / 2;
   p.ldb = N > 1 ? ldb : K / 2;
-  p.ldy = ldy;
   p.ws = static_cast<float*>(workspace);
   p.ws_bytes = workspace ? workspace_bytes : 0;
   return launch_mxfp4_gemm(p, static_cast<hipStream_t>(stream));

@@ -520,6 +520,11 @@ __global__ __launch_bounds__(256) void gemm_mxfp4_join_kernel(Mxfp4GemmParams p)
   }
 }
 
+// Y of an empty K.
+__global__ __launch_bounds__(256) void gemm_mxfp4_zero_kernel(uint16_t* y, int64_t M, int64_t N, int64_t ldy) {
+  for (int64_t t = blockIdx.x * int64_t(256) + threadIdx.x; t < M * N; t += gridDim.x * int64_t(256)) y[t / N * ldy + t % N] = 0;
+}
+
 // ------------------------------------------------------------------ few rows
 // Up to 16 SM rows of A: a block has 16 rows of B and all of K, its W waves contiguous ranges of it; operands go from
 // memory straight to registers, P units of 128 elements at a time, and the waves' sums meet in LDS, added in their
@@ -714,6 +719,12 @@ void launch_few(const Mxfp4GemmParams& p, int64_t blocks, hipStream_t stream) {
   else hipLaunchKernelGGL((gemm_mxfp4_few_kernel<4, W>), grid, block, 0, stream, p);
 }
 
+int finish() {
+  const hipError_t err = hipGetLastError();
+  if (err != hipSuccess) return fail(FP8Q_ELAUNCH, std::string("mxfp4 product launch: ") + hipGetErrorString(err));
+  return FP8Q_OK;
+}
+
 }  // namespace
 
 int64_t mxfp4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) { return shape_of(M, N, K, current_device_shape().cus).ws; }
@@ -739,9 +750,13 @@ int launch_mxfp4_gemm(const Mxfp4GemmParams& p_in, hipStream_t stream) {
     const int64_t quads = p.M * ((p.N + 3) / 4);
     hipLaunchKernelGGL(gemm_mxfp4_join_kernel, dim3(static_cast<unsigned>(std::min<int64_t>((quads + 255) / 256, 4096))), dim3(256), 0, stream, p);
   }
-  const hipError_t err = hipGetLastError();
-  if (err != hipSuccess) return fail(FP8Q_ELAUNCH, std::string("mxfp4 product launch: ") + hipGetErrorString(err));
-  return FP8Q_OK;
+  return finish();
+}
+
+int launch_mxfp4_zero(const Mxfp4GemmParams& p, hipStream_t stream) {
+  const int64_t blocks = std::min<int64_t>((p.M * p.N + 255) / 256, 4096);
+  hipLaunchKernelGGL(gemm_mxfp4_zero_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream, p.y, p.M, p.N, p.ldy);
+  return finish();
 }
 
 }  // namespace fp8q

@@ -42,5 +42,6 @@ struct Mxfp4GemmParams {
 
 int64_t mxfp4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
 int launch_mxfp4_gemm(const Mxfp4GemmParams& p, hipStream_t stream);
+int launch_mxfp4_zero(const Mxfp4GemmParams& p, hipStream_t stream);  // K == 0
 
 }  // namespace fp8q

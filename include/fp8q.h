@@ -364,7 +364,7 @@ int fp8q_mxfp4_dequant(const uint8_t* q, int64_t q_sm, const void* s, int scale_
  * with one UE8M0 byte per (row, k/32). sa_fmt UE8M0_PACKED: byte k/32 % 4 of the 32-bit word at
  * sa + 4*(m*sa_sm + (k/128)*sa_sk) bytes, any strides (column-major words, as the quantizer writes them, are
  * read fastest); sa_fmt UE8M0: row-major bytes (sa_sk == 1) whose rows lie a multiple of 4 bytes apart. sb
- * likewise. Accumulation is fp32; byte 0 counts as 2^-127, and 255 gives NaN.
+ * likewise. Accumulation is fp32; byte 0 counts as 2^-127, and 255 gives NaN. With K == 0 Y is zeros.
  *
  * fp8q_gemm_mxfp4_workspace_size returns the bytes of workspace with which the call splits K over more of
  * the device (0: it does not, or the sizes are refused). With a smaller or NULL workspace the call runs
