@@ -23,6 +23,7 @@
 #include <type_traits>
 
 #include "mxfp4.h"
+#include "mxfp4_shape.h"
 
 namespace fp8q {
 namespace {
@@ -491,18 +492,17 @@ using Flat = Tile<64, 128, 2, 2, 4, 4, 1>;
 
 // Y = bf16( the splits' sums added in their order, so that results do not change from call to call ): four columns per
 // thread.
-constexpr int kMostSplits = 16;
 __global__ __launch_bounds__(256) void gemm_mxfp4_join_kernel(Mxfp4GemmParams p) {
   const int64_t quads = (p.N + 3) / 4, total = p.M * quads, plane = p.M * quads;
   for (int64_t t = blockIdx.x * int64_t(256) + threadIdx.x; t < total; t += gridDim.x * int64_t(256)) {
     const v4f* src = reinterpret_cast<const v4f*>(p.ws) + t;
-    v4f v[kMostSplits];
+    v4f v[kMxfp4MostSplits];
 #pragma unroll
-    for (int s = 0; s < kMostSplits; s++)
+    for (int s = 0; s < kMxfp4MostSplits; s++)
       if (s < p.splits) v[s] = src[s * plane];
     v4f sum = v[0];
 #pragma unroll
-    for (int s = 1; s < kMostSplits; s++)
+    for (int s = 1; s < kMxfp4MostSplits; s++)
       if (s < p.splits) {
 #pragma unroll
         for (int q = 0; q < 4; q++) sum[q] += v[s][q];
@@ -637,75 +637,9 @@ __global__ __launch_bounds__(64 * W, 1) void gemm_mxfp4_few_kernel(Mxfp4GemmPara
 }
 
 // ------------------------------------------------------------------ launch
-enum class Kind { kFew, kLarge, kDeep, kFlat };
-struct Shape {
-  Kind kind;
-  int splits;
-  int64_t ws;  // bytes
-};
-
-int64_t tiles_of(int64_t M, int64_t N, int bm, int bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); }
-
-// The kernel, tile and ranges of K with the least estimated time: rounds of tiles over the CUs, each its steps of 256
-// elements and a part for its outputs, and a part for the call; not less than the bytes take. Splitting adds a launch and
-// the partial sums' way to memory and back. us, each kernel where it was forced (* with K split, where that was the
-// better), the chosen one marked:
-//   M x N x K             256 x 256   128 x 128   64 x 128
-//   8192 x 8192 x 8192    > 308          379         503
-//   4096 x 4096 x 7168    >  66           77         106
-//   2048 x 8192 x 2048    >  28.8         32.9        40.6
-//   2048 x 4096 x 7168       54        >  43          57
-//   1024 x 4096 x 7168       44.7      >  22.3        28.0
-//   3000 x 3000 x  512       18.9      >  14.7        16.0
-//   1993 x 5920 x  256       19.2      >  15.0        17.5
-//    512 x 4096 x 7168       43.4         19.3      > 15.9
-//    128 x 4096 x 7168       41.5         17.3 *    > 14.6 (split 15.3)
-//     65 x 4096 x 7168       44.7         15.2 *    > 14.0 *
-//    333 x 4104 x 2176       24.6         11.2      >  9.2
-//    300 x  300 x 8192       55.1         11.9 *    > 10.9 * (17.0 unsplit)
-// Up to 64 rows, without staging and with tiles of 64 x 128: B goes through the registers of every 16 rows, which is
-// the shorter way while there are few of them or few rounds.
-//   64 x  4096 x 7168   > 11.7   13.9 *      32 x  4096 x 7168   >  7.9   12.7 *
-//   64 x  8192 x 8192     24.1 > 18.5 *      32 x 14336 x 4096     14.0 > 11.3
-//   64 x 14336 x 4096     22.5 > 11.7        32 x 28672 x 8192     51.1 > 33.3
-//   64 x 28672 x 8192     81.9 > 33.8        16 x 28672 x 8192     37.5 > 31.7
-//   64 x  2048 x 4096   >  7.4   10.5 *      16 x  8192 x 8192   > 12.1   14.6 *
-Shape shape_of(int64_t M, int64_t N, int64_t K, int cus) {
-  struct Model {
-    Kind kind;
-    int bm, bn;
-    double step, round, call;  // us
-    bool split;
-  };
-  const Model models[] = {{Kind::kFew, 64, 16, M <= 16 ? 0.08 + 0.003 * M : M <= 32 ? 0.165 : 0.30, 0.4, 3.4, false},
-                          {Kind::kLarge, 256, 256, 1.85, 7.0, 7.0, false},
-                          {Kind::kDeep, 128, 128, 0.58, 2.5, 4.0, true},
-                          {Kind::kFlat, 64, 128, 0.38, 2.0, 4.0, true}};
-  const double steps = static_cast<double>(K) / 256;
-  const double least_time = 4.0 + (static_cast<double>(M + N) * K * 17 / 32 + 2.0 * M * N) / 4.5e6;
-  const int64_t n4 = (N + 3) / 4 * 4;
-  Shape best{Kind::kLarge, 1, 0};
-  double least = 1e300;
-  for (const Model& m : models) {
-    if (m.kind == Kind::kFew && M > m.bm) continue;
-    const int64_t tiles = tiles_of(M, N, m.bm, m.bn);
-    const int64_t most = m.split ? std::max<int64_t>(1, std::min<int64_t>({cus / tiles, K / 1024, kMostSplits})) : 1;
-    for (int64_t s = 1; s <= most; s++) {
-      const double rounds = static_cast<double>((tiles * s + cus - 1) / cus), bytes = static_cast<double>(s * M * n4 * 4);
-      const double join = s > 1 ? 4.0 + 2 * bytes / 3e6 : 0.0;
-      const double time = std::max(m.call + rounds * (steps / s * m.step + m.round) + join, least_time);
-      if (time < least || (time == least && m.kind == best.kind)) {  // (of equal ones the most ranges: more CUs load)
-        least = time;
-        best = {m.kind, static_cast<int>(s), s > 1 ? s * M * n4 * 4 : 0};
-      }
-    }
-  }
-  return best;
-}
-
 template <class C>
 void launch(const Mxfp4GemmParams& p, const DeviceShape& ds, hipStream_t stream) {
-  const int64_t units = tiles_of(p.M, p.N, C::BM, C::BN) * p.splits;
+  const int64_t units = mxfp4_tiles(p.M, p.N, C::BM, C::BN) * p.splits;
   int64_t grid = std::min<int64_t>(units, int64_t(ds.cus) * C::kBlocks);
   grid = std::max<int64_t>((grid + ds.xcds - 1) / ds.xcds * ds.xcds, ds.xcds);
   hipLaunchKernelGGL((gemm_mxfp4_kernel<C>), dim3(static_cast<unsigned>(grid)), dim3(C::kThreads), 0, stream, p);
@@ -727,24 +661,24 @@ int finish() {
 
 }  // namespace
 
-int64_t mxfp4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) { return shape_of(M, N, K, current_device_shape().cus).ws; }
+int64_t mxfp4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) { return mxfp4_shape(M, N, K, current_device_shape().cus).ws; }
 
 int launch_mxfp4_gemm(const Mxfp4GemmParams& p_in, hipStream_t stream) {
   const DeviceShape ds = current_device_shape();
   Mxfp4GemmParams p = p_in;
   p.xcds = ds.xcds;
-  Shape s = shape_of(p.M, p.N, p.K, ds.cus);
+  Mxfp4Shape s = mxfp4_shape(p.M, p.N, p.K, ds.cus);
   if (s.ws > 0 && (p.ws == nullptr || p.ws_bytes < s.ws)) s.splits = 1;
   p.splits = s.splits;
   switch (s.kind) {
-    case Kind::kFew: {
+    case Mxfp4Kind::kFew: {
       const int64_t blocks = (p.N + 15) / 16;
       blocks > ds.cus ? launch_few<4>(p, blocks, stream) : launch_few<8>(p, blocks, stream);
       break;
     }
-    case Kind::kLarge: launch<Large>(p, ds, stream); break;
-    case Kind::kDeep: p.splits > 1 ? launch<Splitting<Deep>>(p, ds, stream) : launch<Deep>(p, ds, stream); break;
-    case Kind::kFlat: p.splits > 1 ? launch<Splitting<Flat>>(p, ds, stream) : launch<Flat>(p, ds, stream); break;
+    case Mxfp4Kind::kLarge: launch<Large>(p, ds, stream); break;
+    case Mxfp4Kind::kDeep: p.splits > 1 ? launch<Splitting<Deep>>(p, ds, stream) : launch<Deep>(p, ds, stream); break;
+    case Mxfp4Kind::kFlat: p.splits > 1 ? launch<Splitting<Flat>>(p, ds, stream) : launch<Flat>(p, ds, stream); break;
   }
   if (p.splits > 1) {
     const int64_t quads = p.M * ((p.N + 3) / 4);
