@@ -141,12 +141,18 @@ def _stream(stream) -> int:
     return int(stream)
 
 
-def _other_gpu(device: int, stream) -> bool:
-    """Whether GPU `device`, which holds a call's tensors, is not the current one: kernels, their shapes and the
-    default stream go by that, so the call makes it current. (A stream's handle does not say whose it is.)"""
+def _stream_here(stream, device: int) -> int | None:
+    """The stream's handle for a call whose tensors are on GPU `device`; None where another GPU is the current one:
+    kernels, their shapes and the default stream go by that, so the call makes the tensors' current. (A handle that is
+    given as a number does not say whose it is.)"""
+    if stream is None:
+        current = torch._C._cuda_getDevice()
+        return torch._C._cuda_getCurrentRawStream(current) if current == device else None
     if isinstance(stream, torch.cuda.Stream) and stream.device_index != device:
         raise ValueError("the stream must be one of the tensors' GPU")
-    return (stream is None or torch.cuda.is_initialized()) and torch._C._cuda_getDevice() != device
+    if torch.cuda.is_initialized() and torch._C._cuda_getDevice() != device:
+        return None
+    return _stream(stream)
 
 
 def _ptr(t: torch.Tensor | None) -> int | None:
@@ -449,16 +455,17 @@ def _mxfp4_rows(entry: str, x, q, s, width, stream) -> None:
         raise ValueError(f"s has shape {tuple(s.shape)} of {s.dtype}, expected a scale per 32 of {(M, K)} elements")
     if not 0 <= x.get_device() == q.get_device() == s.get_device():
         raise ValueError(_ELSEWHERE)
-    if _other_gpu(x.get_device(), stream):
+    handle = _stream_here(stream, x.get_device())
+    if handle is None:
         with torch.cuda.device(x.get_device()):
             return _mxfp4_rows(entry, x, q, s, width, stream)
     s_sm, s_sg = s.stride()
     if entry == "fp8q_mxfp4_dequant":
         _check(load_library().fp8q_mxfp4_dequant(q.data_ptr(), q_sm, s.data_ptr(), fmt, s_sm, s_sg, x.data_ptr(), dt, M, K,
-                                                 x_sm, _stream(stream)))
+                                                 x_sm, handle))
     else:
         _check(getattr(load_library(), entry)(x.data_ptr(), dt, M, K, x_sm, q.data_ptr(), q_sm, s.data_ptr(), fmt, s_sm, s_sg,
-                                              _stream(stream)))
+                                              handle))
 
 
 def fp8q_mxfp4_quant(x: torch.Tensor, q: torch.Tensor, s: torch.Tensor, stream=None) -> None:
@@ -531,10 +538,10 @@ def fp8q_gemm_mxfp4(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torc
             or (workspace is not None and workspace.get_device() != a.get_device()):
         raise ValueError(_ELSEWHERE)
     dev = a.get_device()
-    if _other_gpu(dev, stream):
+    handle = _stream_here(stream, dev)
+    if handle is None:
         with torch.cuda.device(dev):
             return fp8q_gemm_mxfp4(a, sa, b, sb, y, stream, workspace)
-    handle = _stream(stream)
     if workspace is None:
         size = _gemm_mxfp4_workspace_size(dev, M, N, K)
         if size > 0:
@@ -732,24 +739,28 @@ def _kv4_attend(entry: str, sizes: tuple, extra: tuple, q, cache, block_table, k
         lse_ptr, l_st = lse.data_ptr(), lse.stride(0)
     page, kv_heads = cache.k.shape[1:3]
     args = _kv4_args(cache, kv_heads, D)
-    if not kv_lens.get_device() == q.get_device() == out.get_device() == block_table.get_device() == cache.k.get_device() \
-            or (q_indptr is not None and q_indptr.get_device() != q.get_device()) \
-            or (lse is not None and lse.get_device() != q.get_device()) \
-            or (workspace is not None and workspace.get_device() != q.get_device()):
+    dev = q.get_device()
+    if not kv_lens.get_device() == dev == out.get_device() == block_table.get_device() == cache.k.get_device() \
+            or (q_indptr is not None and q_indptr.get_device() != dev) \
+            or (lse is not None and lse.get_device() != dev) \
+            or (workspace is not None and workspace.get_device() != dev):
         raise ValueError(_ELSEWHERE)
-    if _other_gpu(q.get_device(), stream):
-        with torch.cuda.device(q.get_device()):
+    handle = _stream_here(stream, dev)
+    if handle is None:
+        with torch.cuda.device(dev):
             return _kv4_attend(entry, sizes, extra, q, cache, block_table, kv_lens, out, sm_scale, q_indptr, lse, stream,
                                workspace)
-    handle = _stream(stream)
     lib = load_library()
+    ws_ptr, ws_bytes = None, 0
     if workspace is None:
-        workspace = _alloc_workspace(getattr(lib, entry + "_workspace_size")(dt, B, T, H, kv_heads, D, max_pages * page, *sizes), q.device, stream)
+        size = getattr(lib, entry + "_workspace_size")(dt, B, T, H, kv_heads, D, max_pages * page, *sizes)
+        if size > 0:
+            workspace = _alloc_workspace(size, q.device, stream)
+    if workspace is not None:
+        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _check(getattr(lib, entry)(
         q.data_ptr(), dt, q_st, q_sh, *args, block_table.data_ptr(), table_sb, max_pages, kv_lens.data_ptr(), ip_ptr,
-        out.data_ptr(), o_st, o_sh, lse_ptr, l_st, B, T, H, kv_heads, D, sm_scale, *extra,
-        None if workspace is None else workspace.data_ptr(),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), handle))
+        out.data_ptr(), o_st, o_sh, lse_ptr, l_st, B, T, H, kv_heads, D, sm_scale, *extra, ws_ptr, ws_bytes, handle))
 
 
 def fp8q_kv4_attention(q: torch.Tensor, cache: Kv4Cache, block_table: torch.Tensor, kv_lens: torch.Tensor,
@@ -856,7 +867,8 @@ def fp8q_kv4_plan(kv_lens: torch.Tensor, q_lens: torch.Tensor, free_pages: torch
             == q_indptr.get_device() == slots.get_device() == pages_taken.get_device() \
             or (positions is not None and positions.get_device() != dev):
         raise ValueError(_ELSEWHERE)
-    if _other_gpu(dev, stream):
+    handle = _stream_here(stream, dev)
+    if handle is None:
         with torch.cuda.device(dev):
             return fp8q_kv4_plan(kv_lens, q_lens, free_pages, block_table, pages, page_size, new_lens, q_indptr, slots,
                                  pages_taken, positions, stream)
@@ -878,7 +890,7 @@ def fp8q_kv4_plan(kv_lens: torch.Tensor, q_lens: torch.Tensor, free_pages: torch
     _check(load_library().fp8q_kv4_plan(
         kv_lens.data_ptr(), q_lens.data_ptr(), B, free_pages.data_ptr(), F, block_table.data_ptr(), table_sb, max_pages, pages,
         page_size, new_lens.data_ptr(), q_indptr.data_ptr(), slots.data_ptr(),
-        None if positions is None else positions.data_ptr(), T, pages_taken.data_ptr(), _stream(stream)))
+        None if positions is None else positions.data_ptr(), T, pages_taken.data_ptr(), handle))
 
 
 class Kv4Plan(NamedTuple):
