@@ -771,7 +771,8 @@ def fp8q_kv4_attention(q: torch.Tensor, cache: Kv4Cache, block_table: torch.Tens
     q, out [T, heads, D] (bf16 or fp16); block_table int32 [B, max_pages]; kv_lens int32 [B];
     q_indptr int32 [B + 1]: sequence b's queries are rows q_indptr[b] .. q_indptr[b + 1] - 1 (None: row
     b, T == B). causal: the last query of a sequence sees all its cached tokens, the one before it
-    one less, ... lse [T, heads] fp32 receives the logarithm of each row's softmax sum.
+    one less, ... lse [T, heads] fp32 receives the logarithm of each row's softmax sum. The probabilities
+    multiply the values in 16 bits for fp16 outputs and in bf16 for bf16 ones.
     When the shape can use a workspace and none is given, one is taken from torch's allocator."""
     _kv4_attend("fp8q_kv4_attention", (), (causal,), q, cache, block_table, kv_lens, out, sm_scale, q_indptr, lse, stream,
                 workspace)
@@ -800,7 +801,7 @@ def fp8q_kv4_window_attention(q: torch.Tensor, cache: Kv4Cache, block_table: tor
                               q_indptr: torch.Tensor | None = None, lse: torch.Tensor | None = None, stream=None,
                               workspace: torch.Tensor | None = None) -> None:
     """fp8q_kv4_attention (causal) in which a query sees the last `window` tokens up to and with its own, and the
-    first `sinks` of its sequence."""
+    first `sinks` of its sequence. The probabilities have 16 bits for both types."""
     _kv4_attend("fp8q_kv4_window_attention", (window, sinks), (window, sinks), q, cache, block_table, kv_lens, out, sm_scale,
                 q_indptr, lse, stream, workspace)
 
@@ -829,7 +830,7 @@ def fp8q_kv4_tree_attention(q: torch.Tensor, cache: Kv4Cache, block_table: torch
                             workspace: torch.Tensor | None = None) -> None:
     """fp8q_kv4_attention for drafted tokens that form a tree: a sequence's n rows of q are held at its last n cached
     places; each sees every token before them, and drafted token j if bit j % 32 of word j // 32 of its row of
-    tree_mask (int32 [T, words]) is set."""
+    tree_mask (int32 [T, words]) is set. The probabilities have 16 bits for both types."""
     if tree_mask.dtype != torch.int32 or tree_mask.dim() != 2 or tree_mask.shape[0] != q.shape[0] \
             or (tree_mask.shape[1] > 1 and tree_mask.stride(1) != 1):
         raise ValueError("tree_mask must be an int32 [T, words] tensor with contiguous rows")

@@ -44,9 +44,9 @@
 //     (ds_read_b64_tr_b16: lane (r, h) gets dim r of tokens 4h .. 4h + 3).
 //
 // fp16 queries are the sum of two bf16 parts (8 + 3 bits of their 11), multiplied one after the
-// other; the probabilities likewise for fp16 outputs. For bf16 outputs the probabilities are
-// rounded to bf16 once: the error, 2^-8 of each term at most, is of the size of the output's
-// own rounding.
+// other; the probabilities likewise for fp16 outputs, and for those of windows and trees. For the
+// plain calls' bf16 outputs the probabilities are rounded to bf16 once: the error, 2^-8 of each
+// term at most, is of the size of the output's own rounding (probability_parts below).
 #pragma once
 
 #include <algorithm>
@@ -78,6 +78,13 @@ constexpr float kHeadroom = 8.0f;
 constexpr float kNegInf = -__builtin_inff();
 
 __device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }
+
+// Parts that a probability is held in. Two, 16 bits together, for fp16 outputs, and for windows and trees also for bf16
+// ones, which are then as near to 64 bits as their own rounding lets them be: off by 0.0017 of the whole on random
+// values, by 0.0023 with one part. One in the plain calls' bf16. us, two parts and one: 64 single tokens with windows of
+// 4096 62 and 57, the prompt chunk with windows of 1024 131 and 107, 16 trees of up to 64, heads of 128, 101 and 87, one tree
+// of 25 13.9 and 13.4.
+constexpr int probability_parts(int mask, int DT) { return DT == FP8Q_DTYPE_F16 || mask != kAll ? 2 : 1; }
 
 // exp2(scale s - ms) of a row's four scores, added to l, as elements 4 at .. of an operand: bf16, or the sum of two parts
 // (two values to each conversion; a part's value in fp32 is its bits moved up).
@@ -695,7 +702,7 @@ __device__ __forceinline__ bf16x8 read_v(const uint16_t* src, int d) {
 
 template <int MASK, int D, int DT, int WAVES, int N, bool SPLIT, int PAGE>
 __global__ __launch_bounds__(64 * WAVES, waves_per_simd(D, DT, N)) void kv4_attention_kernel(Kv4AttnParams p) {
-  constexpr int PARTS = DT == FP8Q_DTYPE_F16 ? 2 : 1;
+  constexpr int PARTS = DT == FP8Q_DTYPE_F16 ? 2 : 1, P_PARTS = probability_parts(MASK, DT);
   constexpr int kTile = 16 * N;         // tokens of a wave's step
   constexpr int kStep = kTile * WAVES;  // and of the block's
   constexpr int kSteps = D / 32;   // contraction steps of S^T
@@ -823,7 +830,7 @@ __global__ __launch_bounds__(64 * WAVES, waves_per_simd(D, DT, N)) void kv4_atte
           for (int i = 0; i < 4; i++) o[d][i] *= alpha;
       }
       const float ms = m == kNegInf ? 0.0f : m;  // nothing seen yet: every p is 0
-      bf16x8 pr[N / 2][PARTS];
+      bf16x8 pr[N / 2][P_PARTS];
 #pragma unroll
       for (int c = 0; c < N; c++) probabilities(s[c], p.scale_log2, ms, l, pr[c / 2], c % 2);
 
@@ -840,7 +847,7 @@ __global__ __launch_bounds__(64 * WAVES, waves_per_simd(D, DT, N)) void kv4_atte
         if (g + 1 < N / 2 * kDims) vf[(g + 1) & 1] = read_v<kRowV>(v_at + 32 * ((g + 1) / kDims) * kRowV, (g + 1) % kDims);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int a = 0; a < PARTS; a++) o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[g & 1], pr[c][a], o[d], 0, 0, 0);
+        for (int a = 0; a < P_PARTS; a++) o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[g & 1], pr[c][a], o[d], 0, 0, 0);
         __builtin_amdgcn_sched_barrier(0);
       }
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -925,7 +932,7 @@ constexpr int wide_waves_per_simd(int D, int DT, int QT, bool split) {
 
 template <int MASK, int D, int DT, int QT, bool SPLIT, int PAGE>
 __global__ __launch_bounds__(64 * kWideWaves, wide_waves_per_simd(D, DT, QT, SPLIT)) void kv4_attention_wide_kernel(Kv4AttnParams p) {
-  constexpr int PARTS = DT == FP8Q_DTYPE_F16 ? 2 : 1;
+  constexpr int PARTS = DT == FP8Q_DTYPE_F16 ? 2 : 1, P_PARTS = probability_parts(MASK, DT);
   constexpr int kSteps = D / 32, kDims = D / 16, kRowV = D + kPadV;
   constexpr int kHalves = kStepW / 16;
   constexpr int ROWS = 16 * QT * kWideWaves;
@@ -1073,7 +1080,7 @@ __global__ __launch_bounds__(64 * kWideWaves, wide_waves_per_simd(D, DT, QT, SPL
       {
         // wave-uniform
         const bool part = there != ~0ull || tok + kStepW > low || (MASK == kWindow && tok < high && tok + kStepW > p.sinks);
-        bf16x8 pr[QT][kHalves / 2][PARTS];
+        bf16x8 pr[QT][kHalves / 2][P_PARTS];
 #pragma unroll
         for (int n = 0; n < QT; n++) {
           if (part) {
@@ -1122,7 +1129,7 @@ __global__ __launch_bounds__(64 * kWideWaves, wide_waves_per_simd(D, DT, QT, SPL
 #pragma unroll
           for (int n = 0; n < QT; n++)
 #pragma unroll
-            for (int a = 0; a < PARTS; a++)
+            for (int a = 0; a < P_PARTS; a++)
               o[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[g & 1], pr[n][c][a], o[n][d], 0, 0, 0);
           __builtin_amdgcn_sched_barrier(0);
         }

@@ -482,7 +482,9 @@ int fp8q_kv4_read(void* k, int64_t k_st, int64_t k_sh,
  * results. Scale bytes 0 and 1, which the write never stores, count as 2; 255 is no scale. Scores,
  * sums and the output are accumulated in fp32, and must stay inside it: sum_d |q_d k_d| and
  * sm_scale times it below 2^127, the cached values that a sequence sees below 2^122 / kv_lens[b].
- * Outputs past the type's largest finite value become that value.
+ * Outputs past the type's largest finite value become that value. The probabilities multiply the
+ * values in 16 bits (two bf16 parts) for F16 outputs, and for BF16 ones in bf16: each then adds an
+ * error of at most 2^-8 of its term, as the output's own rounding does of the whole.
  *
  * fp8q_kv4_attention_workspace_size returns the bytes of workspace with which the call splits
  * long caches over more of the device (max_tokens = max_pages * page_size; 0: it needs none, or
@@ -514,8 +516,8 @@ int fp8q_kv4_attention(const void* q, int dtype, int64_t q_st, int64_t q_sh,
  * fp8q_kv4_attention with causal == 1 in which a query that would see tokens 0 .. p (its own place p being
  * the last) sees those j of them with j > p - window or j < sinks: `window` tokens with its own, and the
  * first `sinks` of the sequence. Pages that no query of a sequence sees are not read; their table entries may
- * be anything. window >= 1, sinks >= 0 [EINVAL]. Everything else is as there, the workspace's size by
- * fp8q_kv4_window_attention_workspace_size.
+ * be anything. window >= 1, sinks >= 0 [EINVAL]. The probabilities have 16 bits for both types. Everything else
+ * is as there, the workspace's size by fp8q_kv4_window_attention_workspace_size.
  */
 int64_t fp8q_kv4_window_attention_workspace_size(int dtype, int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
                                                  int64_t max_tokens, int64_t window, int64_t sinks);
@@ -541,8 +543,8 @@ int fp8q_kv4_window_attention(const void* q, int dtype, int64_t q_st, int64_t q_
  * int32 [T][tree_words]; drafted tokens from 32 * tree_words on are not seen, and bits past the draft, or of
  * drafted tokens that kv_lens[b] < n leaves out of the cache (the first n - kv_lens[b]), do nothing. tree_words
  * <= 2^26 [EUNSUPPORTED], tree_words, tree_st >= 0, tree_mask not NULL unless tree_words == 0 [EINVAL],
- * 4-byte aligned [EALIGN]. Everything else is as there, the workspace's size by
- * fp8q_kv4_tree_attention_workspace_size.
+ * 4-byte aligned [EALIGN]. The probabilities have 16 bits for both types. Everything else is as there, the
+ * workspace's size by fp8q_kv4_tree_attention_workspace_size.
  */
 int64_t fp8q_kv4_tree_attention_workspace_size(int dtype, int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
                                                int64_t max_tokens);
