@@ -343,7 +343,8 @@ int fp8q_grouped_gemm_contiguous(const uint8_t* a, int64_t lda,
  * Requirements (else the status in brackets): dtype in {BF16, F16, F32}, scale_fmt as above, K <= 2^30
  * [EUNSUPPORTED]; K % 32 == 0 (packed: 128), M, K >= 0, strides non-negative, written rows not
  * overlapping, scale strides row- or column-major [EINVAL]; x, q and their row strides 16-byte aligned,
- * packed words 4-byte [EALIGN].
+ * packed words 4-byte [EALIGN]. (fp8q_gemm_mxfp4 takes less: K % 128 == 0, and bytes in row-major order alone. A row of
+ * another K is its operand when zeros fill it up: codes and scales of zeros add nothing.)
  */
 int fp8q_mxfp4_quant(const void* x, int in_dtype, int64_t M, int64_t K, int64_t x_sm,
                      uint8_t* q, int64_t q_sm, void* s, int scale_fmt, int64_t s_sm, int64_t s_sg, void* stream);
