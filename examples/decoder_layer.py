@@ -1,6 +1,7 @@
 """The attention half of a decoder layer on this library: FP8 projections and a 4-bit paged
 key/value cache, for a batch of sequences that are first prompted and then decoded.
 
+    lengths -> kv4_plan -> slots, positions, page tables
     x, residual -> rms_norm_group_quant -> qkv GEMM -> rotation -> kv4_write -> kv4_attention
                 -> group_quant -> output GEMM -> (x for the next half, residual)
 
@@ -46,7 +47,7 @@ class AttentionLayer:
 
     def __init__(self, hidden, heads, kv_heads, dim, seqs, max_tokens, page=64, seed=0, device="cuda"):
         g = torch.Generator(device=device).manual_seed(seed)
-        self.heads, self.kv_heads, self.dim, self.page = heads, kv_heads, dim, page
+        self.heads, self.kv_heads, self.dim = heads, kv_heads, dim
 
         def weight(n, k):
             return quantize_weight(torch.randn(n, k, device=device, generator=g) / math.sqrt(k))
@@ -54,24 +55,42 @@ class AttentionLayer:
         self.norm = (1 + 0.1 * torch.randn(hidden, device=device, generator=g)).to(torch.bfloat16)
         self.w_qkv = weight((heads + 2 * kv_heads) * dim, hidden)
         self.w_out = weight(hidden, heads * dim)
-        # every sequence owns enough pages, scattered over the cache
+        # pages enough for every sequence, taken in a scattered order
         per_seq = -(-max_tokens // page)
         self.cache = fq.alloc_kv4_cache(seqs * per_seq, page, kv_heads, dim, device=device)
-        self.table = torch.randperm(seqs * per_seq, device=device, generator=g).to(torch.int32).view(seqs, per_seq)
+        self.order = torch.randperm(seqs * per_seq, device=device, generator=g).to(torch.int32)
+        self.table = torch.full((seqs, per_seq), -1, dtype=torch.int32, device=device)
+        self.clear()
 
-    def forward(self, x, residual, seq_of, positions, kv_lens, q_indptr=None):
-        """Rows x [T, hidden] (bf16) of tokens at `positions` of sequences `seq_of` [T]; kv_lens [B]: cached
-        tokens per sequence with these included; q_indptr [B + 1]: each sequence's rows (None: one each).
+    def clear(self):
+        """No tokens are cached, all pages are free."""
+        self.lens = torch.zeros(self.table.shape[0], dtype=torch.int32, device=self.table.device)
+        self.free = self.order
+
+    def plan(self, q_lens, tokens):
+        """The step in which sequence b gets q_lens[b] new tokens, `tokens` in all: the table's new entries, and what
+        forward() takes. The step can be planned again until it is done()."""
+        return fq.kv4_plan(self.cache, self.lens, q_lens, self.free, self.table, tokens)
+
+    def done(self, plan):
+        """The planned tokens are cached, their pages no longer free (without a copy to the host: the taken pages move
+        to the list's end, behind as many as are ever needed)."""
+        self.lens = plan.kv_lens
+        n = self.free.numel()
+        self.free = self.free[(torch.arange(n, device=self.free.device) + plan.pages_taken) % n]
+
+    def forward(self, x, residual, plan, single=False):
+        """Rows x [T, hidden] (bf16) of a planned step's tokens, one sequence after the other; single: one of each.
         Returns the layer's output and the new residual."""
         T, h, hk, d = x.shape[0], self.heads, self.kv_heads, self.dim
         q8, s8, residual = fq.rms_norm_group_quant(x, self.norm, residual=residual)
         qkv = torch.empty(T, (h + 2 * hk) * d, dtype=torch.bfloat16, device=x.device)
         fq.fp8q_gemm_blockscaled(q8, s8, *self.w_qkv, qkv)
         q, k, v = qkv.view(T, h + 2 * hk, d).split((h, hk, hk), 1)
-        q, k = rotate(q, positions), rotate(k, positions)
-        slots = self.table[seq_of, positions // self.page] * self.page + (positions % self.page).to(torch.int32)
-        fq.fp8q_kv4_write(k, v, slots, self.cache)
-        o = fq.kv4_attention(q, self.cache, self.table, kv_lens, 1 / math.sqrt(d), q_indptr=q_indptr)
+        q, k = rotate(q, plan.positions), rotate(k, plan.positions)
+        fq.fp8q_kv4_write(k, v, plan.slots, self.cache)
+        o = fq.kv4_attention(q, self.cache, self.table, plan.kv_lens, 1 / math.sqrt(d),
+                             q_indptr=None if single else plan.q_indptr)
         q8, s8 = fq.group_quant(o.view(T, h * d))
         y = torch.empty_like(x)
         fq.fp8q_gemm_blockscaled(q8, s8, *self.w_out, y)
@@ -100,17 +119,16 @@ def decode_batch(layer, x, residual, prompt_lens, steps):
     """Prompts of the given lengths, then `steps` tokens for every sequence, one at a time. x, residual:
     one [prompt + steps, hidden] tensor per sequence. Returns the outputs in the same layout."""
     dev, seqs = x[0].device, len(prompt_lens)
-    seq = torch.arange(seqs, device=dev)
-    lens = torch.tensor(prompt_lens, dtype=torch.int32, device=dev)
-    indptr = torch.zeros(seqs + 1, dtype=torch.int32, device=dev)
-    indptr[1:] = lens.cumsum(0)
-    positions = torch.cat([torch.arange(n, device=dev) for n in prompt_lens])
-    rows = [torch.cat([t[:n] for t, n in zip(s, prompt_lens)]) for s in (x, residual)]
-    y, _ = layer.forward(*rows, seq.repeat_interleave(lens), positions, lens, indptr)
+    layer.clear()
+    plan = layer.plan(torch.tensor(prompt_lens, dtype=torch.int32, device=dev), sum(prompt_lens))
+    y, _ = layer.forward(*(torch.cat([t[:n] for t, n in zip(s, prompt_lens)]) for s in (x, residual)), plan)
+    layer.done(plan)
     out = [list(part) for part in y.split(prompt_lens)]
+    one = torch.ones(seqs, dtype=torch.int32, device=dev)
     for i in range(steps):
-        rows = [torch.stack([t[n + i] for t, n in zip(s, prompt_lens)]) for s in (x, residual)]
-        y, _ = layer.forward(*rows, seq, (lens + i).long(), lens + i + 1)
+        plan = layer.plan(one, seqs)
+        y, _ = layer.forward(*(torch.stack([t[n + i] for t, n in zip(s, prompt_lens)]) for s in (x, residual)), plan, True)
+        layer.done(plan)
         for o, row in zip(out, y):
             o.append(row)
     return [torch.stack(o) for o in out]
@@ -128,14 +146,18 @@ def main():
           f"relative difference to the fp32 layer {float((out.float() - ref).norm() / ref.norm()):.3f}")
 
     # a decode step as a graph: the rows and lengths are read from the captured tensors at each replay
-    seq = torch.arange(len(prompts), device="cuda")
-    lens = torch.tensor(prompts, dtype=torch.int32, device="cuda")
+    one = torch.ones(len(prompts), dtype=torch.int32, device="cuda")
+    layer.lens = layer.lens - one  # the last token again, whose page is held
     row, res = torch.stack([t[-1] for t in x]), torch.stack([t[-1] for t in residual])
-    layer.forward(row, res, seq, lens.long(), lens + 1)
+
+    def step():
+        return layer.forward(row, res, layer.plan(one, len(prompts)), True)
+
+    step()
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        layer.forward(row, res, seq, lens.long(), lens + 1)
+        step()
     graph.replay()
     torch.cuda.synchronize()
     t0 = time.perf_counter()
