@@ -12,13 +12,13 @@
 // Rows are swizzled in LDS so that no reads collide. The outputs go through LDS, 32 rows x 64 columns of a wave at a
 // time, so that every store writes whole lines (past the caches they are slower).
 //
-// What bounds it. 8192^3, tiles of 256 x 256: 280 to 305 us back to back (by the card; 3.6 to 3.9 PFLOP/s), 257 in calls with
-// pauses between them. The matrix pipe is busy in 58 % of the cycles of a clock that the power holds at 1.7 GHz (products
+// What bounds it. 8192^3, tiles of 256 x 256: 281 to 312 us back to back (by the clock that the power allows; 3.5 to 3.9
+// PFLOP/s), 260 in calls with pauses between them. The matrix pipe is busy in 58 % of the cycles of a clock that the power holds at 1.7 GHz (products
 // alone, without loads, reach 6.3 to 6.9 PFLOP/s on random codes and 8.6 to 9.2 on zeros). The loads come next: 31
 // clocks of a CU for each 1 KB, so that 32 of a step's 34 KB take 992 clocks next to 1024 of products. Scale words by
 // 16-byte loads, four in the place of eight of the 40 instructions: 2 to 4 % less on column-major words, but no other
-// layout; not done. 8 waves to a block, or tiles in groups of 2 or 8 rows instead of 4: no faster. 4096^2 x 7168 66 us (3.6
-// PFLOP/s), 2048 x 4096 x 7168 43 (2.8), 1024 x 4096 x 7168 22.5 (2.7), 333 x 4104 x 2176 9.1, 1024^3 6.6.
+// layout; not done. 8 waves to a block, or tiles in groups of 2 or 8 rows instead of 4: no faster. 4096^2 x 7168 67 us (3.6
+// PFLOP/s), 2048 x 4096 x 7168 44 (2.7), 1024 x 4096 x 7168 22.7 (2.6), 333 x 4104 x 2176 9.4, 1024^3 6.5.
 #include <algorithm>
 #include <type_traits>
 
@@ -531,8 +531,8 @@ __global__ __launch_bounds__(256) void gemm_mxfp4_zero_kernel(uint16_t* y, int64
 // order. (v_mfma_scale_f32_16x16x128: lane (r, h) holds row r, the 32 elements of K block h, and its scale byte.) A lane
 // loads the scale word of one row for one of four units (lane group h the h-th), which the others get by exchanges.
 //
-// The weights' bytes bound it, for one row N x K (launch included): 4096 x 7168, 15.6 MB, 5.7 us; 16384 x 4096, 35.7 MB, 8.8
-// (4.0 TB/s); 28672 x 8192, 125 MB, 25.7 (4.9). A range that is not whole in P ends in a step of four units or of P with
+// The weights' bytes bound it, for one row N x K (launch included): 4096 x 7168, 15.6 MB, 5.6 us; 16384 x 4096, 35.7 MB, 8.9
+// (4.0 TB/s); 28672 x 8192, 125 MB, 25.3 (4.9). A range that is not whole in P ends in a step of four units or of P with
 // clamped loads (steps of P only: 16384 x 4096, of 4 units to a wave, 12.9). Blocks are of 8 waves while no CU has two,
 // else of 4, which then have more loads each under way: us for 4 and 8, one row, 4096 x 7168 6.0 and 5.7, 16384 x 4096 8.8 and
 // 10.1, 28672 x 8192 25.7 and 29.8; 32 rows, 4096 x 7168 8.5 and 7.7, 8192 x 8192 15.4 and 15.9; 64 rows, 4096 x 7168 13.9 and

@@ -26,11 +26,12 @@
 //
 // Masks. A window's tokens are read and no others: a unit's places run through the sinks' steps and go on where its first
 // row's window begins, so that every row of it finds its own there. A tree's mask is looked up in a unit's last steps
-// only. Both hide scores of steps that some row does not see whole, and cost little: 16 trees of up to 64 tokens over up
-// to 4096, 32 heads on 8 of 64 (fp16) 81 us, the plain call on the same 80; of 128 (bf16) 87 and 86. 64 single tokens with windows of
-// 4096, 64 heads on 8 of 128: 288 MB in 59 us = 4.9 TB/s. 2 x 1434 and 2048 queries with windows of 1024, 32 heads on 8
-// of 128: 62.6 GFLOP in 107 us = 0.58 PFLOP/s: a tile's rows have 31 tokens more together than each alone, the
-// steps round that up, and 872 units of 18 steps fill the device's 1024 places unevenly.
+// only. Both hide scores of steps that some row does not see whole, which costs little: 16 trees of up to 64 tokens over up
+// to 4096, 32 heads on 8 of 64 (fp16) 81 us, the plain call on the same 80; of 128 (bf16, with one part to a probability, as
+// the plain call has) 87 and 86. 64 single tokens with windows of 4096, 64 heads on 8 of 128: 288 MB in 60 us = 4.8 TB/s.
+// 2 x 1434 and 2048 queries with windows of 1024, 32 heads on 8 of 128: 62.6 GFLOP in 131 us = 0.48 PFLOP/s: the vector pipe
+// issues in 61 % of the cycles and the matrix pipe is busy in 40 %; a tile's rows have 31 tokens more together than each
+// alone, the steps round that up, and 872 units of 18 steps fill the device's 1024 places unevenly.
 //
 // Layouts (v_mfma_f32_16x16x32_bf16; lane l, r = l % 16, h = l / 16):
 //   S^T = K Q^T: lane (r, h) loads dims [D/4 h, D/4 (h + 1)) of token r, one or two scale blocks

@@ -28,7 +28,7 @@ constexpr int waves_per_simd(int64_t D, int DT, int N) {
 }
 
 // Rows of the widest tile whose queries and outputs the registers hold (in fp16, as two parts, all but up
-// to 17 of them).
+// to 24 of them).
 constexpr int widest(int dtype, int64_t D) { return D * (dtype == FP8Q_DTYPE_F16 ? 2 : 1) <= 128 ? 128 : 64; }
 
 constexpr int kMostWideSteps = 32;  // of a unit that the wide kernel does not split
@@ -67,8 +67,12 @@ constexpr int tall_waves(int DT, int64_t D) { return waves_per_simd(D, DT, 2) * 
 //   1 x  500  7.1  8.0 10.4    16 x  700  9.0  9.1 17.0    64 x  300 10.5 15.9 19.6
 //   1 x 2000 15   13.6 12.1    16 x 1500 15   12.4 19.2    64 x 1500 20.3 25.3 31.9
 //   2 x 4000 25   19.1 11.5    32 x 5000      33   39.6    64 x 3000 38.9 41.7 47
-// Trees stay whole for two steps more: one of 25 over 1000 tokens 13.3 and tall 14.6, 16 of 4 14.1 and 15.5 (but 8 single tokens
-// with windows of 700 11.9 and 10.9).
+// Trees stay whole for two steps more, up to 1024 tokens of the table's width (heads of 128 in bf16). us whole, tall and split:
+//   one of 25 over 1000  13.1 14.3 13.5    4 of 25 over 1000  13.9 15.4 19.1    16 of 4 over 1000  13.6 15.0 17.6
+//                  1280  14.6 15.1 15.2                 1250  15.5 16.4 21.2                 1250  15.1 15.9 22.4
+//                  1536  16.2 16.4 15.9                 1500  17.3 17.8 21.8                 1500  16.8 17.2 19.9
+//                  2000  19.0 18.4 16.5                 2000  20.4 20.0 29.6                 2000  20.7 20.2 21.4
+// (five and six steps are within 5 % either way; 8 single tokens with windows of 700 9.7 and 10.0).
 enum class Cut { kWhole, kTall, kSplit };
 constexpr int kMostSteps = 16, kMostTallSteps = 12;
 
@@ -102,9 +106,9 @@ inline int64_t window_tokens(int64_t max_tokens, int64_t window, int64_t sinks) 
 }
 
 // Tiles of a window or tree call: 16 rows while there are few of them, which then use more of the device than tiles of 64
-// (us for 16 and 64 rows, 32 heads on 8 cached ones of 128: a tree of 25 over 1000 tokens 13.2 and 17.2, of 60 over 4000 22 and
-// 28, 4 trees of 25 over 2000 20 and 28, 256 queries with a window of 512 15 and 19; 8 trees of 60 over 1000, which have 960
-// tiles of 16 rows, 33 and 28).
+// (us for 16 and 64 rows, each cut as it is best, 32 heads on 8 cached ones of 128: a tree of 25 over 1000 tokens 13.1 and
+// 16.7, of 60 over 4000 24 and 30, 4 trees of 25 over 2000 20 and 28, 256 queries with a window of 512 16.3 and 21.5; 8 trees of
+// 60 over 1000, which have 960 tiles of 16 rows, 34 and 30).
 inline bool few_narrow_tiles(int cus, int64_t B, int64_t rows_each, int64_t Hkv) {
   return Hkv * B * ((rows_each + kRows - 1) / kRows) <= 2 * static_cast<int64_t>(cus);
 }
@@ -133,7 +137,7 @@ inline AttnShape attention_shape(int cus, int dtype, int64_t B, int64_t T, int64
   const bool narrow = s.rows == kRows;
   s.blocks = static_cast<int64_t>(cus) * (narrow ? narrow_blocks(dtype, D) : 2);
   // Windows are about equally long, so that nothing is gained by cutting them once every CU has two units (64 single tokens
-  // with windows of 4096, 8 cached heads of 128: 65 us whole, 70 split).
+  // with windows of 4096, 8 cached heads of 128: 59 us whole, 66 split).
   const Cut cut = narrow && mask == kWindow && units >= 2 * static_cast<int64_t>(cus) ? Cut::kWhole
                   : narrow ? narrow_cut(cus, dtype, D, units, max_tokens, s.blocks, mask) : wide_cut(units, max_tokens, s.blocks);
   s.tall = cut == Cut::kTall;

@@ -22,28 +22,30 @@ inline int64_t mxfp4_tiles(int64_t M, int64_t N, int bm, int bn) { return ((M + 
 
 // The kernel, tile and ranges of K with the least estimated time: rounds of tiles over the CUs, each its steps of 256
 // elements and a part for its outputs, and a part for the call; not less than the bytes take. Splitting adds a launch and
-// the partial sums' way to memory and back. us, each kernel where it was forced (* with K split, where that was the
-// better), the chosen one marked:
+// the partial sums' way to memory and back. us by replayed graphs, calls back to back on quantized normal values, each
+// kernel where it was forced (* with K split, where that was the better), the chosen one marked; where two are given, the
+// clock that the power allows decides:
 //   M x N x K             256 x 256   128 x 128   64 x 128
-//   8192 x 8192 x 8192    > 308          379         503
-//   4096 x 4096 x 7168    >  66           77         106
-//   2048 x 8192 x 2048    >  28.8         32.9        40.6
-//   2048 x 4096 x 7168       54        >  43          57
-//   1024 x 4096 x 7168       44.7      >  22.3        28.0
-//   3000 x 3000 x  512       18.9      >  14.7        16.0
-//   1993 x 5920 x  256       19.2      >  15.0        17.5
-//    512 x 4096 x 7168       43.4         19.3      > 15.9
-//    128 x 4096 x 7168       41.5         17.3 *    > 14.6 (split 15.3)
-//     65 x 4096 x 7168       44.7         15.2 *    > 14.0 *
-//    333 x 4104 x 2176       24.6         11.2      >  9.2
-//    300 x  300 x 8192       55.1         11.9 *    > 10.9 * (17.0 unsplit)
+//   8192 x 8192 x 8192    > 281-312      343         456
+//   4096 x 4096 x 7168    >  67           82         111
+//   2048 x 8192 x 2048    >  29.8         32.9        41.1
+//   2048 x 4096 x 7168       53        >  44          58
+//   1024 x 4096 x 7168       45        >  22.7        29.0
+//   3000 x 3000 x  512       18.7      >  14.7        16.0
+//   1993 x 5920 x  256       18.4      >  14.2        16.8
+//    512 x 4096 x 7168       43.9         19.8      > 16.9
+//    128 x 4096 x 7168       41.2         17.8 *    > 14.8
+//     65 x 4096 x 7168       41.6         15.8 *    > 14.2 *
+//    333 x 4104 x 2176       23.8         11.4      >  9.4
+//    300 x  300 x 8192       50.2         12.1 *    > 11.8 * (16.7 unsplit)
 // Up to 64 rows, without staging and with tiles of 64 x 128: B goes through the registers of every 16 rows, which is
 // the shorter way while there are few of them or few rounds.
-//   64 x  4096 x 7168   > 11.7   13.9 *      32 x  4096 x 7168   >  7.9   12.7 *
-//   64 x  8192 x 8192     24.1 > 18.5 *      32 x 14336 x 4096     14.0 > 11.3
-//   64 x 14336 x 4096     22.5 > 11.7        32 x 28672 x 8192     51.1 > 33.3
-//   64 x 28672 x 8192     81.9 > 33.8        16 x 28672 x 8192     37.5 > 31.7
-//   64 x  2048 x 4096   >  7.4   10.5 *      16 x  8192 x 8192   > 12.1   14.6 *
+//   64 x  4096 x 7168   > 11.6   13.8 *      32 x  4096 x 7168   >  8.0   12.7 *
+//   64 x  8192 x 8192     23.4 > 18.5        32 x 14336 x 4096     14.6 > 11.6
+//   64 x 14336 x 4096     21.6 > 12.0        32 x 28672 x 8192     50.8 > 31-34
+//   64 x 28672 x 8192     80.9 > 32-35       16 x 28672 x 8192     37.4 > 30-32
+//   64 x  2048 x 4096   >  7.4   10.7        16 x  8192 x 8192   > 11.9   14.5 *
+//                                            16 x 14336 x 4096     10.4 > 11.2
 inline Mxfp4Shape mxfp4_shape(int64_t M, int64_t N, int64_t K, int cus) {
   struct Model {
     Mxfp4Kind kind;
