@@ -57,3 +57,14 @@ def test_sums_past_the_range(M, N):
     want[:, N // 2] = 1.5 * 2.0 ** 126
     want[M // 2] *= -1
     assert torch.equal(y.float().cpu(), want)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+def test_a_scale_byte_of_255_is_nan(dtype):
+    """Every code of its 32 elements, zeros too, and no other."""
+    q = torch.arange(256, dtype=torch.uint8).repeat(8, 1)
+    s = torch.full((8, 16), 127, dtype=torch.uint8)
+    s[2, 5] = s[7, 15] = s[3] = 255
+    for scales in (s, s.view(torch.int32)):
+        got = fq().mxfp4_dequant(q.cuda(), scales.cuda(), DT[dtype]).cpu()
+        assert torch.equal(torch.isnan(got), (s == 255).repeat_interleave(32, 1))
